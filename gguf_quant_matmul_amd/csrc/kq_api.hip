@@ -474,4 +474,237 @@ int kq_gather_qmm_seg_bf16(int codec, const void* w, int64_t n_experts, int64_t 
                                             y, bf16_out(y_dtype), (hipStream_t)stream));
 }
 
+// ---- key/value cache in 4 bits ----
+namespace {
+
+constexpr int64_t kMaxSeqs = (int64_t)1 << 20;
+
+// codec, page, row size and kv heads of a cache; fills log2(page)
+int check_cache(const char* op, int codec, int64_t page, int64_t d, int64_t heads, int* shift) {
+  if (codec != KQ_Q4_0) return fail(KQ_ERR_CODEC, op, "codec id %d: the cache holds q4_0 blocks", codec);
+  if (page < 16 || page > 4096 || (page & (page - 1)))
+    return fail(KQ_ERR_SHAPE, op, "page=%lld is not a power of two in 16..4096", (long long)page);
+  if (d < 32 || d > 256 || d % 32)
+    return fail(KQ_ERR_SHAPE, op, "d=%lld is not a multiple of 32 in 32..256", (long long)d);
+  if (heads < 1 || heads > 4096) return fail(KQ_ERR_ARG, op, "kv_heads=%lld out of 1..4096", (long long)heads);
+  *shift = __builtin_ctzll((unsigned long long)page);
+  return KQ_OK;
+}
+
+// the two caches: page count and pointers
+int check_pages(const char* op, const void* kc, const void* vc, int64_t pages, int64_t page) {
+  if (pages < 1 || pages * page >= kMaxDim || pages >= kMaxDim)
+    return fail(KQ_ERR_ARG, op, "pages=%lld out of range", (long long)pages);
+  if (!kc || !vc) return fail(KQ_ERR_ARG, op, "null cache (k_cache=%p v_cache=%p)", kc, vc);
+  if (!aligned(kc, 16) || !aligned(vc, 16)) return fail(KQ_ERR_ALIGN, op, "caches must be 16-byte aligned");
+  return KQ_OK;
+}
+
+int elem_bytes(int dt) { return dt == KQ_F32 ? 4 : 2; }
+int elem_id(int dt) { return dt == KQ_F32 ? 0 : dt == KQ_F16 ? 1 : 2; }
+
+int check_any_dtype(const char* op, const char* what, int dt) {
+  if (dt != KQ_F32 && dt != KQ_F16 && dt != KQ_BF16)
+    return fail(KQ_ERR_ARG, op, "%s dtype %d is not KQ_F32, KQ_F16 or KQ_BF16", what, dt);
+  return KQ_OK;
+}
+
+int check_rows(const char* op, int64_t tokens, int64_t heads, int64_t d) {
+  if (tokens < 0 || tokens >= kMaxDim || tokens * heads * d >= (int64_t)1 << 34)
+    return fail(KQ_ERR_ARG, op, "tokens=%lld out of range", (long long)tokens);
+  return KQ_OK;
+}
+
+int check_attn_sizes(const char* op, int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d,
+                     int64_t max_new, int64_t max_kv) {
+  if (d < 32 || d > 256 || d % 32)
+    return fail(KQ_ERR_SHAPE, op, "d=%lld is not a multiple of 32 in 32..256", (long long)d);
+  if (kv_heads < 1 || kv_heads > 4096) return fail(KQ_ERR_ARG, op, "kv_heads=%lld out of 1..4096", (long long)kv_heads);
+  if (q_heads < 1 || q_heads > 4096 || q_heads % kv_heads)
+    return fail(KQ_ERR_SHAPE, op, "q_heads=%lld is not a multiple of kv_heads=%lld (at most 4096)", (long long)q_heads,
+                (long long)kv_heads);
+  if (tokens < 0 || tokens >= kMaxDim || tokens * q_heads >= (int64_t)1 << 25)
+    return fail(KQ_ERR_ARG, op, "tokens=%lld out of range (tokens * q_heads below 2^25)", (long long)tokens);
+  if (n_seqs < 0 || n_seqs > kMaxSeqs || n_seqs * kv_heads >= (int64_t)1 << 22)
+    return fail(KQ_ERR_ARG, op, "n_seqs=%lld out of range (n_seqs * kv_heads below 2^22)", (long long)n_seqs);
+  if (max_new < 1 || max_new >= kMaxDim) return fail(KQ_ERR_ARG, op, "max_new=%lld out of range", (long long)max_new);
+  if (max_kv < 1 || max_kv >= kMaxDim) return fail(KQ_ERR_ARG, op, "max_kv=%lld out of range", (long long)max_kv);
+  return KQ_OK;
+}
+
+}  // namespace
+
+int kq_kv_page_bytes(int codec, int64_t page, int64_t d, int64_t* page_bytes) {
+  const char* op = "kq_kv_page_bytes";
+  int shift;
+  const int st = check_cache(op, codec, page, d, 1, &shift);
+  if (st) return st;
+  if (!page_bytes) return fail(KQ_ERR_ARG, op, "null output");
+  *page_bytes = page * (d / 2 + d / 16);
+  return KQ_OK;
+}
+
+int kq_block_tables(const int32_t* ctx_lens, const int32_t* new_lens, int64_t n_seqs, int64_t page,
+                    const int32_t* free_pages, int64_t n_free, const int32_t* free_head, int32_t* table,
+                    int64_t width, int32_t* slots, int64_t tokens, int32_t* cu_new, int32_t* seq_lens,
+                    int32_t* free_head_out, uint32_t* status, void* stream) {
+  const char* op = "kq_block_tables";
+  int shift;
+  const int st = check_cache(op, KQ_Q4_0, page, 32, 1, &shift);
+  if (st) return st;
+  if (n_seqs < 0 || n_seqs > kMaxSeqs) return fail(KQ_ERR_ARG, op, "n_seqs=%lld out of range", (long long)n_seqs);
+  if (n_free < 0 || n_free >= kMaxDim) return fail(KQ_ERR_ARG, op, "n_free=%lld out of range", (long long)n_free);
+  if (width < 0 || width >= kMaxDim || n_seqs * width >= kMaxElems)
+    return fail(KQ_ERR_ARG, op, "width=%lld out of range", (long long)width);
+  if (tokens < 0 || tokens >= kMaxDim) return fail(KQ_ERR_ARG, op, "tokens=%lld out of range", (long long)tokens);
+  if (!free_head || !free_head_out || !cu_new) return fail(KQ_ERR_ARG, op, "null free_head, free_head_out or cu_new");
+  if (n_seqs > 0 && (!ctx_lens || !new_lens || !seq_lens || (width > 0 && !table)))
+    return fail(KQ_ERR_ARG, op, "null ctx_lens, new_lens, table or seq_lens");
+  if ((n_free > 0 && !free_pages) || (tokens > 0 && !slots)) return fail(KQ_ERR_ARG, op, "null free_pages or slots");
+  const void* in[] = {ctx_lens, new_lens, free_pages, free_head};
+  const int64_t in_n[] = {n_seqs, n_seqs, n_free, 1};
+  const void* out[] = {table, slots, cu_new, seq_lens, free_head_out, status};
+  const int64_t out_n[] = {n_seqs * width, tokens, n_seqs + 1, n_seqs, 1, 1};
+  for (int i = 0; i < 6; ++i) {
+    if (!out[i] || out_n[i] == 0) continue;
+    if (!aligned(out[i], 4)) return fail(KQ_ERR_ALIGN, op, "arrays must be 4-byte aligned");
+    for (int j = 0; j < 4; ++j)
+      if (in[j] && overlaps(in[j], 4 * in_n[j], out[i], 4 * out_n[i]))
+        return fail(KQ_ERR_ARG, op, "an output overlaps an input");
+    for (int j = 0; j < i; ++j)
+      if (out[j] && overlaps(out[j], 4 * out_n[j], out[i], 4 * out_n[i]))
+        return fail(KQ_ERR_ARG, op, "two outputs overlap");
+  }
+  for (const void* p : in)
+    if (p && !aligned(p, 4)) return fail(KQ_ERR_ALIGN, op, "arrays must be 4-byte aligned");
+  return hip_status(op, kq::launch_block_tables(ctx_lens, new_lens, n_seqs, shift, free_pages, n_free, free_head,
+                                                table, width, slots, tokens, cu_new, seq_lens, free_head_out, status,
+                                                (hipStream_t)stream));
+}
+
+int kq_kv_store(int codec, const void* k, const void* v, int x_dtype, int64_t tokens, int64_t kv_heads, int64_t d,
+                int64_t k_stride, int64_t v_stride, const int32_t* slots, void* k_cache, void* v_cache,
+                int64_t pages, int64_t page, void* stream) {
+  const char* op = "kq_kv_store";
+  int shift;
+  int st = check_cache(op, codec, page, d, kv_heads, &shift);
+  if (st) return st;
+  if ((st = check_any_dtype(op, "row", x_dtype))) return st;
+  if ((st = check_rows(op, tokens, kv_heads, d))) return st;
+  if (k_stride < kv_heads * d || v_stride < kv_heads * d || k_stride >= kMaxDim || v_stride >= kMaxDim)
+    return fail(KQ_ERR_SHAPE, op, "row strides k=%lld v=%lld out of range (kv_heads * d = %lld)", (long long)k_stride,
+                (long long)v_stride, (long long)(kv_heads * d));
+  if (k_stride % 8 || v_stride % 8)
+    return fail(KQ_ERR_ALIGN, op, "row strides k=%lld v=%lld are not multiples of 8", (long long)k_stride,
+                (long long)v_stride);
+  if ((st = check_pages(op, k_cache, v_cache, pages, page))) return st;
+  const int64_t cache = pages * kv_heads * page * (d / 2 + d / 16);
+  if (overlaps(k_cache, cache, v_cache, cache)) return fail(KQ_ERR_ARG, op, "k_cache and v_cache overlap");
+  if (tokens == 0) return KQ_OK;
+  if (!k || !v || !slots) return fail(KQ_ERR_ARG, op, "null pointer (k=%p v=%p slots=%p)", k, v, (const void*)slots);
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(KQ_ERR_ALIGN, op, "k=%p, v=%p are not 16-byte aligned", k, v);
+  if (!aligned(slots, 4)) return fail(KQ_ERR_ALIGN, op, "slots=%p is not 4-byte aligned", (const void*)slots);
+  return hip_status(op, kq::launch_kv_store(k, v, elem_id(x_dtype), tokens, kv_heads, d, k_stride, v_stride, slots,
+                                            (uint8_t*)k_cache, (uint8_t*)v_cache, pages, shift, (hipStream_t)stream));
+}
+
+int kq_kv_load(int codec, const void* k_cache, const void* v_cache, int64_t pages, int64_t page, int64_t kv_heads,
+               int64_t d, const int32_t* slots, int64_t tokens, void* k, void* v, int out_dtype, void* stream) {
+  const char* op = "kq_kv_load";
+  int shift;
+  int st = check_cache(op, codec, page, d, kv_heads, &shift);
+  if (st) return st;
+  if ((st = check_any_dtype(op, "output", out_dtype))) return st;
+  if ((st = check_rows(op, tokens, kv_heads, d))) return st;
+  if ((st = check_pages(op, k_cache, v_cache, pages, page))) return st;
+  if (tokens == 0) return KQ_OK;
+  if (!k || !v || !slots) return fail(KQ_ERR_ARG, op, "null pointer (k=%p v=%p slots=%p)", k, v, (const void*)slots);
+  if (!aligned(k, 16) || !aligned(v, 16)) return fail(KQ_ERR_ALIGN, op, "k=%p, v=%p are not 16-byte aligned", k, v);
+  if (!aligned(slots, 4)) return fail(KQ_ERR_ALIGN, op, "slots=%p is not 4-byte aligned", (const void*)slots);
+  const int64_t bytes = tokens * kv_heads * d * elem_bytes(out_dtype);
+  if (overlaps(k, bytes, v, bytes)) return fail(KQ_ERR_ARG, op, "k and v overlap");
+  return hip_status(op, kq::launch_kv_load((const uint8_t*)k_cache, (const uint8_t*)v_cache, pages, shift, kv_heads, d,
+                                           slots, tokens, k, v, elem_id(out_dtype), (hipStream_t)stream));
+}
+
+int kq_kv_attention_workspace(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d,
+                              int64_t max_new, int64_t max_kv, int64_t* bytes) {
+  const char* op = "kq_kv_attention_workspace";
+  const int st = check_attn_sizes(op, tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv);
+  if (st) return st;
+  if (!bytes) return fail(KQ_ERR_ARG, op, "null output");
+  *bytes = tokens == 0 || n_seqs == 0 ? 0 : kq::attn_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv).bytes;
+  return KQ_OK;
+}
+
+int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64_t q_heads, int64_t kv_heads,
+                    int64_t d, int64_t q_stride, const int32_t* cu_new, const int32_t* seq_lens, int64_t n_seqs,
+                    const int32_t* table, int64_t width, const void* k_cache, const void* v_cache, int64_t pages,
+                    int64_t page, float scale, int64_t window, int64_t max_new, int64_t max_kv, void* out,
+                    int out_dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  const char* op = "kq_kv_attention";
+  int shift;
+  int st = check_cache(op, codec, page, d, kv_heads, &shift);
+  if (st) return st;
+  if ((st = check_attn_sizes(op, tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv))) return st;
+  if (q_dtype != KQ_F16 && q_dtype != KQ_BF16)
+    return fail(KQ_ERR_ARG, op, "query dtype %d is not KQ_F16 or KQ_BF16", q_dtype);
+  if ((st = check_any_dtype(op, "output", out_dtype))) return st;
+  if (q_stride < q_heads * d || q_stride >= kMaxDim)
+    return fail(KQ_ERR_SHAPE, op, "row stride %lld out of range (q_heads * d = %lld)", (long long)q_stride,
+                (long long)(q_heads * d));
+  if (q_stride % 8) return fail(KQ_ERR_ALIGN, op, "row stride %lld is not a multiple of 8", (long long)q_stride);
+  if (width < 0 || width * page >= (int64_t)1 << 30 || width >= (int64_t)1 << 30)
+    return fail(KQ_ERR_ARG, op, "width=%lld out of range (width * page below 2^30)", (long long)width);
+  if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(KQ_ERR_ARG, op, "scale=%g is not finite", (double)scale);
+  if (window < 0) return fail(KQ_ERR_ARG, op, "window=%lld is negative", (long long)window);
+  if ((st = check_pages(op, k_cache, v_cache, pages, page))) return st;
+  if (tokens == 0 || n_seqs == 0) return KQ_OK;
+  if (!q || !out || !cu_new || !seq_lens || (width > 0 && !table))
+    return fail(KQ_ERR_ARG, op, "null pointer (q=%p out=%p cu_new=%p seq_lens=%p table=%p)", q, out,
+                (const void*)cu_new, (const void*)seq_lens, (const void*)table);
+  if (!aligned(q, 16) || !aligned(out, 16)) return fail(KQ_ERR_ALIGN, op, "q=%p, out=%p are not 16-byte aligned", q, out);
+  if (!aligned(cu_new, 4) || !aligned(seq_lens, 4) || !aligned(table, 4))
+    return fail(KQ_ERR_ALIGN, op, "cu_new, seq_lens and table must be 4-byte aligned");
+  const int64_t out_bytes = tokens * q_heads * d * elem_bytes(out_dtype);
+  if (overlaps(q, ((tokens - 1) * q_stride + q_heads * d) * 2, out, out_bytes))
+    return fail(KQ_ERR_ARG, op, "out overlaps q");
+  const kq::AttnPlan plan = kq::attn_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv);
+  if (plan.bytes > 0) {
+    if (!workspace || workspace_bytes < plan.bytes)
+      return fail(KQ_ERR_CAPACITY, op, "workspace of %lld bytes is below the %lld these sizes need",
+                  (long long)(workspace ? workspace_bytes : 0), (long long)plan.bytes);
+    if (!aligned(workspace, 16)) return fail(KQ_ERR_ALIGN, op, "workspace=%p is not 16-byte aligned", workspace);
+    if (overlaps(workspace, plan.bytes, out, out_bytes)) return fail(KQ_ERR_ARG, op, "workspace overlaps out");
+  }
+  kq::AttnArgs a;
+  a.q = q;
+  a.cu = cu_new;
+  a.lens = seq_lens;
+  a.table = table;
+  a.kc = (const uint8_t*)k_cache;
+  a.vc = (const uint8_t*)v_cache;
+  a.out = out;
+  a.part = (float*)workspace;
+  a.q_stride = q_stride;
+  a.width = width;
+  a.page_head_bytes = page * (d / 2 + d / 16);
+  a.tokens = (int)tokens;
+  a.n_seqs = (int)n_seqs;
+  a.hq = (int)q_heads;
+  a.hkv = (int)kv_heads;
+  a.group = (int)(q_heads / kv_heads);
+  a.d = (int)d;
+  a.pages = (int)pages;
+  a.page_shift = shift;
+  a.window = window < (int64_t)1 << 30 ? (int)window : 0;  // no request is that long
+  a.scale = scale;
+  a.q_bf16 = q_dtype == KQ_BF16;
+  a.out_type = elem_id(out_dtype);
+  a.splits = plan.splits;
+  a.chunk = plan.chunk;
+  a.one_tile = plan.one_tile;
+  return hip_status(op, kq::launch_kv_attention(a, (hipStream_t)stream));
+}
+
 }  // extern "C"

@@ -388,4 +388,44 @@ struct PieceWalk {
   }
 };
 
+hipError_t launch_block_tables(const int32_t* ctx, const int32_t* nw, int64_t n_seqs, int page_shift,
+                               const int32_t* free_pages, int64_t n_free, const int32_t* free_head, int32_t* table,
+                               int64_t width, int32_t* slots, int64_t tokens, int32_t* cu, int32_t* lens,
+                               int32_t* head_out, uint32_t* status, hipStream_t s);
+// element types of the cache row launchers: 0 float32, 1 float16, 2 bfloat16
+hipError_t launch_kv_store(const void* k, const void* v, int type, int64_t tokens, int64_t heads, int64_t d,
+                           int64_t k_stride, int64_t v_stride, const int32_t* slots, uint8_t* kc, uint8_t* vc,
+                           int64_t pages, int page_shift, hipStream_t s);
+hipError_t launch_kv_load(const uint8_t* kc, const uint8_t* vc, int64_t pages, int page_shift, int64_t heads,
+                          int64_t d, const int32_t* slots, int64_t tokens, void* k, void* v, int type, hipStream_t s);
+
+// One kq_kv_attention call: device pointers and sizes as the kernels take them.
+struct AttnArgs {
+  const void* q;
+  const int32_t* cu;
+  const int32_t* lens;
+  const int32_t* table;
+  const uint8_t* kc;
+  const uint8_t* vc;
+  void* out;
+  float* part;     // workspace: partial sums, then (maximum, sum) pairs, then split counts
+  int64_t q_stride, width, page_head_bytes;
+  int tokens, n_seqs, hq, hkv, group, d;
+  int pages, page_shift;
+  int window;      // 0: none
+  float scale;
+  int q_bf16, out_type;
+  int splits;      // most workgroups that share one row's keys
+  int chunk;       // keys a workgroup takes before another one is worth it
+  int one_tile;    // a request's rows fit one 16-row tile: tile index = request
+};
+// How a call's work is split, from its host-known sizes alone.
+struct AttnPlan {
+  int splits, chunk, one_tile;
+  int64_t bytes;   // workspace
+};
+AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
+                   int64_t max_kv);
+hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t s);
+
 }  // namespace kq

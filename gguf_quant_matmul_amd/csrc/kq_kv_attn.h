@@ -1,0 +1,203 @@
+// Pieces shared by the attention kernels over the 4-bit cache
+// (kq_kv_attention): a request's rows and the keys they see, page lookups,
+// and the unpacking of 4-bit keys and values into matrix operands.
+//
+// The rows of a (request, kv head) are its new tokens times the group of
+// query heads that share the kv head: row r is token r / group, query head
+// kv_head * group + r % group.
+#pragma once
+
+#include "kq_internal.h"
+
+namespace kq {
+
+constexpr float NEG_INF = -__builtin_inff();
+
+// A request as the kernels see it: device data clamped to what is in bounds.
+struct Seq {
+  int row0, n;  // first token row, new tokens
+  int len;      // keys
+};
+__device__ __forceinline__ Seq load_seq(const AttnArgs& a, int s) {
+  int b = a.cu[s], e = a.cu[s + 1];
+  b = b < 0 ? 0 : b > a.tokens ? a.tokens : b;
+  e = e < b ? b : e > a.tokens ? a.tokens : e;
+  const int64_t cap = a.width << a.page_shift;
+  int64_t len = a.lens[s];
+  len = len < 0 ? 0 : len > cap ? cap : len;
+  return Seq{b, e - b, (int)len};
+}
+
+// Keys that rows r0 .. r1 of a request see: lo (64-aligned) .. end - 1.
+struct Keys {
+  int lo, end;
+};
+__device__ __forceinline__ Keys key_range(const AttnArgs& a, const Seq& q, int r0, int r1) {
+  const int p0 = q.len - q.n + r0 / a.group, p1 = q.len - q.n + r1 / a.group;  // positions
+  Keys k;
+  k.end = p1 + 1 > 0 ? p1 + 1 : 0;
+  const int64_t lo = a.window > 0 ? (int64_t)p0 - a.window + 1 : 0;
+  k.lo = (lo > 0 ? (int)lo : 0) & ~63;
+  return k;
+}
+// Workgroups that share those keys.
+__device__ __forceinline__ int split_count(const AttnArgs& a, const Keys& k) {
+  const int n = k.end - k.lo, s = n > 0 ? (int)(((int64_t)n + a.chunk - 1) / a.chunk) : 0;
+  return s < a.splits ? s : a.splits;
+}
+
+// Request and tile index inside it of tile `tile`, the tiles of all requests
+// numbered one after the other (`rows` rows to a tile); false past the last.
+// Every wave scans the requests 64 at a time.
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, int rows, int& seq, int& sub) {
+  const int lane = threadIdx.x & 63;
+  int64_t before = 0;
+  for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
+    const int s = s0 + lane;
+    int64_t t = 0;
+    if (s < a.n_seqs) t = ((int64_t)load_seq(a, s).n * a.group + rows - 1) / rows;
+    int64_t incl = t;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int64_t u = __shfl_up(incl, o, 64);
+      if (lane >= o) incl += u;
+    }
+    const uint64_t hit = __ballot(before + incl > tile);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      seq = s0 + l;
+      sub = (int)(tile - before - (__shfl(incl, l, 64) - __shfl(t, l, 64)));
+      return true;
+    }
+    before += __shfl(incl, 63, 64);
+  }
+  return false;
+}
+
+// N consecutive dwords from a 4-byte aligned address (16- or 8-byte loads
+// where N allows them).
+template <int N>
+__device__ __forceinline__ void load_dwords(const uint8_t* p, uint32_t* r) {
+  constexpr int Q = N / 4, H = (N % 4) / 2;
+  typedef uint32_t u2 __attribute__((ext_vector_type(2), aligned(4)));
+#pragma unroll
+  for (int i = 0; i < Q; ++i) {
+    const u32x4 v = ld_16B_a4(p + 16 * i);
+    r[4 * i] = v.x; r[4 * i + 1] = v.y; r[4 * i + 2] = v.z; r[4 * i + 3] = v.w;
+  }
+  if constexpr (H) {
+    const u2 v = *(const u2*)(p + 16 * Q);
+    r[4 * Q] = v.x; r[4 * Q + 1] = v.y;
+  }
+  if constexpr (N % 2) r[N - 1] = ld_u32(p + 4 * (N - 1));
+}
+
+// Eight codes (nibbles of w) as float16 pairs (n0, n4) (n1, n5) (n2, n6)
+// (n3, n7), each c - 8: a nibble or-ed into the low mantissa bits of 1024 is
+// 1024 + c, one or-ed four bits higher 1024 + 16 c; both come out exactly.
+struct H2x4 {
+  half2_t v[4];
+};
+__device__ __forceinline__ H2x4 unpack8(uint32_t w) {
+  constexpr uint32_t M = 0x64006400u;
+  const uint32_t u = w >> 8;
+  const half2_t k0 = half2_t{(half_t)1032.f, (half_t)1032.f}, k1 = half2_t{(half_t)-72.f, (half_t)-72.f},
+                s = half2_t{(half_t)0.0625f, (half_t)0.0625f};
+  H2x4 r;
+  r.v[0] = as_h2((w & 0x000F000Fu) | M) - k0;
+  r.v[1] = __builtin_elementwise_fma(as_h2((w & 0x00F000F0u) | M), s, k1);
+  r.v[2] = as_h2((u & 0x000F000Fu) | M) - k0;
+  r.v[3] = __builtin_elementwise_fma(as_h2((u & 0x00F000F0u) | M), s, k1);
+  return r;
+}
+__device__ __forceinline__ half8_t operand(half2_t a, half2_t b, half2_t c, half2_t d) {
+  return half8_t{a.x, a.y, b.x, b.y, c.x, c.y, d.x, d.y};
+}
+
+// Eight values of a query row in unpack8's order (0 4 1 5 2 6 3 7).
+__device__ __forceinline__ half8_t query_order(half8_t v) {
+  return __builtin_shufflevector(v, v, 0, 4, 1, 5, 2, 6, 3, 7);
+}
+
+// Maximum or sum over the four lane groups that hold one query's keys
+// (lanes l, l ^ 16, l ^ 32, l ^ 48).
+__device__ __forceinline__ float groups_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16, 64));
+  return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float groups_sum(float v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+// Query operands of one row for NB = d / 32 matrix steps: lane group g of
+// step s holds values g * d / 4 + 8 s .. + 7.  bfloat16 values are scaled by
+// a power of two that brings the row's largest near 2^14, which float16
+// holds exactly down to 2^-28 of the largest; `factor` takes that power of two
+// back out of the products, times scale * log2(e).  A negative scale is put
+// into the queries' signs, so that factor > 0 and the largest product has the
+// largest weight.
+template <int NB>
+__device__ __forceinline__ void load_query(const AttnArgs& a, const void* row, bool live, int g, half8_t (&q)[NB],
+                                           float& factor) {
+  const float log2e = 1.4426950408889634f;
+  const bool neg = a.scale < 0.f;
+  factor = fabsf(a.scale) * log2e;
+  if (a.q_bf16) {
+    typedef __bf16 b8 __attribute__((ext_vector_type(8)));
+    float v[NB][8], amax = 0.f;
+#pragma unroll
+    for (int s = 0; s < NB; ++s) {
+      const b8 r = live ? *(const b8*)((const __bf16*)row + g * (8 * NB) + 8 * s) : b8{};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v[s][i] = (float)r[i];
+        amax = fmaxf(amax, fabsf(v[s][i]));
+      }
+    }
+    amax = groups_max(amax);
+    // NaN and infinities keep their places; a row of zeros keeps its size
+    int e = amax > 0.f && amax < __builtin_inff() ? (int)((__builtin_bit_cast(uint32_t, amax) >> 23) & 255u) - 127 : 14;
+    e = e < -100 ? -100 : e;
+    const float up = __builtin_bit_cast(float, (uint32_t)(127 + 14 - e) << 23);
+    factor *= __builtin_bit_cast(float, (uint32_t)(127 - 14 + e) << 23);
+#pragma unroll
+    for (int s = 0; s < NB; ++s) {
+      half8_t h;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) h[i] = (half_t)(neg ? -v[s][i] * up : v[s][i] * up);
+      q[s] = query_order(h);
+    }
+  } else {
+#pragma unroll
+    for (int s = 0; s < NB; ++s) {
+      half8_t h = live ? *(const half8_t*)((const half_t*)row + g * (8 * NB) + 8 * s) : half8_t{};
+      if (neg) h = -h;
+      q[s] = query_order(h);
+    }
+  }
+  factor = fmaxf(factor, 1.17549435e-38f);  // a zero factor would turn masked -inf into NaN
+}
+
+// where the workspace holds the split counts, pairs and partial sums
+__host__ __device__ __forceinline__ int64_t part_rows(int64_t tokens, int64_t hq, int64_t splits) { return tokens * hq * splits; }
+
+template <int OUT>
+__device__ __forceinline__ void store4(void* out, int64_t i, float4_t v) {
+  if constexpr (OUT == 0) {
+    *(float4_t*)((float*)out + i) = v;
+  } else if constexpr (OUT == 1) {
+    typedef half_t h4 __attribute__((ext_vector_type(4)));
+    *(h4*)((half_t*)out + i) = h4{(half_t)v.x, (half_t)v.y, (half_t)v.z, (half_t)v.w};
+  } else {
+    typedef __bf16 b4 __attribute__((ext_vector_type(4)));
+    *(b4*)((__bf16*)out + i) = b4{(__bf16)v.x, (__bf16)v.y, (__bf16)v.z, (__bf16)v.w};
+  }
+}
+__device__ __forceinline__ void store4(void* out, int type, int64_t i, float4_t v) {
+  if (type == 0) store4<0>(out, i, v);
+  else if (type == 1) store4<1>(out, i, v);
+  else store4<2>(out, i, v);
+}
+
+}  // namespace kq

@@ -1,0 +1,342 @@
+// kq_kv_attention: attention over key/value rows held in 4 bits.
+//
+//   out = sum_j softmax_j(scale q . k_j) v_j,   k_j, v_j = D (c - 8)
+//
+// One pass over the keys with a running maximum and sum.  A workgroup takes
+// one 16-row tile of a (request, kv head); its four waves take 64-key steps in
+// turn, each with sums of its own, merged through LDS at the end.  Both
+// products run on v_mfma_f32_16x16x32_f16, transposed so that nothing moves
+// between lanes in between:
+//   S^T [16 keys x 16 rows] = K [16 x d] Q^T; lane l holds row l % 16, keys
+//     4 (l / 16) .. + 3 of each of a step's four 16-key groups.
+//   O^T [16 d x 16 rows] += V^T [16 d x 32 keys] P^T; its operand wants for
+//     lane l eight keys of row l % 16, and which key stands in which place is
+//     free as long as V^T agrees, so the places are given to the very keys
+//     whose probabilities the lane holds.
+// K operands: lane l reads quarter l / 16 of key l % 16's codes, contiguous in
+// memory; the matrix steps then run over values in that order, and so do the
+// queries.  V operands need eight keys of one value per lane: codes go through
+// LDS and come back through the 4-bit transposing read (ds_read_b64_tr_b4: 16
+// rows of 16 nibbles per 16 lanes, the row addresses free), which hands lane l
+// value l % 16 of 16 keys.  Codes become float16 by or-ing them into 1024's
+// mantissa, times the block's scale.
+#include "kq_kv_attn.h"
+
+namespace kq {
+namespace {
+
+constexpr int WAVES = 4;
+constexpr int STEP = 64;  // keys of one step
+
+// LDS of one wave: 64 rows of codes and their scales.  Row strides are odd
+// multiples of 16 bytes, which puts a lane group's 16 rows on distinct banks.
+template <int NB>
+struct Stage {
+  static constexpr int ROW = 16 * (NB | 1);
+  static constexpr int BYTES = STEP * ROW + STEP * NB * 2;
+};
+// LDS to hand one wave's sums to another: O^T [d][16], then maximum and sum
+template <int NB>
+constexpr int merge_bytes() { return 16 * 32 * NB * 4 + 2 * 16 * 4; }
+template <int NB>
+constexpr int lds_bytes() {
+  constexpr int s = WAVES * Stage<NB>::BYTES, m = 2 * merge_bytes<NB>();
+  return s > m ? s : m;
+}
+
+template <int NB>
+__global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
+  constexpr int D = 32 * NB;
+  constexpr int DT = D / 16;  // 16-value tiles of O^T
+  __shared__ __attribute__((aligned(16))) uint8_t lds[lds_bytes<NB>()];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
+  const int h = blockIdx.x % a.hkv, tile = blockIdx.x / a.hkv, split = blockIdx.y;
+
+  int s = tile, sub = 0;
+  if (!a.one_tile && !find_tile(a, tile, 16, s, sub)) return;
+  const Seq sq = load_seq(a, s);
+  const int rows = sq.n * a.group;
+  // with one tile to a request, a request that has more walks its own
+  for (; sub * 16 < rows; ++sub) {
+    const int r0 = sub * 16, r1 = r0 + 15 < rows ? r0 + 15 : rows - 1;
+    const Keys keys = key_range(a, sq, r0, r1);
+    const int n_split = split_count(a, keys);
+    const int row = r0 + col;
+    const bool live = row < rows;
+    const int tok = sq.row0 + row / a.group, head = h * a.group + row % a.group;
+    const int64_t orow = (int64_t)tok * a.hq + head;
+    // positions of this lane's row, of the tile's first and last
+    const int p = live ? sq.len - sq.n + row / a.group : -1;
+    const int p0 = sq.len - sq.n + r0 / a.group, p1 = sq.len - sq.n + r1 / a.group;
+
+    int32_t* counts = (int32_t*)(a.part + part_rows(a.tokens, a.hq, a.splits) * (D + 2));
+    if (a.splits > 1 && split == 0 && threadIdx.x < 16 && live) counts[orow] = n_split > 1 ? n_split : 0;
+    if (n_split == 0 && split == 0) {
+      for (int t = wave; t < DT; t += WAVES)
+        if (live) store4(a.out, a.out_type, orow * D + 16 * t + 4 * g, float4_t{0, 0, 0, 0});
+    }
+    if (split < n_split) {
+      const int steps = (keys.end - keys.lo + STEP - 1) / STEP;
+      const int st0 = (int)((int64_t)steps * split / n_split), st1 = (int)((int64_t)steps * (split + 1) / n_split);
+
+      half8_t q[NB];
+      float factor;
+      load_query<NB>(a, (const uint16_t*)a.q + (int64_t)tok * a.q_stride + (int64_t)head * D, live, g, q, factor);
+
+      float4_t o[DT];
+#pragma unroll
+      for (int t = 0; t < DT; ++t) o[t] = float4_t{0, 0, 0, 0};
+      float m = NEG_INF, l = 0.f;
+
+      uint8_t* codes = lds + wave * Stage<NB>::BYTES;
+      uint16_t* scales = (uint16_t*)(codes + STEP * Stage<NB>::ROW);
+      const int64_t row_scales = (int64_t)(D / 2) << a.page_shift;  // scales behind a page's codes
+      const int page_mask = (1 << a.page_shift) - 1;
+      const int32_t* pages = a.table + (int64_t)s * a.width;
+
+      for (int st = st0 + wave; st < st1; st += WAVES) {
+        const int base = keys.lo + st * STEP;
+        // the step's four 16-key groups: page, offset; a group past the end or
+        // without a page reads page 0 and is left out
+        int64_t at[4];  // byte offset of the (page, head)
+        int off[4];
+        bool ok[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = base + 16 * i;
+          const int id = k < keys.end ? pages[k >> a.page_shift] : -1;
+          ok[i] = id >= 0 && id < a.pages;
+          at[i] = ((int64_t)(ok[i] ? id : 0) * a.hkv + h) * a.page_head_bytes;
+          off[i] = k & page_mask;
+        }
+        // V into LDS: 16-byte pieces of codes, the row of key 16 i + 4 c + j at 16 c + 4 i + j, so that
+        // lane group c's keys lie together; scales in the order of the operands
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int piece = i * 64 + lane, key = piece / NB, b = piece % NB, kg = key >> 4;
+          const int64_t pa = kg == 0 ? at[0] : kg == 1 ? at[1] : kg == 2 ? at[2] : at[3];
+          const int po = (kg == 0 ? off[0] : kg == 1 ? off[1] : kg == 2 ? off[2] : off[3]) + (key & 15);
+          const u32x4 w = ld_16B(a.vc + pa + (int64_t)po * (D / 2) + 16 * b);
+          const int lr = ((key >> 2) & 3) * 16 + kg * 4 + (key & 3);
+          *(u32x4*)(codes + lr * Stage<NB>::ROW + 16 * b) = w;
+        }
+        {
+          const int kg = lane >> 4;
+          const int64_t pa = kg == 0 ? at[0] : kg == 1 ? at[1] : kg == 2 ? at[2] : at[3];
+          const int po = (kg == 0 ? off[0] : kg == 1 ? off[1] : kg == 2 ? off[2] : off[3]) + (lane & 15);
+          const bool good = (kg == 0 ? ok[0] : kg == 1 ? ok[1] : kg == 2 ? ok[2] : ok[3]) && base + lane < keys.end;
+          const uint8_t* sp = a.vc + pa + row_scales + (int64_t)po * (D / 16);
+          const int pos = ((lane >> 2) & 3) * 16 + (kg >> 1) * 8 + (lane & 3) * 2 + (kg & 1);
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            // bytes behind the last key are anything, NaN included: their values enter as 0 * code
+            const uint32_t sc = ld_u16(sp + 2 * b);
+            scales[b * 64 + pos] = good ? (uint16_t)sc : (uint16_t)0;
+          }
+        }
+        // S^T
+        float4_t sc[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          uint32_t w[NB];
+          const uint8_t* kp = a.kc + at[i];
+          load_dwords<NB>(kp + (int64_t)(off[i] + col) * (D / 2) + g * (D / 8), w);
+          const uint8_t* sp = kp + row_scales + (int64_t)(off[i] + col) * (D / 16);
+          sc[i] = float4_t{0, 0, 0, 0};
+          half2_t ks;
+#pragma unroll
+          for (int j = 0; j < NB; ++j) {
+            // dword j of quarter g lies in block (g NB + j) / 4
+            if (j == 0 || (NB & (NB - 1)) != 0 || j % 4 == 0) {
+              const half_t v = __builtin_bit_cast(half_t, (uint16_t)ld_u16(sp + 2 * ((g * NB + j) >> 2)));
+              ks = half2_t{v, v};
+            }
+            const H2x4 u = unpack8(w[j]);
+            sc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                operand(u.v[0] * ks, u.v[1] * ks, u.v[2] * ks, u.v[3] * ks), q[j], sc[i], 0, 0, 0);
+          }
+        }
+        const bool all_ok = ok[0] && ok[1] && ok[2] && ok[3];
+        if (base + STEP - 1 > p0 || (a.window > 0 && base <= p1 - a.window) || !all_ok) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int k = base + 16 * i + 4 * g + j;
+              const bool see = ok[i] && k <= p && (a.window <= 0 || k > p - a.window);
+              sc[i][j] = see ? sc[i][j] : NEG_INF;
+            }
+        }
+        // running maximum and sum
+        float mx = sc[0][0];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[i >> 2][i & 3]);
+        mx = fmaxf(groups_max(mx), m);
+        const float ref = mx == NEG_INF ? 0.f : mx;
+        const float corr = __builtin_amdgcn_exp2f((m - ref) * factor);
+        m = mx;
+        l *= corr;
+#pragma unroll
+        for (int t = 0; t < DT; ++t) o[t] *= corr;
+        const float bias = -ref * factor;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            sc[i][j] = __builtin_amdgcn_exp2f(fmaf(sc[i][j], factor, bias));
+            l += sc[i][j];
+          }
+        // P^T operands: places (2 s, 2 s + 1) hold keys s of groups 2 m and 2 m + 1
+        half8_t pt[2];
+#pragma unroll
+        for (int mm = 0; mm < 2; ++mm)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            pt[mm][2 * j] = (half_t)sc[2 * mm][j];
+            pt[mm][2 * j + 1] = (half_t)sc[2 * mm + 1][j];
+          }
+        // O^T += V^T P^T
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          half2_t vs[8];
+          *(u32x4*)&vs[0] = *(const u32x4*)(scales + b * 64 + g * 16);
+          *(u32x4*)&vs[4] = *(const u32x4*)(scales + b * 64 + g * 16 + 8);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            typedef int v2i __attribute__((ext_vector_type(2)));
+            typedef v2i __attribute__((address_space(3))) lds_v2i;
+            const v2i w = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+                (lds_v2i*)(codes + (g * 16 + col) * Stage<NB>::ROW + 16 * b + 8 * t));
+#pragma unroll
+            for (int mm = 0; mm < 2; ++mm) {
+              const H2x4 u = unpack8((uint32_t)w[mm]);
+              o[2 * b + t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                  operand(u.v[0] * vs[4 * mm], u.v[1] * vs[4 * mm + 1], u.v[2] * vs[4 * mm + 2],
+                          u.v[3] * vs[4 * mm + 3]),
+                  pt[mm], o[2 * b + t], 0, 0, 0);
+            }
+          }
+        }
+      }
+      l = groups_sum(l);
+
+      // merge: waves 2, 3 into 0, 1, then 1 into 0
+#pragma unroll
+      for (int half = WAVES / 2; half > 0; half >>= 1) {
+        __syncthreads();
+        float* buf = (float*)(lds + (wave & (half - 1)) * merge_bytes<NB>());
+        if (wave >= half && wave < 2 * half) {
+#pragma unroll
+          for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) buf[(16 * t + 4 * g + j) * 16 + col] = o[t][j];
+          if (g == 0) { buf[D * 16 + col] = m; buf[D * 16 + 16 + col] = l; }
+        }
+        __syncthreads();
+        if (wave < half) {
+          const float m2 = buf[D * 16 + col], l2 = buf[D * 16 + 16 + col];
+          const float mx = fmaxf(m, m2), ref = mx == NEG_INF ? 0.f : mx;
+          const float c1 = __builtin_amdgcn_exp2f((m - ref) * factor), c2 = __builtin_amdgcn_exp2f((m2 - ref) * factor);
+          m = mx;
+          l = l * c1 + l2 * c2;
+#pragma unroll
+          for (int t = 0; t < DT; ++t)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[t][j] = o[t][j] * c1 + buf[(16 * t + 4 * g + j) * 16 + col] * c2;
+        }
+      }
+      if (wave == 0 && live) {
+        if (n_split == 1) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;  // no key seen: zeros
+#pragma unroll
+          for (int t = 0; t < DT; ++t) store4(a.out, a.out_type, orow * D + 16 * t + 4 * g, o[t] * inv);
+        } else {
+          const int64_t pr = (int64_t)split * a.tokens * a.hq + orow;
+#pragma unroll
+          for (int t = 0; t < DT; ++t) store4<0>(a.part, pr * D + 16 * t + 4 * g, o[t]);
+          if (g == 0) {
+            float* ml = a.part + part_rows(a.tokens, a.hq, a.splits) * D + 2 * pr;
+            ml[0] = m == NEG_INF ? NEG_INF : m * factor;  // in powers of two, for the merge
+            ml[1] = l;
+          }
+        }
+      }
+      __syncthreads();  // the next tile reuses the LDS
+    }
+    if (!a.one_tile) break;
+  }
+}
+
+// Joins the partial sums of split rows: a thread per 4 values of a row.
+__global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
+  const int per = a.d / 4;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / per;
+  const int c = (int)(i - row * per) * 4;
+  const int64_t n_rows = (int64_t)a.tokens * a.hq;
+  if (row >= n_rows) return;
+  int b = a.cu[0], e = a.cu[a.n_seqs];
+  b = b < 0 ? 0 : b;
+  const int tok = (int)(row / a.hq);
+  if (tok < b || tok >= e) return;  // no request's row: its count was not written
+  const int64_t pr = part_rows(a.tokens, a.hq, a.splits);
+  const int32_t* counts = (const int32_t*)(a.part + pr * (a.d + 2));
+  int n = counts[row];
+  n = n > a.splits ? a.splits : n;
+  if (n <= 1) return;  // written by the workgroup itself
+  const float* ml = a.part + pr * a.d;
+  float m = NEG_INF;
+  for (int s = 0; s < n; ++s) m = fmaxf(m, ml[2 * (s * n_rows + row)]);
+  const float ref = m == NEG_INF ? 0.f : m;
+  float4_t o = {0, 0, 0, 0};
+  float l = 0.f;
+  for (int s = 0; s < n; ++s) {
+    const int64_t r = s * n_rows + row;
+    const float w = __builtin_amdgcn_exp2f(ml[2 * r] - ref);
+    l += w * ml[2 * r + 1];
+    o += w * *(const float4_t*)(a.part + r * a.d + c);
+  }
+  store4(a.out, a.out_type, row * a.d + c, o * (l == 0.f ? 0.f : 1.f / l));
+}
+
+}  // namespace
+
+AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
+                   int64_t max_kv) {
+  AttnPlan p;
+  const int64_t group = q_heads / kv_heads;
+  p.one_tile = max_new * group <= 16;
+  const int64_t tiles = p.one_tile ? n_seqs : (tokens * group) / 16 + n_seqs;
+  // enough workgroups for three on each of 256 CUs, none with fewer than 256
+  // keys; never more than 4096 keys to one, whose length differs from others'
+  const int64_t want = (768 + tiles * kv_heads - 1) / (tiles * kv_heads);
+  int64_t chunk = (max_kv + want - 1) / want;
+  chunk = chunk < 256 ? 256 : chunk > 4096 ? 4096 : chunk;
+  p.chunk = (int)((chunk + 63) / 64 * 64);
+  p.splits = (int)((max_kv + p.chunk - 1) / p.chunk);
+  p.splits = p.splits < 1 ? 1 : p.splits > 256 ? 256 : p.splits;
+  p.bytes = p.splits > 1 ? part_rows(tokens, q_heads, p.splits) * (d + 2) * 4 + tokens * q_heads * 4 : 0;
+  return p;
+}
+
+hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t s) {
+  const int64_t tiles = a.one_tile ? a.n_seqs : ((int64_t)a.tokens * a.group) / 16 + a.n_seqs;
+  const dim3 grid((unsigned)(tiles * a.hkv), (unsigned)a.splits), block(64 * WAVES);
+  const auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, s, a); };
+  switch (a.d / 32) {
+    case 1: go(attn_split_kernel<1>); break;
+    case 2: go(attn_split_kernel<2>); break;
+    case 3: go(attn_split_kernel<3>); break;
+    case 4: go(attn_split_kernel<4>); break;
+    case 5: go(attn_split_kernel<5>); break;
+    case 6: go(attn_split_kernel<6>); break;
+    case 7: go(attn_split_kernel<7>); break;
+    default: go(attn_split_kernel<8>); break;
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || a.splits == 1) return e;
+  const int64_t n = (int64_t)a.tokens * a.hq * (a.d / 4);
+  hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
+  return hipGetLastError();
+}
+
+}  // namespace kq

@@ -56,6 +56,16 @@ _SIGS = {
     "kq_qmm_bf16": (c_int, [c_int, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp, c_int, c_vp]),
     "kq_gather_qmm_seg_bf16": (c_int, [c_int, c_vp, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_int,
                                        c_vp]),
+    "kq_kv_page_bytes": (c_int, [c_int, c_i64, c_i64, _P(c_i64)]),
+    "kq_block_tables": (c_int, [c_vp, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp,
+                                c_vp, c_vp]),
+    "kq_kv_store": (c_int, [c_int, c_vp, c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_vp, c_i64, c_i64,
+                            c_vp]),
+    "kq_kv_load": (c_int, [c_int, c_vp, c_vp, c_i64, c_i64, c_i64, c_i64, c_vp, c_i64, c_vp, c_vp, c_int, c_vp]),
+    "kq_kv_attention_workspace": (c_int, [c_i64, c_i64, c_i64, c_i64, c_i64, c_i64, c_i64, _P(c_i64)]),
+    "kq_kv_attention": (c_int, [c_int, c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64,
+                                c_vp, c_vp, c_i64, c_i64, ctypes.c_float, c_i64, c_i64, c_i64, c_vp, c_int, c_vp, c_i64,
+                                c_vp]),
 }
 
 #: every symbol the header declares
@@ -271,6 +281,163 @@ def kq_stream_read(src, out, nbytes: int | None = None, stream=None) -> None:
 
 
 # ---------------------------------------------------------------------------
+# key/value cache in 4 bits
+# ---------------------------------------------------------------------------
+
+def _ints(op: str, n: int | None, **arrays) -> None:
+    """Index arrays are contiguous 32-bit integers, of n entries where n is given."""
+    for name, t in arrays.items():
+        if t is None:
+            continue
+        if t.dtype not in (torch.int32, torch.uint32):
+            raise TypeError(f"{op}: {name} must be int32, got {t.dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{op}: {name} must be contiguous")
+        if n is not None and t.numel() != n:
+            raise ValueError(f"{op}: {name} has {t.numel()} entries, expected {n}")
+
+
+def _same_device(op: str, first, *rest) -> None:
+    for t in rest:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{op}: tensors on {first.device} and {t.device}")
+
+
+def _run_on(t, stream, call) -> None:
+    """call(stream) with t's device current: the given stream, else t's device's current one."""
+    if not t.is_cuda or t.device.index == torch.cuda.current_device():
+        _check(call(_stream(stream)))
+        return
+    with torch.cuda.device(t.device):
+        _check(call(_stream(stream)))
+
+
+def _cache(op: str, codec, k_cache, v_cache, page: int, d: int) -> tuple[int, int]:
+    """(pages, kv_heads) of two caches uint8 [pages, kv_heads, page_bytes]."""
+    pb = kq_kv_page_bytes(codec, page, d)
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
+        if t.dtype != torch.uint8 or t.dim() != 3 or not t.is_contiguous() or t.shape != k_cache.shape:
+            raise ValueError(f"{op}: {name} must be a contiguous uint8 [pages, kv_heads, {pb}]")
+    if k_cache.shape[2] != pb:
+        raise ValueError(f"{op}: pages hold {k_cache.shape[2]} bytes a head, {pb} expected for page={page}, d={d}")
+    return k_cache.shape[0], k_cache.shape[1]
+
+
+def _row_stride(op: str, name: str, x) -> int:
+    """Elements between rows of x [tokens, heads, d], whose rows are dense."""
+    if x.dim() != 3:
+        raise ValueError(f"{op}: {name} must be [tokens, heads, d]")
+    dense = x.shape[1] * x.shape[2]
+    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2])):
+        raise ValueError(f"{op}: the rows of {name} must be dense")
+    return x.stride(0) if x.shape[0] > 1 else dense
+
+
+def kq_kv_page_bytes(codec, page: int, d: int) -> int:
+    """Bytes of one (page, kv head) of a 4-bit key or value cache."""
+    out = c_i64()
+    _check(_lib.kq_kv_page_bytes(_codec(codec), page, d, ctypes.byref(out)))
+    return out.value
+
+
+def kq_block_tables(ctx_lens, new_lens, free_pages, free_head, page: int, table, slots, cu_new, seq_lens,
+                    free_head_out, status=None, stream=None) -> None:
+    """Pages and slots of a step's new tokens.  ctx_lens, new_lens, seq_lens int32 [n]; free_pages int32 [n_free] from
+    free_head int32 [1]; table int32 [n, width]; slots int32 [tokens]; cu_new int32 [n + 1]; free_head_out, status [1]."""
+    op, n = "kq_block_tables", ctx_lens.numel()
+    if table.dim() != 2 or table.shape[0] != n:
+        raise ValueError(f"{op}: table must be [{n}, width]")
+    _ints(op, n, ctx_lens=ctx_lens, new_lens=new_lens, seq_lens=seq_lens)
+    _ints(op, 1, free_head=free_head, free_head_out=free_head_out, status=status)
+    _ints(op, n + 1, cu_new=cu_new)
+    _ints(op, None, free_pages=free_pages, table=table, slots=slots)
+    _same_device(op, ctx_lens, new_lens, free_pages, free_head, table, slots, cu_new, seq_lens, free_head_out, status)
+    _run_on(ctx_lens, stream, lambda st: _lib.kq_block_tables(
+        _ptr(ctx_lens), _ptr(new_lens), n, page, _ptr(free_pages), free_pages.numel(), _ptr(free_head), _ptr(table),
+        table.shape[1], _ptr(slots), slots.numel(), _ptr(cu_new), _ptr(seq_lens), _ptr(free_head_out), _ptr(status), st))
+
+
+def kq_kv_store(codec, k, v, slots, k_cache, v_cache, page: int, stream=None) -> None:
+    """k, v float32/float16/bfloat16 [tokens, kv_heads, d] (dense rows, any row stride) into slots int32 [tokens] of
+    k_cache, v_cache uint8 [pages, kv_heads, page_bytes]."""
+    op = "kq_kv_store"
+    ks, vs = _row_stride(op, "k", k), _row_stride(op, "v", v)
+    if k.shape != v.shape or k.dtype != v.dtype:
+        raise ValueError(f"{op}: k and v must have the same shape and dtype")
+    tokens, heads, d = k.shape
+    pages, cache_heads = _cache(op, codec, k_cache, v_cache, page, d)
+    if cache_heads != heads:
+        raise ValueError(f"{op}: rows of {heads} heads, a cache of {cache_heads}")
+    _ints(op, tokens, slots=slots)
+    _same_device(op, k_cache, k, v, slots, v_cache)
+    _run_on(k_cache, stream, lambda st: _lib.kq_kv_store(
+        _codec(codec), _ptr(k), _ptr(v), _dtype_id(k), tokens, heads, d, ks, vs, _ptr(slots), _ptr(k_cache),
+        _ptr(v_cache), pages, page, st))
+
+
+def kq_kv_load(codec, k_cache, v_cache, slots, page: int, k, v, stream=None) -> None:
+    """The rows at slots int32 [tokens] of the caches to k, v [tokens, kv_heads, d] (float32, float16 or bfloat16)."""
+    op = "kq_kv_load"
+    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or not k.is_contiguous() or not v.is_contiguous():
+        raise ValueError(f"{op}: k and v must be contiguous [tokens, kv_heads, d] of one dtype")
+    tokens, heads, d = k.shape
+    pages, cache_heads = _cache(op, codec, k_cache, v_cache, page, d)
+    if cache_heads != heads:
+        raise ValueError(f"{op}: rows of {heads} heads, a cache of {cache_heads}")
+    _ints(op, tokens, slots=slots)
+    _same_device(op, k_cache, v_cache, slots, k, v)
+    _run_on(k_cache, stream, lambda st: _lib.kq_kv_load(
+        _codec(codec), _ptr(k_cache), _ptr(v_cache), pages, page, heads, d, _ptr(slots), tokens, _ptr(k), _ptr(v),
+        _dtype_id(k), st))
+
+
+def kq_kv_attention_workspace(tokens: int, n_seqs: int, q_heads: int, kv_heads: int, d: int, max_new: int,
+                              max_kv: int) -> int:
+    """Bytes of workspace that kq_kv_attention needs for these sizes (0: none)."""
+    out = c_i64()
+    _check(_lib.kq_kv_attention_workspace(tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv, ctypes.byref(out)))
+    return out.value
+
+
+def kq_kv_attention(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page: int, out, scale: float | None = None,
+                    window: int = 0, max_new: int | None = None, max_kv: int | None = None, workspace=None,
+                    stream=None) -> None:
+    """out[t, h] = softmax(scale * q . K^T) V over the 4-bit rows each token sees (causal, window > 0: the last `window`
+    keys).  q float16/bfloat16 [tokens, q_heads, d] (dense rows, any row stride); cu_new int32 [n + 1], seq_lens int32
+    [n], table int32 [n, width]; out [tokens, q_heads, d]; scale defaults to d^-0.5.  max_new and max_kv bound a
+    request's new tokens and length (default: tokens, width * page).  workspace: uint8 of kq_kv_attention_workspace
+    bytes; allocated on the current stream if left out."""
+    op, n = "kq_kv_attention", seq_lens.numel()
+    qs = _row_stride(op, "q", q)
+    tokens, heads, d = q.shape
+    if out.shape != q.shape or not out.is_contiguous():
+        raise ValueError(f"{op}: out must be a contiguous [{tokens}, {heads}, {d}]")
+    if table.dim() != 2 or table.shape[0] != n:
+        raise ValueError(f"{op}: table must be [{n}, width]")
+    pages, kv_heads = _cache(op, codec, k_cache, v_cache, page, d)
+    _ints(op, n, seq_lens=seq_lens)
+    _ints(op, n + 1, cu_new=cu_new)
+    _ints(op, None, table=table)
+    _same_device(op, q, cu_new, seq_lens, table, k_cache, v_cache, out, workspace)
+    max_new = max(tokens, 1) if max_new is None else max_new
+    max_kv = max(table.shape[1] * page, 1) if max_kv is None else max_kv
+    if workspace is None:
+        need = kq_kv_attention_workspace(tokens, n, heads, kv_heads, d, max_new, max_kv)
+        if need:
+            if stream is not None and _stream(stream) != _stream(None):
+                raise ValueError(f"{op}: a call on another stream than the current one needs its own workspace")
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError(f"{op}: workspace must be contiguous")
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run_on(q, stream, lambda st: _lib.kq_kv_attention(
+        _codec(codec), _ptr(q), _dtype_id(q), tokens, heads, kv_heads, d, qs, _ptr(cu_new), _ptr(seq_lens), n,
+        _ptr(table), table.shape[1], _ptr(k_cache), _ptr(v_cache), pages, page,
+        d ** -0.5 if scale is None else scale, window, max_new, max_kv, _ptr(out), _dtype_id(out), _ptr(workspace),
+        ws_bytes, st))
+
+
+# ---------------------------------------------------------------------------
 # allocating conveniences (torch allocates; the library computes)
 # ---------------------------------------------------------------------------
 
@@ -306,3 +473,24 @@ def expert_tile_map(sorted_ids, n_experts: int):
     counts = torch.empty((1,), dtype=torch.int32, device=sorted_ids.device)
     kq_expert_tile_map(sorted_ids, n_experts, map_[:cap] if cap else map_, counts)
     return map_, counts
+
+
+def kv_cache(codec, pages: int, kv_heads: int, page: int, d: int, device="cuda"):
+    """A zeroed key and value cache, uint8 [pages, kv_heads, page_bytes] each."""
+    shape = (pages, kv_heads, kq_kv_page_bytes(codec, page, d))
+    return tuple(torch.zeros(shape, dtype=torch.uint8, device=device) for _ in range(2))
+
+
+def block_tables(ctx_lens, new_lens, free_pages, free_head, page: int, table, tokens: int):
+    """(slots [tokens], cu_new [n + 1], seq_lens [n], free_head_out [1], status [1]) of a step; table is updated."""
+    n, dev = ctx_lens.numel(), ctx_lens.device
+    slots, cu, lens, head, status = (torch.empty((m,), dtype=torch.int32, device=dev) for m in (tokens, n + 1, n, 1, 1))
+    kq_block_tables(ctx_lens, new_lens, free_pages, free_head, page, table, slots, cu, lens, head, status)
+    return slots, cu, lens, head, status
+
+
+def kv_attention(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page: int, scale=None, window: int = 0,
+                 max_new=None, max_kv=None, out_dtype=None):
+    out = torch.zeros(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    kq_kv_attention(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page, out, scale, window, max_new, max_kv)
+    return out

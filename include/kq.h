@@ -273,6 +273,107 @@ int kq_moe_glu_gather(int codec, const void* gate_w, const void* up_w, int64_t n
 int kq_quantize(int codec, const float* w, int64_t rows, int64_t k,
                 void* out, void* stream);
 
+/* ---- key/value cache in 4 bits: what one row holds ----
+ * A cache keeps key (or value) rows as q4_0 blocks in pages:
+ * uint8 [pages][kv_heads][page_bytes], page rows ("slots") to a page; slot
+ * s is row s % page of page s / page.  Inside one (page, head): the codes
+ * of its rows (d / 2 bytes a row, value v in nibble v, the low nibble of a
+ * byte first), then their scales (d / 32 float16 a row); page_bytes =
+ * page * (d / 2 + d / 16), as many bytes as the wire format's 18 per 32
+ * values, with every row of codes 16-byte aligned.  Code c of a block of
+ * scale D stands for D * (c - 8).  The codec is KQ_Q4_0 (KQ_ERR_CODEC
+ * otherwise); d a multiple of 32 in 32..256 and page a power of two in
+ * 16..4096 (KQ_ERR_SHAPE otherwise); caches are 16-byte aligned. */
+int kq_kv_page_bytes(int codec, int64_t page, int64_t d, int64_t* page_bytes);
+
+/* ---- block tables and slot map of one step ----
+ * The pages and slots of a step's new tokens, built on the GPU from the
+ * requests' lengths: no host sync.  Request s holds ctx_lens[s] tokens in
+ * the pages table[s][0 .. ceil(ctx / page)) and adds new_lens[s]; the new
+ * tokens of all requests lie one after the other in the step's token buffer
+ * of `tokens` rows.  The pages it grows by are taken, requests in order,
+ * from free_pages[free_head[0] ..] (int32 [n_free]).  Written:
+ *   table     int32 [n_seqs][width]: the new pages' ids, behind the held
+ *             ones (the other entries stay as they were)
+ *   slots     int32 [tokens]: page id * page + offset of every new token;
+ *             -1 for rows behind the last request and for refused requests
+ *   cu_new    int32 [n_seqs + 1]: first row of each request, then the end
+ *             (clamped to `tokens`)
+ *   seq_lens  int32 [n_seqs]: ctx + new (0 for refused requests, whose
+ *             queries then attend nothing)
+ *   free_head_out  int32 [1]: free_head plus the pages taken
+ *   status    nullable uint32 [1]: bit0 = a request refused because the free
+ *             pages ran out (it takes none), bit1 = one that needs more than
+ *             `width` pages, bit2 = one whose rows pass `tokens`, bit3 = a
+ *             negative length (taken as no rows).
+ * A request refused for its width, rows or lengths takes no pages; once
+ * pages run out, later requests that need any are refused too.  Ids read
+ * from the table and the free list are not checked here: a token whose page
+ * id is negative, or whose slot does not fit 31 bits, gets slot -1.  Outputs
+ * must not overlap inputs or each other (KQ_ERR_ARG). */
+int kq_block_tables(const int32_t* ctx_lens, const int32_t* new_lens, int64_t n_seqs, int64_t page,
+                    const int32_t* free_pages, int64_t n_free, const int32_t* free_head,
+                    int32_t* table, int64_t width, int32_t* slots, int64_t tokens, int32_t* cu_new,
+                    int32_t* seq_lens, int32_t* free_head_out, uint32_t* status, void* stream);
+
+/* ---- cache rows: encode into slots, decode from slots ----
+ * kq_kv_store: rows k, v [tokens][kv_heads][d] (x_dtype KQ_F32, KQ_F16 or
+ * KQ_BF16; row t starts k_stride resp. v_stride elements after row t - 1, so
+ * they may be slices of a fused projection) become q4_0 blocks at
+ * slots[t] (int32, device) of k_cache and v_cache.  Rows whose slot is
+ * outside 0 .. pages * page - 1 are skipped; slots of one call must differ
+ * (equal slots race).  The block encoding is kq_quantize's for q4_0, made
+ * total: NaN counts as 0, magnitudes above 65504 as 65504, and the scale
+ * float16(max|x| / 7) is at most 8188 (kq_quantize's own result wherever
+ * max|x| <= 57316), so that every stored value is a finite float16.
+ * kq_kv_load: the values at slots[t], as out_dtype, to k, v
+ * [tokens][kv_heads][d] dense; each is D * (c - 8), rounded once.  Rows whose
+ * slot is outside the cache are left unwritten.
+ * k, v are 16-byte aligned, strides multiples of 8 elements and >=
+ * kv_heads * d (KQ_ERR_ALIGN, KQ_ERR_SHAPE). */
+int kq_kv_store(int codec, const void* k, const void* v, int x_dtype, int64_t tokens, int64_t kv_heads, int64_t d,
+                int64_t k_stride, int64_t v_stride, const int32_t* slots, void* k_cache, void* v_cache,
+                int64_t pages, int64_t page, void* stream);
+int kq_kv_load(int codec, const void* k_cache, const void* v_cache, int64_t pages, int64_t page, int64_t kv_heads,
+               int64_t d, const int32_t* slots, int64_t tokens, void* k, void* v, int out_dtype, void* stream);
+
+/* ---- attention over the cache ----
+ * q [tokens][q_heads][d] (q_dtype KQ_F16 or KQ_BF16, rows q_stride elements
+ * apart): the new tokens of n_seqs requests, request s in rows cu_new[s] ..
+ * cu_new[s + 1] - 1 (n of them).  Its keys and values are the rows 0 ..
+ * seq_lens[s] - 1 of the pages table[s][0 ..] (int32 [n_seqs][width]), new
+ * tokens included (store them first).  Row i of the request stands at
+ * position p = seq_lens[s] - n + i and sees the keys j <= p, with window > 0
+ * only those with j > p - window.  Query head h reads kv head
+ * h / (q_heads / kv_heads).
+ *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j
+ * out [tokens][q_heads][d] dense, out_dtype KQ_F32, KQ_F16 or KQ_BF16.  A
+ * row that sees no key (a request of length 0, p < 0) is all zeros; rows
+ * outside cu_new[0] .. cu_new[n_seqs] - 1 are left unwritten.  Keys and values
+ * enter the matrix cores as float16, rounded once from their exact values;
+ * queries exactly (bfloat16 ones scaled by a power of two per row); products,
+ * softmax statistics and sums are float32, probabilities float16.
+ * Device data is bounded, not trusted: cu_new entries are clamped to 0 ..
+ * tokens, a length to 0 .. width * page, and keys whose table entry is not a
+ * page of the cache are left out.  The cache is expected to hold finite
+ * values, as kq_kv_store writes.
+ * max_new and max_kv are the host's bounds on new tokens and length of a
+ * request (at least 1): they choose the split of the work and the size of
+ * the workspace; a request beyond them is still computed whole.
+ * workspace (16-byte aligned) holds partial results where the keys of a row
+ * are split over workgroups: kq_kv_attention_workspace gives its bytes (0:
+ * none needed, workspace may be NULL; KQ_ERR_CAPACITY if it is too small) for
+ * the same sizes.  Its contents mean nothing between calls; calls that may run
+ * at the same time need one each.  Results are deterministic for given sizes
+ * and lengths. */
+int kq_kv_attention_workspace(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d,
+                              int64_t max_new, int64_t max_kv, int64_t* bytes);
+int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64_t q_heads, int64_t kv_heads,
+                    int64_t d, int64_t q_stride, const int32_t* cu_new, const int32_t* seq_lens, int64_t n_seqs,
+                    const int32_t* table, int64_t width, const void* k_cache, const void* v_cache, int64_t pages,
+                    int64_t page, float scale, int64_t window, int64_t max_new, int64_t max_kv, void* out,
+                    int out_dtype, void* workspace, int64_t workspace_bytes, void* stream);
+
 /* ---- measurement helper: plain read of device memory ----
  * Reads `bytes` (a multiple of 16) at src with nontemporal 16-byte loads,
  * split over `groups` workgroups (1..2^20) of four waves that each read one

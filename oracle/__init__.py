@@ -34,4 +34,4 @@ oracle's own code) are listed in each module's header. Parity status:
     file or gguf package is available to check the byte layout against).
 """
 
-from . import codecs, encode, matmul  # noqa: F401
+from . import codecs, encode, kvcache, matmul  # noqa: F401
