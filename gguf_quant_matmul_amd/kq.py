@@ -115,8 +115,15 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is not None:
         return int(stream) if isinstance(stream, int) else stream.cuda_stream
-    import torch
+    return _current_stream()
 
+
+def _current_stream() -> int:
+    """The current device's current stream (torch's raw accessor where it has one: a tenth of the time that building
+    a Stream object takes)."""
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if raw is not None:
+        return raw(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -284,111 +291,126 @@ def kq_stream_read(src, out, nbytes: int | None = None, stream=None) -> None:
 # key/value cache in 4 bits
 # ---------------------------------------------------------------------------
 
-def _ints(op: str, n: int | None, **arrays) -> None:
-    """Index arrays are contiguous 32-bit integers, of n entries where n is given."""
-    for name, t in arrays.items():
-        if t is None:
-            continue
-        if t.dtype not in (torch.int32, torch.uint32):
-            raise TypeError(f"{op}: {name} must be int32, got {t.dtype}")
-        if not t.is_contiguous():
-            raise ValueError(f"{op}: {name} must be contiguous")
-        if n is not None and t.numel() != n:
-            raise ValueError(f"{op}: {name} has {t.numel()} entries, expected {n}")
+# These calls are often shorter than their Python side, so the checks are
+# written out: one attribute read each, no helper call on the good path.
+_INTS = (torch.int32, torch.uint32)
+_DTYPES = {torch.float32: KQ_F32, torch.float16: KQ_F16, torch.bfloat16: KQ_BF16}
 
 
-def _same_device(op: str, first, *rest) -> None:
-    for t in rest:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{op}: tensors on {first.device} and {t.device}")
+def _index_error(op: str, name: str, t, n: int | None, device: int) -> None:
+    """Raise for an index array that is not contiguous 32-bit integers (n of them, where n is given) on the device."""
+    if t.dtype not in _INTS:
+        raise TypeError(f"{op}: {name} must be int32, got {t.dtype}")
+    if not t.is_contiguous():
+        raise ValueError(f"{op}: {name} must be contiguous")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{op}: {name} has {t.numel()} entries, expected {n}")
+    raise ValueError(f"{op}: {name} is on device {t.get_device()}, not {device}")
 
 
-def _run_on(t, stream, call) -> None:
-    """call(stream) with t's device current: the given stream, else t's device's current one."""
-    if not t.is_cuda or t.device.index == torch.cuda.current_device():
-        _check(call(_stream(stream)))
-        return
-    with torch.cuda.device(t.device):
-        _check(call(_stream(stream)))
+def _index(op: str, name: str, t, n: int | None, device: int) -> int:
+    """Device pointer of an index array, checked."""
+    if (t.dtype not in _INTS or not t.is_contiguous() or (n is not None and t.numel() != n)
+            or t.get_device() != device):
+        _index_error(op, name, t, n, device)
+    return t.data_ptr()
 
 
-def _cache(op: str, codec, k_cache, v_cache, page: int, d: int) -> tuple[int, int]:
-    """(pages, kv_heads) of two caches uint8 [pages, kv_heads, page_bytes]."""
-    pb = kq_kv_page_bytes(codec, page, d)
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        if t.dtype != torch.uint8 or t.dim() != 3 or not t.is_contiguous() or t.shape != k_cache.shape:
-            raise ValueError(f"{op}: {name} must be a contiguous uint8 [pages, kv_heads, {pb}]")
-    if k_cache.shape[2] != pb:
-        raise ValueError(f"{op}: pages hold {k_cache.shape[2]} bytes a head, {pb} expected for page={page}, d={d}")
-    return k_cache.shape[0], k_cache.shape[1]
+def _call_on(device: int, stream, fn, *args) -> None:
+    """fn(*args, stream) with `device` current: on the given stream, else on that device's current one."""
+    if device < 0 or device == torch.cuda.current_device():
+        status = fn(*args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            status = fn(*args, _stream(stream))
+    if status != KQ_OK:
+        _check(status)
 
 
-def _row_stride(op: str, name: str, x) -> int:
+_PAGE_BYTES: dict = {}  # (codec, page, d) -> (codec id, bytes): pure functions of their arguments
+
+
+def _page_bytes(codec, page: int, d: int) -> tuple[int, int]:
+    key = (codec, page, d)
+    got = _PAGE_BYTES.get(key)
+    if got is None:
+        out, cid = c_i64(), _codec(codec)
+        _check(_lib.kq_kv_page_bytes(cid, page, d, ctypes.byref(out)))
+        got = _PAGE_BYTES[key] = (cid, out.value)
+    return got
+
+
+def _cache(op: str, codec, k_cache, v_cache, page: int, d: int, heads: int | None, device: int):
+    """(codec id, pages, kv heads) of two caches uint8 [pages, kv_heads, page_bytes]."""
+    cid, pb = _page_bytes(codec, page, d)
+    shape = k_cache.shape
+    if (k_cache.dtype is not torch.uint8 or v_cache.dtype is not torch.uint8 or len(shape) != 3
+            or v_cache.shape != shape or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        raise ValueError(f"{op}: k_cache and v_cache must be contiguous uint8 [pages, kv_heads, {pb}]")
+    pages, cache_heads, have = shape
+    if have != pb:
+        raise ValueError(f"{op}: pages hold {have} bytes a head, {pb} expected for page={page}, d={d}")
+    if heads is not None and cache_heads != heads:
+        raise ValueError(f"{op}: rows of {heads} heads, a cache of {cache_heads}")
+    if k_cache.get_device() != device or v_cache.get_device() != device:
+        raise ValueError(f"{op}: caches on devices {k_cache.get_device()} and {v_cache.get_device()}, rows on {device}")
+    return cid, pages, cache_heads
+
+
+def _row_stride(op: str, name: str, x, shape) -> int:
     """Elements between rows of x [tokens, heads, d], whose rows are dense."""
-    if x.dim() != 3:
-        raise ValueError(f"{op}: {name} must be [tokens, heads, d]")
-    dense = x.shape[1] * x.shape[2]
-    if x.numel() and (x.stride(2) != 1 or (x.shape[1] > 1 and x.stride(1) != x.shape[2])):
+    tokens, heads, d = shape
+    st = x.stride()
+    if x.numel() and (st[2] != 1 or (heads > 1 and st[1] != d)):
         raise ValueError(f"{op}: the rows of {name} must be dense")
-    return x.stride(0) if x.shape[0] > 1 else dense
+    return st[0] if tokens > 1 else heads * d
 
 
 def kq_kv_page_bytes(codec, page: int, d: int) -> int:
     """Bytes of one (page, kv head) of a 4-bit key or value cache."""
-    out = c_i64()
-    _check(_lib.kq_kv_page_bytes(_codec(codec), page, d, ctypes.byref(out)))
-    return out.value
+    return _page_bytes(codec, page, d)[1]
 
 
 def kq_block_tables(ctx_lens, new_lens, free_pages, free_head, page: int, table, slots, cu_new, seq_lens,
                     free_head_out, status=None, stream=None) -> None:
     """Pages and slots of a step's new tokens.  ctx_lens, new_lens, seq_lens int32 [n]; free_pages int32 [n_free] from
     free_head int32 [1]; table int32 [n, width]; slots int32 [tokens]; cu_new int32 [n + 1]; free_head_out, status [1]."""
-    op, n = "kq_block_tables", ctx_lens.numel()
+    op, n, dev = "kq_block_tables", ctx_lens.numel(), ctx_lens.get_device()
     if table.dim() != 2 or table.shape[0] != n:
         raise ValueError(f"{op}: table must be [{n}, width]")
-    _ints(op, n, ctx_lens=ctx_lens, new_lens=new_lens, seq_lens=seq_lens)
-    _ints(op, 1, free_head=free_head, free_head_out=free_head_out, status=status)
-    _ints(op, n + 1, cu_new=cu_new)
-    _ints(op, None, free_pages=free_pages, table=table, slots=slots)
-    _same_device(op, ctx_lens, new_lens, free_pages, free_head, table, slots, cu_new, seq_lens, free_head_out, status)
-    _run_on(ctx_lens, stream, lambda st: _lib.kq_block_tables(
-        _ptr(ctx_lens), _ptr(new_lens), n, page, _ptr(free_pages), free_pages.numel(), _ptr(free_head), _ptr(table),
-        table.shape[1], _ptr(slots), slots.numel(), _ptr(cu_new), _ptr(seq_lens), _ptr(free_head_out), _ptr(status), st))
+    _call_on(dev, stream, _lib.kq_block_tables, _index(op, "ctx_lens", ctx_lens, n, dev),
+             _index(op, "new_lens", new_lens, n, dev), n, page, _index(op, "free_pages", free_pages, None, dev),
+             free_pages.numel(), _index(op, "free_head", free_head, 1, dev), _index(op, "table", table, None, dev),
+             table.shape[1], _index(op, "slots", slots, None, dev), slots.numel(),
+             _index(op, "cu_new", cu_new, n + 1, dev), _index(op, "seq_lens", seq_lens, n, dev),
+             _index(op, "free_head_out", free_head_out, 1, dev),
+             None if status is None else _index(op, "status", status, 1, dev))
 
 
 def kq_kv_store(codec, k, v, slots, k_cache, v_cache, page: int, stream=None) -> None:
     """k, v float32/float16/bfloat16 [tokens, kv_heads, d] (dense rows, any row stride) into slots int32 [tokens] of
     k_cache, v_cache uint8 [pages, kv_heads, page_bytes]."""
-    op = "kq_kv_store"
-    ks, vs = _row_stride(op, "k", k), _row_stride(op, "v", v)
-    if k.shape != v.shape or k.dtype != v.dtype:
-        raise ValueError(f"{op}: k and v must have the same shape and dtype")
-    tokens, heads, d = k.shape
-    pages, cache_heads = _cache(op, codec, k_cache, v_cache, page, d)
-    if cache_heads != heads:
-        raise ValueError(f"{op}: rows of {heads} heads, a cache of {cache_heads}")
-    _ints(op, tokens, slots=slots)
-    _same_device(op, k_cache, k, v, slots, v_cache)
-    _run_on(k_cache, stream, lambda st: _lib.kq_kv_store(
-        _codec(codec), _ptr(k), _ptr(v), _dtype_id(k), tokens, heads, d, ks, vs, _ptr(slots), _ptr(k_cache),
-        _ptr(v_cache), pages, page, st))
+    op, shape, dt, dev = "kq_kv_store", k.shape, _DTYPES.get(k.dtype), k.get_device()
+    if len(shape) != 3 or v.shape != shape or v.dtype is not k.dtype or dt is None or v.get_device() != dev:
+        raise ValueError(f"{op}: k and v must be [tokens, kv_heads, d] of one float dtype and device")
+    tokens, heads, d = shape
+    ks, vs = _row_stride(op, "k", k, shape), _row_stride(op, "v", v, shape)
+    cid, pages, _ = _cache(op, codec, k_cache, v_cache, page, d, heads, dev)
+    _call_on(dev, stream, _lib.kq_kv_store, cid, k.data_ptr(), v.data_ptr(), dt, tokens, heads, d, ks, vs,
+             _index(op, "slots", slots, tokens, dev),
+             k_cache.data_ptr(), v_cache.data_ptr(), pages, page)
 
 
 def kq_kv_load(codec, k_cache, v_cache, slots, page: int, k, v, stream=None) -> None:
     """The rows at slots int32 [tokens] of the caches to k, v [tokens, kv_heads, d] (float32, float16 or bfloat16)."""
-    op = "kq_kv_load"
-    if k.dim() != 3 or k.shape != v.shape or k.dtype != v.dtype or not k.is_contiguous() or not v.is_contiguous():
-        raise ValueError(f"{op}: k and v must be contiguous [tokens, kv_heads, d] of one dtype")
-    tokens, heads, d = k.shape
-    pages, cache_heads = _cache(op, codec, k_cache, v_cache, page, d)
-    if cache_heads != heads:
-        raise ValueError(f"{op}: rows of {heads} heads, a cache of {cache_heads}")
-    _ints(op, tokens, slots=slots)
-    _same_device(op, k_cache, v_cache, slots, k, v)
-    _run_on(k_cache, stream, lambda st: _lib.kq_kv_load(
-        _codec(codec), _ptr(k_cache), _ptr(v_cache), pages, page, heads, d, _ptr(slots), tokens, _ptr(k), _ptr(v),
-        _dtype_id(k), st))
+    op, shape, dt, dev = "kq_kv_load", k.shape, _DTYPES.get(k.dtype), k.get_device()
+    if (len(shape) != 3 or v.shape != shape or v.dtype is not k.dtype or dt is None or v.get_device() != dev
+            or not k.is_contiguous() or not v.is_contiguous()):
+        raise ValueError(f"{op}: k and v must be contiguous [tokens, kv_heads, d] of one float dtype and device")
+    tokens, heads, d = shape
+    cid, pages, _ = _cache(op, codec, k_cache, v_cache, page, d, heads, dev)
+    _call_on(dev, stream, _lib.kq_kv_load, cid, k_cache.data_ptr(), v_cache.data_ptr(), pages, page, heads, d,
+             _index(op, "slots", slots, tokens, dev), tokens, k.data_ptr(), v.data_ptr(), dt)
 
 
 def kq_kv_attention_workspace(tokens: int, n_seqs: int, q_heads: int, kv_heads: int, d: int, max_new: int,
@@ -407,34 +429,39 @@ def kq_kv_attention(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page: i
     [n], table int32 [n, width]; out [tokens, q_heads, d]; scale defaults to d^-0.5.  max_new and max_kv bound a
     request's new tokens and length (default: tokens, width * page).  workspace: uint8 of kq_kv_attention_workspace
     bytes; allocated on the current stream if left out."""
-    op, n = "kq_kv_attention", seq_lens.numel()
-    qs = _row_stride(op, "q", q)
-    tokens, heads, d = q.shape
-    if out.shape != q.shape or not out.is_contiguous():
-        raise ValueError(f"{op}: out must be a contiguous [{tokens}, {heads}, {d}]")
-    if table.dim() != 2 or table.shape[0] != n:
+    op, n, shape, dev = "kq_kv_attention", seq_lens.numel(), q.shape, q.get_device()
+    qdt, odt = _DTYPES.get(q.dtype), _DTYPES.get(out.dtype)
+    if len(shape) != 3 or qdt is None or odt is None:
+        raise ValueError(f"{op}: q must be float16 or bfloat16 [tokens, q_heads, d], out a float tensor of its shape")
+    tokens, heads, d = shape
+    if out.shape != shape or not out.is_contiguous() or out.get_device() != dev:
+        raise ValueError(f"{op}: out must be a contiguous [{tokens}, {heads}, {d}] on q's device")
+    tshape = table.shape
+    if len(tshape) != 2 or tshape[0] != n:
         raise ValueError(f"{op}: table must be [{n}, width]")
-    pages, kv_heads = _cache(op, codec, k_cache, v_cache, page, d)
-    _ints(op, n, seq_lens=seq_lens)
-    _ints(op, n + 1, cu_new=cu_new)
-    _ints(op, None, table=table)
-    _same_device(op, q, cu_new, seq_lens, table, k_cache, v_cache, out, workspace)
-    max_new = max(tokens, 1) if max_new is None else max_new
-    max_kv = max(table.shape[1] * page, 1) if max_kv is None else max_kv
+    cid, pages, kv_heads = _cache(op, codec, k_cache, v_cache, page, d, None, dev)
+    width = tshape[1]
+    if max_new is None:
+        max_new = max(tokens, 1)
+    if max_kv is None:
+        max_kv = max(width * page, 1)
     if workspace is None:
         need = kq_kv_attention_workspace(tokens, n, heads, kv_heads, d, max_new, max_kv)
+        ws = None
         if need:
-            if stream is not None and _stream(stream) != _stream(None):
+            if stream is not None and _stream(stream) != torch.cuda.current_stream(q.device).cuda_stream:
                 raise ValueError(f"{op}: a call on another stream than the current one needs its own workspace")
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif not workspace.is_contiguous():
-        raise ValueError(f"{op}: workspace must be contiguous")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _run_on(q, stream, lambda st: _lib.kq_kv_attention(
-        _codec(codec), _ptr(q), _dtype_id(q), tokens, heads, kv_heads, d, qs, _ptr(cu_new), _ptr(seq_lens), n,
-        _ptr(table), table.shape[1], _ptr(k_cache), _ptr(v_cache), pages, page,
-        d ** -0.5 if scale is None else scale, window, max_new, max_kv, _ptr(out), _dtype_id(out), _ptr(workspace),
-        ws_bytes, st))
+            ws = workspace.data_ptr()
+    else:
+        if not workspace.is_contiguous() or workspace.get_device() != dev:
+            raise ValueError(f"{op}: workspace must be contiguous, on q's device")
+        need, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
+    _call_on(dev, stream, _lib.kq_kv_attention, cid, q.data_ptr(), qdt, tokens, heads, kv_heads, d,
+             _row_stride(op, "q", q, shape), _index(op, "cu_new", cu_new, n + 1, dev),
+             _index(op, "seq_lens", seq_lens, n, dev), n, _index(op, "table", table, None, dev), width,
+             k_cache.data_ptr(), v_cache.data_ptr(), pages, page, d ** -0.5 if scale is None else scale, window,
+             max_new, max_kv, out.data_ptr(), odt, ws, need)
 
 
 # ---------------------------------------------------------------------------
