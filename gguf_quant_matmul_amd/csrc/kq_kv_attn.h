@@ -99,7 +99,10 @@ struct H2x4 {
   half2_t v[4];
 };
 __device__ __forceinline__ H2x4 unpack8(uint32_t w) {
-  constexpr uint32_t M = 0x64006400u;
+  // in a vector register, so that and-or is one instruction (it takes one
+  // scalar operand, the mask): 13 instead of 17 for eight values
+  uint32_t M = 0x64006400u;
+  asm("" : "+v"(M));
   const uint32_t u = w >> 8;
   const half2_t k0 = half2_t{(half_t)1032.f, (half_t)1032.f}, k1 = half2_t{(half_t)-72.f, (half_t)-72.f},
                 s = half2_t{(half_t)0.0625f, (half_t)0.0625f};

@@ -44,16 +44,57 @@ constexpr int lds_bytes() {
   return s > m ? s : m;
 }
 
+// A step's four 16-key groups: byte offsets of their codes and scales in the
+// caches, and which of them are there (a group past the last key or without a
+// page of the cache reads page 0 and is left out).  Uniform over the wave.
+struct Groups {
+  int64_t codes[4], scales[4];
+  uint32_t ok;  // bit i
+};
+template <int D>
+__device__ __forceinline__ Groups groups_of(const AttnArgs& a, const int (&ids)[4], int base, int end, int h) {
+  Groups r;
+  r.ok = 0;
+  const int mask = (1 << a.page_shift) - 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = base + 16 * i;
+    const bool ok = k < end && ids[i] >= 0 && ids[i] < a.pages;
+    const int64_t at = ((int64_t)(ok ? ids[i] : 0) * a.hkv + h) * a.page_head_bytes;
+    r.codes[i] = at + (int64_t)(k & mask) * (D / 2);
+    r.scales[i] = at + ((int64_t)(D / 2) << a.page_shift) + (int64_t)(k & mask) * (D / 16);
+    r.ok |= ok ? 1u << i : 0u;
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ T pick4(const T (&v)[4], int i) {
+  const T lo = i & 1 ? v[1] : v[0], hi = i & 1 ? v[3] : v[2];
+  return i & 2 ? hi : lo;
+}
+
 template <int NB>
-__global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
+__global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnArgs a) {
   constexpr int D = 32 * NB;
   constexpr int DT = D / 16;  // 16-value tiles of O^T
+  // 16-key groups of V are whole or half waves of 16-byte pieces: which group
+  // a load belongs to is then the same for all lanes
+  constexpr bool WHOLE = NB % 4 == 0;
+  // K scales of a lane: one where its quarter row lies inside a block, one per
+  // block where it covers whole ones, else one per dword
+  constexpr int KS = NB == 1 || NB == 2 || NB == 4 ? 1 : NB == 8 ? 2 : NB;
   __shared__ __attribute__((aligned(16))) uint8_t lds[lds_bytes<NB>()];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, col = lane & 15, g = lane >> 4;
+  const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = blockIdx.x % a.hkv, tile = blockIdx.x / a.hkv, split = blockIdx.y;
 
   int s = tile, sub = 0;
-  if (!a.one_tile && !find_tile(a, tile, 16, s, sub)) return;
+  if (!a.one_tile) {
+    if (!find_tile(a, tile, 16, s, sub)) return;
+    s = __builtin_amdgcn_readfirstlane(s);
+    sub = __builtin_amdgcn_readfirstlane(sub);
+  }
   const Seq sq = load_seq(a, s);
   const int rows = sq.n * a.group;
   // with one tile to a request, a request that has more walks its own
@@ -79,128 +120,147 @@ __global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
       const int steps = (keys.end - keys.lo + STEP - 1) / STEP;
       const int st0 = (int)((int64_t)steps * split / n_split), st1 = (int)((int64_t)steps * (split + 1) / n_split);
 
+      uint8_t* codes = lds + wave * Stage<NB>::BYTES;
+      uint16_t* scales = (uint16_t*)(codes + STEP * Stage<NB>::ROW);
+      const int32_t* pages = a.table + (int64_t)s * a.width;
+
+      // registers of the step in flight
+      uint32_t kw[4][NB];
+      uint16_t ks[4][KS];
+      u32x4 vw[NB];
+      uint16_t vs[NB];
+      const auto page_ids = [&](int st, int (&ids)[4]) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int k = keys.lo + st * STEP + 16 * i;
+          ids[i] = st < st1 && k < keys.end ? pages[k >> a.page_shift] : -1;
+        }
+      };
+      const auto load_k = [&](const Groups& gr) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          load_dwords<NB>(a.kc + gr.codes[i] + (uint32_t)(col * (D / 2) + g * (D / 8)), kw[i]);
+#pragma unroll
+          for (int j = 0; j < KS; ++j) {
+            // dword j of quarter g lies in block (g NB + j) / 4
+            const uint32_t b = KS == NB ? (g * NB + j) >> 2 : KS == 2 ? 2 * g + j : (g * NB) >> 2;
+            ks[i][j] = (uint16_t)ld_u16(a.kc + gr.scales[i] + (uint32_t)(col * (D / 16) + 2 * b));
+          }
+        }
+      };
+      const auto load_v = [&](const Groups& gr) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int piece = i * 64 + lane, key = piece / NB, b = piece % NB;
+          const int64_t at = WHOLE ? gr.codes[i / (NB / 4 > 0 ? NB / 4 : 1)] : pick4(gr.codes, key >> 4);
+          vw[i] = ld_16B(a.vc + at + (uint32_t)((key & 15) * (D / 2) + 16 * b));
+        }
+        const uint8_t* sp = a.vc + pick4(gr.scales, g) + (uint32_t)(col * (D / 16));
+#pragma unroll
+        for (int b = 0; b < NB; ++b) vs[b] = (uint16_t)ld_u16(sp + 2 * b);
+      };
+
+      int ids[4], ids_next[4];
+      page_ids(st0 + wave, ids);
+      page_ids(st0 + wave + WAVES, ids_next);
       half8_t q[NB];
       float factor;
       load_query<NB>(a, (const uint16_t*)a.q + (int64_t)tok * a.q_stride + (int64_t)head * D, live, g, q, factor);
+      // probabilities may reach 2^8 before the sums are brought to a new maximum
+      const float slack = 8.f / factor;
 
       float4_t o[DT];
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[t] = float4_t{0, 0, 0, 0};
-      float m = NEG_INF, l = 0.f;
+      float4_t l4 = {0, 0, 0, 0};
+      float m = NEG_INF;
 
-      uint8_t* codes = lds + wave * Stage<NB>::BYTES;
-      uint16_t* scales = (uint16_t*)(codes + STEP * Stage<NB>::ROW);
-      const int64_t row_scales = (int64_t)(D / 2) << a.page_shift;  // scales behind a page's codes
-      const int page_mask = (1 << a.page_shift) - 1;
-      const int32_t* pages = a.table + (int64_t)s * a.width;
-
+      Groups gr = groups_of<D>(a, ids, keys.lo + (st0 + wave) * STEP, keys.end, h);
+      if (st0 + wave < st1) {
+        load_k(gr);
+        load_v(gr);
+      }
       for (int st = st0 + wave; st < st1; st += WAVES) {
         const int base = keys.lo + st * STEP;
-        // the step's four 16-key groups: page, offset; a group past the end or
-        // without a page reads page 0 and is left out
-        int64_t at[4];  // byte offset of the (page, head)
-        int off[4];
-        bool ok[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int k = base + 16 * i;
-          const int id = k < keys.end ? pages[k >> a.page_shift] : -1;
-          ok[i] = id >= 0 && id < a.pages;
-          at[i] = ((int64_t)(ok[i] ? id : 0) * a.hkv + h) * a.page_head_bytes;
-          off[i] = k & page_mask;
-        }
+        const uint32_t ok = gr.ok;
+        const bool more = st + WAVES < st1;
         // V into LDS: 16-byte pieces of codes, the row of key 16 i + 4 c + j at 16 c + 4 i + j, so that
         // lane group c's keys lie together; scales in the order of the operands
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
-          const int piece = i * 64 + lane, key = piece / NB, b = piece % NB, kg = key >> 4;
-          const int64_t pa = kg == 0 ? at[0] : kg == 1 ? at[1] : kg == 2 ? at[2] : at[3];
-          const int po = (kg == 0 ? off[0] : kg == 1 ? off[1] : kg == 2 ? off[2] : off[3]) + (key & 15);
-          const u32x4 w = ld_16B(a.vc + pa + (int64_t)po * (D / 2) + 16 * b);
-          const int lr = ((key >> 2) & 3) * 16 + kg * 4 + (key & 3);
-          *(u32x4*)(codes + lr * Stage<NB>::ROW + 16 * b) = w;
+          const int piece = i * 64 + lane, key = piece / NB, b = piece % NB;
+          const int lr = ((key >> 2) & 3) * 16 + (key >> 4) * 4 + (key & 3);
+          *(u32x4*)(codes + lr * Stage<NB>::ROW + 16 * b) = vw[i];
         }
         {
-          const int kg = lane >> 4;
-          const int64_t pa = kg == 0 ? at[0] : kg == 1 ? at[1] : kg == 2 ? at[2] : at[3];
-          const int po = (kg == 0 ? off[0] : kg == 1 ? off[1] : kg == 2 ? off[2] : off[3]) + (lane & 15);
-          const bool good = (kg == 0 ? ok[0] : kg == 1 ? ok[1] : kg == 2 ? ok[2] : ok[3]) && base + lane < keys.end;
-          const uint8_t* sp = a.vc + pa + row_scales + (int64_t)po * (D / 16);
-          const int pos = ((lane >> 2) & 3) * 16 + (kg >> 1) * 8 + (lane & 3) * 2 + (kg & 1);
+          // bytes behind the last key are anything, NaN included: their values enter as 0 * code
+          const bool good = ((ok >> g) & 1u) && base + lane < keys.end;
+          const int pos = ((lane >> 2) & 3) * 16 + (g >> 1) * 8 + (lane & 3) * 2 + (g & 1);
 #pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            // bytes behind the last key are anything, NaN included: their values enter as 0 * code
-            const uint32_t sc = ld_u16(sp + 2 * b);
-            scales[b * 64 + pos] = good ? (uint16_t)sc : (uint16_t)0;
-          }
+          for (int b = 0; b < NB; ++b) scales[b * 64 + pos] = good ? vs[b] : (uint16_t)0;
         }
+        // the next step's addresses; its V goes into the registers just emptied
+        gr = groups_of<D>(a, ids_next, base + WAVES * STEP, keys.end, h);
+        if (more) load_v(gr);
+        page_ids(st + 2 * WAVES, ids_next);
         // S^T
         float4_t sc[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          uint32_t w[NB];
-          const uint8_t* kp = a.kc + at[i];
-          load_dwords<NB>(kp + (int64_t)(off[i] + col) * (D / 2) + g * (D / 8), w);
-          const uint8_t* sp = kp + row_scales + (int64_t)(off[i] + col) * (D / 16);
           sc[i] = float4_t{0, 0, 0, 0};
-          half2_t ks;
 #pragma unroll
           for (int j = 0; j < NB; ++j) {
-            // dword j of quarter g lies in block (g NB + j) / 4
-            if (j == 0 || (NB & (NB - 1)) != 0 || j % 4 == 0) {
-              const half_t v = __builtin_bit_cast(half_t, (uint16_t)ld_u16(sp + 2 * ((g * NB + j) >> 2)));
-              ks = half2_t{v, v};
-            }
-            const H2x4 u = unpack8(w[j]);
+            const half_t v = __builtin_bit_cast(half_t, ks[i][KS == NB ? j : KS == 2 ? j / 4 : 0]);
+            const half2_t kv = half2_t{v, v};
+            const H2x4 u = unpack8(kw[i][j]);
             sc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                operand(u.v[0] * ks, u.v[1] * ks, u.v[2] * ks, u.v[3] * ks), q[j], sc[i], 0, 0, 0);
+                operand(u.v[0] * kv, u.v[1] * kv, u.v[2] * kv, u.v[3] * kv), q[j], sc[i], 0, 0, 0);
           }
         }
-        const bool all_ok = ok[0] && ok[1] && ok[2] && ok[3];
-        if (base + STEP - 1 > p0 || (a.window > 0 && base <= p1 - a.window) || !all_ok) {
+        if (more) load_k(gr);
+        if (base + STEP - 1 > p0 || (a.window > 0 && base <= p1 - a.window) || ok != 15u) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
               const int k = base + 16 * i + 4 * g + j;
-              const bool see = ok[i] && k <= p && (a.window <= 0 || k > p - a.window);
+              const bool see = ((ok >> i) & 1u) && k <= p && (a.window <= 0 || k > p - a.window);
               sc[i][j] = see ? sc[i][j] : NEG_INF;
             }
         }
-        // running maximum and sum
+        // running maximum; the sums move to a new one only when it is well above the old
         float mx = sc[0][0];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) mx = fmaxf(mx, sc[i >> 2][i & 3]);
-        mx = fmaxf(groups_max(mx), m);
-        const float ref = mx == NEG_INF ? 0.f : mx;
-        const float corr = __builtin_amdgcn_exp2f((m - ref) * factor);
-        m = mx;
-        l *= corr;
+        for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i >> 2][i & 3]);
+        mx = groups_max(mx);
+        if (__any(!(mx <= m + slack))) {
+          mx = fmaxf(mx, m);
+          const float corr = mx == NEG_INF ? 1.f : __builtin_amdgcn_exp2f((m - mx) * factor);
+          m = mx;
+          l4 *= corr;
 #pragma unroll
-        for (int t = 0; t < DT; ++t) o[t] *= corr;
-        const float bias = -ref * factor;
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            sc[i][j] = __builtin_amdgcn_exp2f(fmaf(sc[i][j], factor, bias));
-            l += sc[i][j];
-          }
+          for (int t = 0; t < DT; ++t) o[t] *= corr;
+        }
+        const float bias = m == NEG_INF ? 0.f : -m * factor;
         // P^T operands: places (2 s, 2 s + 1) hold keys s of groups 2 m and 2 m + 1
         half8_t pt[2];
 #pragma unroll
         for (int mm = 0; mm < 2; ++mm)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            pt[mm][2 * j] = (half_t)sc[2 * mm][j];
-            pt[mm][2 * j + 1] = (half_t)sc[2 * mm + 1][j];
+            pt[mm][2 * j] = (half_t)__builtin_amdgcn_exp2f(fmaf(sc[2 * mm][j], factor, bias));
+            pt[mm][2 * j + 1] = (half_t)__builtin_amdgcn_exp2f(fmaf(sc[2 * mm + 1][j], factor, bias));
           }
+        // sums of the (rounded) probabilities: one more row tile of V^T, all ones
+        const half_t one = (half_t)1.f;
+        const half8_t ones = half8_t{one, one, one, one, one, one, one, one};
+        l4 = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pt[0], l4, 0, 0, 0);
+        l4 = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pt[1], l4, 0, 0, 0);
         // O^T += V^T P^T
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          half2_t vs[8];
-          *(u32x4*)&vs[0] = *(const u32x4*)(scales + b * 64 + g * 16);
-          *(u32x4*)&vs[4] = *(const u32x4*)(scales + b * 64 + g * 16 + 8);
+          const u32x4 s0 = *(const u32x4*)(scales + b * 64 + g * 16), s1 = *(const u32x4*)(scales + b * 64 + g * 16 + 8);
+          const uint32_t vsc[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             typedef int v2i __attribute__((ext_vector_type(2)));
@@ -211,14 +271,14 @@ __global__ __launch_bounds__(64 * WAVES) void attn_split_kernel(AttnArgs a) {
             for (int mm = 0; mm < 2; ++mm) {
               const H2x4 u = unpack8((uint32_t)w[mm]);
               o[2 * b + t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                  operand(u.v[0] * vs[4 * mm], u.v[1] * vs[4 * mm + 1], u.v[2] * vs[4 * mm + 2],
-                          u.v[3] * vs[4 * mm + 3]),
+                  operand(u.v[0] * as_h2(vsc[4 * mm]), u.v[1] * as_h2(vsc[4 * mm + 1]),
+                          u.v[2] * as_h2(vsc[4 * mm + 2]), u.v[3] * as_h2(vsc[4 * mm + 3])),
                   pt[mm], o[2 * b + t], 0, 0, 0);
             }
           }
         }
       }
-      l = groups_sum(l);
+      float l = l4[0];
 
       // merge: waves 2, 3 into 0, 1, then 1 into 0
 #pragma unroll
