@@ -28,12 +28,15 @@ namespace {
 constexpr int WAVES = 4;
 constexpr int STEP = 64;  // keys of one step
 
-// LDS of one wave: 64 rows of codes and their scales.  Row strides are odd
-// multiples of 16 bytes, which puts a lane group's 16 rows on distinct banks.
+// LDS of one wave: a step's rows of codes and their scales, keys and values.
+// Row strides are odd multiples of 16 bytes, which puts 16 neighbouring rows
+// on distinct banks.  Wide heads use one place for both, one after the other.
 template <int NB>
 struct Stage {
+  static constexpr bool SHARED = NB > 5;
   static constexpr int ROW = 16 * (NB | 1);
-  static constexpr int BYTES = STEP * ROW + STEP * NB * 2;
+  static constexpr int ONE = STEP * ROW + STEP * NB * 2;  // rows, then scales [block][64]
+  static constexpr int BYTES = SHARED ? ONE : 2 * ONE;
 };
 // LDS to hand one wave's sums to another: O^T [d][16], then maximum and sum
 template <int NB>
@@ -78,8 +81,8 @@ template <int NB>
 __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnArgs a) {
   constexpr int D = 32 * NB;
   constexpr int DT = D / 16;  // 16-value tiles of O^T
-  // 16-key groups of V are whole or half waves of 16-byte pieces: which group
-  // a load belongs to is then the same for all lanes
+  // 16-key groups are whole numbers of 16-byte pieces to a load of the wave:
+  // which group a load belongs to is then the same for all lanes
   constexpr bool WHOLE = NB % 4 == 0;
   // K scales of a lane: one where its quarter row lies inside a block, one per
   // block where it covers whole ones, else one per dword
@@ -120,15 +123,16 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
       const int steps = (keys.end - keys.lo + STEP - 1) / STEP;
       const int st0 = (int)((int64_t)steps * split / n_split), st1 = (int)((int64_t)steps * (split + 1) / n_split);
 
-      uint8_t* codes = lds + wave * Stage<NB>::BYTES;
-      uint16_t* scales = (uint16_t*)(codes + STEP * Stage<NB>::ROW);
-      const int32_t* pages = a.table + (int64_t)s * a.width;
+      uint8_t* kcodes = lds + wave * Stage<NB>::BYTES;
+      uint8_t* vcodes = kcodes + (Stage<NB>::SHARED ? 0 : Stage<NB>::ONE);
+      uint16_t* kscales = (uint16_t*)(kcodes + STEP * Stage<NB>::ROW);
+      uint16_t* vscales = (uint16_t*)(vcodes + STEP * Stage<NB>::ROW);
+      // read only here, so scalar loads may fetch it
+      const auto* pages = (const __attribute__((address_space(4))) int32_t*)(a.table + (int64_t)s * a.width);
 
       // registers of the step in flight
-      uint32_t kw[4][NB];
-      uint16_t ks[4][KS];
-      u32x4 vw[NB];
-      uint16_t vs[NB];
+      u32x4 kw[NB], vw[NB];
+      uint32_t ks[(NB + 1) / 2], vs[(NB + 1) / 2];
       const auto page_ids = [&](int st, int (&ids)[4]) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -136,28 +140,47 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
           ids[i] = st < st1 && k < keys.end ? pages[k >> a.page_shift] : -1;
         }
       };
-      const auto load_k = [&](const Groups& gr) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          load_dwords<NB>(a.kc + gr.codes[i] + (uint32_t)(col * (D / 2) + g * (D / 8)), kw[i]);
-#pragma unroll
-          for (int j = 0; j < KS; ++j) {
-            // dword j of quarter g lies in block (g NB + j) / 4
-            const uint32_t b = KS == NB ? (g * NB + j) >> 2 : KS == 2 ? 2 * g + j : (g * NB) >> 2;
-            ks[i][j] = (uint16_t)ld_u16(a.kc + gr.scales[i] + (uint32_t)(col * (D / 16) + 2 * b));
-          }
-        }
-      };
-      const auto load_v = [&](const Groups& gr) {
+      // codes in 16-byte pieces, lanes on consecutive ones; scales a lane to a key
+      const auto load_rows = [&](const uint8_t* cache, const Groups& gr, u32x4 (&w)[NB], uint32_t (&sc)[(NB + 1) / 2]) {
 #pragma unroll
         for (int i = 0; i < NB; ++i) {
           const int piece = i * 64 + lane, key = piece / NB, b = piece % NB;
-          const int64_t at = WHOLE ? gr.codes[i / (NB / 4 > 0 ? NB / 4 : 1)] : pick4(gr.codes, key >> 4);
-          vw[i] = ld_16B(a.vc + at + (uint32_t)((key & 15) * (D / 2) + 16 * b));
+          const int64_t at = WHOLE ? gr.codes[4 * i / NB] : pick4(gr.codes, key >> 4);
+          w[i] = ld_16B(cache + at + (uint32_t)((key & 15) * (D / 2) + 16 * b));
         }
-        const uint8_t* sp = a.vc + pick4(gr.scales, g) + (uint32_t)(col * (D / 16));
+        const uint8_t* sp = cache + pick4(gr.scales, g) + (uint32_t)(col * (D / 16));
+        if constexpr (NB % 2 == 0) {
+          load_dwords<NB / 2>(sp, sc);
+        } else {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) vs[b] = (uint16_t)ld_u16(sp + 2 * b);
+          for (int b = 0; b < NB; b += 2) sc[b / 2] = ld_u16(sp + 2 * b) | (b + 1 < NB ? ld_u16(sp + 2 * b + 2) << 16 : 0u);
+        }
+      };
+      // K: row of key k at k, scales [block][key % 16][key / 16], a lane's four
+      // tiles side by side
+      const auto stage_k = [&]() {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int piece = i * 64 + lane;
+          *(u32x4*)(kcodes + (piece / NB) * Stage<NB>::ROW + 16 * (piece % NB)) = kw[i];
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) kscales[b * 64 + col * 4 + g] = (uint16_t)(ks[b / 2] >> (16 * (b & 1)));
+      };
+      // V: row of key 16 i + 4 c + j at 16 c + 4 i + j, so that lane group c's
+      // keys lie together; scales in the order of the operands
+      const auto stage_v = [&](int base, uint32_t ok) {
+#pragma unroll
+        for (int i = 0; i < NB; ++i) {
+          const int piece = i * 64 + lane, key = piece / NB, b = piece % NB;
+          const int lr = ((key >> 2) & 3) * 16 + (key >> 4) * 4 + (key & 3);
+          *(u32x4*)(vcodes + lr * Stage<NB>::ROW + 16 * b) = vw[i];
+        }
+        // bytes behind the last key are anything, NaN included: their values enter as 0 * code
+        const bool good = ((ok >> g) & 1u) && base + lane < keys.end;
+        const int pos = ((lane >> 2) & 3) * 16 + (g >> 1) * 8 + (lane & 3) * 2 + (g & 1);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) vscales[b * 64 + pos] = (uint16_t)((good ? vs[b / 2] : 0u) >> (16 * (b & 1)));
       };
 
       int ids[4], ids_next[4];
@@ -177,47 +200,52 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
 
       Groups gr = groups_of<D>(a, ids, keys.lo + (st0 + wave) * STEP, keys.end, h);
       if (st0 + wave < st1) {
-        load_k(gr);
-        load_v(gr);
+        load_rows(a.kc, gr, kw, ks);
+        load_rows(a.vc, gr, vw, vs);
       }
       for (int st = st0 + wave; st < st1; st += WAVES) {
         const int base = keys.lo + st * STEP;
         const uint32_t ok = gr.ok;
         const bool more = st + WAVES < st1;
-        // V into LDS: 16-byte pieces of codes, the row of key 16 i + 4 c + j at 16 c + 4 i + j, so that
-        // lane group c's keys lie together; scales in the order of the operands
-#pragma unroll
-        for (int i = 0; i < NB; ++i) {
-          const int piece = i * 64 + lane, key = piece / NB, b = piece % NB;
-          const int lr = ((key >> 2) & 3) * 16 + (key >> 4) * 4 + (key & 3);
-          *(u32x4*)(codes + lr * Stage<NB>::ROW + 16 * b) = vw[i];
-        }
-        {
-          // bytes behind the last key are anything, NaN included: their values enter as 0 * code
-          const bool good = ((ok >> g) & 1u) && base + lane < keys.end;
-          const int pos = ((lane >> 2) & 3) * 16 + (g >> 1) * 8 + (lane & 3) * 2 + (g & 1);
-#pragma unroll
-          for (int b = 0; b < NB; ++b) scales[b * 64 + pos] = good ? vs[b] : (uint16_t)0;
-        }
-        // the next step's addresses; its V goes into the registers just emptied
+        // into LDS; the registers take the next step at once
+        stage_k();
+        if constexpr (!Stage<NB>::SHARED) stage_v(base, ok);
         gr = groups_of<D>(a, ids_next, base + WAVES * STEP, keys.end, h);
-        if (more) load_v(gr);
+        if (more) {
+          load_rows(a.kc, gr, kw, ks);
+          if constexpr (!Stage<NB>::SHARED) load_rows(a.vc, gr, vw, vs);
+        }
         page_ids(st + 2 * WAVES, ids_next);
-        // S^T
+        // S^T; dword j of quarter g lies in block (g NB + j) / 4
         float4_t sc[4];
+        {
+          uint32_t sc4[KS][2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sc[i] = float4_t{0, 0, 0, 0};
+          for (int j = 0; j < KS; ++j) {
+            const int b = KS == NB ? (g * NB + j) >> 2 : KS == 2 ? 2 * g + j : (g * NB) >> 2;
+            const u32x2 v = *(const u32x2*)(kscales + b * 64 + col * 4);
+            sc4[j][0] = v.x; sc4[j][1] = v.y;
+          }
 #pragma unroll
-          for (int j = 0; j < NB; ++j) {
-            const half_t v = __builtin_bit_cast(half_t, ks[i][KS == NB ? j : KS == 2 ? j / 4 : 0]);
-            const half2_t kv = half2_t{v, v};
-            const H2x4 u = unpack8(kw[i][j]);
-            sc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                operand(u.v[0] * kv, u.v[1] * kv, u.v[2] * kv, u.v[3] * kv), q[j], sc[i], 0, 0, 0);
+          for (int i = 0; i < 4; ++i) {
+            uint32_t w[NB];
+            load_dwords<NB>(kcodes + (16 * i + col) * Stage<NB>::ROW + g * (D / 8), w);
+            sc[i] = float4_t{0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+              const half2_t pair = as_h2(sc4[KS == NB ? j : KS == 2 ? j / 4 : 0][i >> 1]);
+              const half_t v = i & 1 ? pair.y : pair.x;
+              const half2_t kv = half2_t{v, v};
+              const H2x4 u = unpack8(w[j]);
+              sc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                  operand(u.v[0] * kv, u.v[1] * kv, u.v[2] * kv, u.v[3] * kv), q[j], sc[i], 0, 0, 0);
+            }
           }
         }
-        if (more) load_k(gr);
+        if constexpr (Stage<NB>::SHARED) {
+          stage_v(base, ok);
+          if (more) load_rows(a.vc, gr, vw, vs);
+        }
         if (base + STEP - 1 > p0 || (a.window > 0 && base <= p1 - a.window) || ok != 15u) {
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -259,14 +287,14 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
         // O^T += V^T P^T
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
-          const u32x4 s0 = *(const u32x4*)(scales + b * 64 + g * 16), s1 = *(const u32x4*)(scales + b * 64 + g * 16 + 8);
+          const u32x4 s0 = *(const u32x4*)(vscales + b * 64 + g * 16), s1 = *(const u32x4*)(vscales + b * 64 + g * 16 + 8);
           const uint32_t vsc[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
             typedef int v2i __attribute__((ext_vector_type(2)));
             typedef v2i __attribute__((address_space(3))) lds_v2i;
             const v2i w = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
-                (lds_v2i*)(codes + (g * 16 + col) * Stage<NB>::ROW + 16 * b + 8 * t));
+                (lds_v2i*)(vcodes + (g * 16 + col) * Stage<NB>::ROW + 16 * b + 8 * t));
 #pragma unroll
             for (int mm = 0; mm < 2; ++mm) {
               const H2x4 u = unpack8((uint32_t)w[mm]);
