@@ -704,7 +704,8 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
   a.splits = plan.splits;
   a.chunk = plan.chunk;
   a.one_tile = plan.one_tile;
-  return hip_status(op, kq::launch_kv_attention(a, (hipStream_t)stream));
+  a.few_rows = plan.few_rows;
+  return hip_status(op, kq::launch_kv_attention(a, plan, (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -418,14 +418,18 @@ struct AttnArgs {
   int splits;      // most workgroups that share one row's keys
   int chunk;       // keys a workgroup takes before another one is worth it
   int one_tile;    // a request's rows fit one 16-row tile: tile index = request
+  int few_rows;    // requests of at most so many rows take 16-row tiles, others prompt tiles
 };
 // How a call's work is split, from its host-known sizes alone.
 struct AttnPlan {
-  int splits, chunk, one_tile;
-  int64_t bytes;   // workspace
+  int splits, chunk, one_tile, few_rows;
+  int64_t few_tiles, many_tiles;  // tiles of 16 rows, of a prompt tile's rows (bounds; 0: that kernel does not run)
+  int64_t bytes;                  // workspace
 };
 AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
                    int64_t max_kv);
-hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t s);
+hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
+int attn_prompt_rows(int64_t d);  // rows of a prompt tile
+hipError_t launch_attn_prompt(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
 
 }  // namespace kq

@@ -46,16 +46,21 @@ __device__ __forceinline__ int split_count(const AttnArgs& a, const Keys& k) {
   return s < a.splits ? s : a.splits;
 }
 
-// Request and tile index inside it of tile `tile`, the tiles of all requests
-// numbered one after the other (`rows` rows to a tile); false past the last.
-// Every wave scans the requests 64 at a time.
-__device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, int rows, int& seq, int& sub) {
+// Request and tile index inside it of tile `tile`, the tiles of the requests
+// with more than `above` and at most `most` rows numbered one after the other
+// (`rows` rows to a tile); false past the last.  Every wave scans the requests
+// 64 at a time.
+__device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, int rows, int above, int most, int& seq,
+                                          int& sub) {
   const int lane = threadIdx.x & 63;
   int64_t before = 0;
   for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
     const int s = s0 + lane;
     int64_t t = 0;
-    if (s < a.n_seqs) t = ((int64_t)load_seq(a, s).n * a.group + rows - 1) / rows;
+    if (s < a.n_seqs) {
+      const int r = load_seq(a, s).n * a.group;
+      t = r > above && r <= most ? (r + rows - 1) / rows : 0;
+    }
     int64_t incl = t;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -67,11 +72,43 @@ __device__ __forceinline__ bool find_tile(const AttnArgs& a, int tile, int rows,
       const int l = __builtin_ctzll(hit);
       seq = s0 + l;
       sub = (int)(tile - before - (__shfl(incl, l, 64) - __shfl(t, l, 64)));
+      seq = __builtin_amdgcn_readfirstlane(seq);
+      sub = __builtin_amdgcn_readfirstlane(sub);
       return true;
     }
     before += __shfl(incl, 63, 64);
   }
   return false;
+}
+
+// A step's four 16-key groups: byte offsets of their codes and scales in the
+// caches, and which of them are there (a group past the last key or without a
+// page of the cache reads page 0 and is left out).  Uniform over the wave.
+struct Groups {
+  int64_t codes[4], scales[4];
+  uint32_t ok;  // bit i
+};
+template <int D>
+__device__ __forceinline__ Groups groups_of(const AttnArgs& a, const int (&ids)[4], int base, int end, int h) {
+  Groups r;
+  r.ok = 0;
+  const int mask = (1 << a.page_shift) - 1;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int k = base + 16 * i;
+    const bool ok = k < end && ids[i] >= 0 && ids[i] < a.pages;
+    const int64_t at = ((int64_t)(ok ? ids[i] : 0) * a.hkv + h) * a.page_head_bytes;
+    r.codes[i] = at + (int64_t)(k & mask) * (D / 2);
+    r.scales[i] = at + ((int64_t)(D / 2) << a.page_shift) + (int64_t)(k & mask) * (D / 16);
+    r.ok |= ok ? 1u << i : 0u;
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ T pick4(const T (&v)[4], int i) {
+  const T lo = i & 1 ? v[1] : v[0], hi = i & 1 ? v[3] : v[2];
+  return i & 2 ? hi : lo;
 }
 
 // N consecutive dwords from a 4-byte aligned address (16- or 8-byte loads
@@ -134,13 +171,13 @@ __device__ __forceinline__ float groups_sum(float v) {
 }
 
 // Query operands of one row for NB = d / 32 matrix steps: lane group g of
-// step s holds values g * d / 4 + 8 s .. + 7.  bfloat16 values are scaled by
+// step s holds eight values from g * GS + s * SS on.  bfloat16 values are scaled by
 // a power of two that brings the row's largest near 2^14, which float16
 // holds exactly down to 2^-28 of the largest; `factor` takes that power of two
 // back out of the products, times scale * log2(e).  A negative scale is put
 // into the queries' signs, so that factor > 0 and the largest product has the
 // largest weight.
-template <int NB>
+template <int NB, int GS, int SS>
 __device__ __forceinline__ void load_query(const AttnArgs& a, const void* row, bool live, int g, half8_t (&q)[NB],
                                            float& factor) {
   const float log2e = 1.4426950408889634f;
@@ -151,7 +188,7 @@ __device__ __forceinline__ void load_query(const AttnArgs& a, const void* row, b
     float v[NB][8], amax = 0.f;
 #pragma unroll
     for (int s = 0; s < NB; ++s) {
-      const b8 r = live ? *(const b8*)((const __bf16*)row + g * (8 * NB) + 8 * s) : b8{};
+      const b8 r = live ? *(const b8*)((const __bf16*)row + g * GS + s * SS) : b8{};
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         v[s][i] = (float)r[i];
@@ -174,7 +211,7 @@ __device__ __forceinline__ void load_query(const AttnArgs& a, const void* row, b
   } else {
 #pragma unroll
     for (int s = 0; s < NB; ++s) {
-      half8_t h = live ? *(const half8_t*)((const half_t*)row + g * (8 * NB) + 8 * s) : half8_t{};
+      half8_t h = live ? *(const half8_t*)((const half_t*)row + g * GS + s * SS) : half8_t{};
       if (neg) h = -h;
       q[s] = query_order(h);
     }

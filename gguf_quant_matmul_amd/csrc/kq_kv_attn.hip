@@ -47,36 +47,6 @@ constexpr int lds_bytes() {
   return s > m ? s : m;
 }
 
-// A step's four 16-key groups: byte offsets of their codes and scales in the
-// caches, and which of them are there (a group past the last key or without a
-// page of the cache reads page 0 and is left out).  Uniform over the wave.
-struct Groups {
-  int64_t codes[4], scales[4];
-  uint32_t ok;  // bit i
-};
-template <int D>
-__device__ __forceinline__ Groups groups_of(const AttnArgs& a, const int (&ids)[4], int base, int end, int h) {
-  Groups r;
-  r.ok = 0;
-  const int mask = (1 << a.page_shift) - 1;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int k = base + 16 * i;
-    const bool ok = k < end && ids[i] >= 0 && ids[i] < a.pages;
-    const int64_t at = ((int64_t)(ok ? ids[i] : 0) * a.hkv + h) * a.page_head_bytes;
-    r.codes[i] = at + (int64_t)(k & mask) * (D / 2);
-    r.scales[i] = at + ((int64_t)(D / 2) << a.page_shift) + (int64_t)(k & mask) * (D / 16);
-    r.ok |= ok ? 1u << i : 0u;
-  }
-  return r;
-}
-
-template <typename T>
-__device__ __forceinline__ T pick4(const T (&v)[4], int i) {
-  const T lo = i & 1 ? v[1] : v[0], hi = i & 1 ? v[3] : v[2];
-  return i & 2 ? hi : lo;
-}
-
 template <int NB>
 __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel(AttnArgs a) {
   constexpr int D = 32 * NB;
@@ -94,9 +64,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
 
   int s = tile, sub = 0;
   if (!a.one_tile) {
-    if (!find_tile(a, tile, 16, s, sub)) return;
-    s = __builtin_amdgcn_readfirstlane(s);
-    sub = __builtin_amdgcn_readfirstlane(sub);
+    if (!find_tile(a, tile, 16, 0, a.few_rows, s, sub)) return;
   }
   const Seq sq = load_seq(a, s);
   const int rows = sq.n * a.group;
@@ -188,7 +156,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
       page_ids(st0 + wave + WAVES, ids_next);
       half8_t q[NB];
       float factor;
-      load_query<NB>(a, (const uint16_t*)a.q + (int64_t)tok * a.q_stride + (int64_t)head * D, live, g, q, factor);
+      load_query<NB, 8 * NB, 8>(a, (const uint16_t*)a.q + (int64_t)tok * a.q_stride + (int64_t)head * D, live, g, q, factor);
       // probabilities may reach 2^8 before the sums are brought to a new maximum
       const float slack = 8.f / factor;
 
@@ -388,14 +356,26 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 
 }  // namespace
 
+// rows of a request up to which its own 16-row tiles beat a share of a prompt
+// tile, when a batch holds both
+constexpr int FEW_ROWS = 32;
+
 AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
                    int64_t max_kv) {
   AttnPlan p;
-  const int64_t group = q_heads / kv_heads;
-  p.one_tile = max_new * group <= 16;
-  const int64_t tiles = p.one_tile ? n_seqs : (tokens * group) / 16 + n_seqs;
+  const int64_t group = q_heads / kv_heads, most = (max_new < tokens ? max_new : tokens) * group;
+  p.one_tile = most <= 16;
+  // Which kernels run.  Requests of few rows only: 16-row tiles.  One request
+  // of many rows: prompt tiles.  Else each request goes where its rows fit.
+  p.few_rows = most <= 64 ? 0x7FFFFFFF : n_seqs == 1 ? 0 : FEW_ROWS;
+  const int64_t all = tokens * group;
+  p.few_tiles = p.one_tile ? n_seqs : p.few_rows == 0 ? 0 : all / 16 + n_seqs;
+  if (p.few_rows == FEW_ROWS && p.few_tiles > n_seqs * (FEW_ROWS / 16)) p.few_tiles = n_seqs * (FEW_ROWS / 16);
+  const int tile = attn_prompt_rows(d);
+  p.many_tiles = p.few_rows == 0x7FFFFFFF ? 0 : all / tile + n_seqs;
   // enough workgroups for three on each of 256 CUs, none with fewer than 256
   // keys; never more than 4096 keys to one, whose length differs from others'
+  const int64_t tiles = p.many_tiles ? p.many_tiles : p.few_tiles;
   const int64_t want = (768 + tiles * kv_heads - 1) / (tiles * kv_heads);
   int64_t chunk = (max_kv + want - 1) / want;
   chunk = chunk < 256 ? 256 : chunk > 4096 ? 4096 : chunk;
@@ -406,21 +386,27 @@ AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_h
   return p;
 }
 
-hipError_t launch_kv_attention(const AttnArgs& a, hipStream_t s) {
-  const int64_t tiles = a.one_tile ? a.n_seqs : ((int64_t)a.tokens * a.group) / 16 + a.n_seqs;
-  const dim3 grid((unsigned)(tiles * a.hkv), (unsigned)a.splits), block(64 * WAVES);
-  const auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, s, a); };
-  switch (a.d / 32) {
-    case 1: go(attn_split_kernel<1>); break;
-    case 2: go(attn_split_kernel<2>); break;
-    case 3: go(attn_split_kernel<3>); break;
-    case 4: go(attn_split_kernel<4>); break;
-    case 5: go(attn_split_kernel<5>); break;
-    case 6: go(attn_split_kernel<6>); break;
-    case 7: go(attn_split_kernel<7>); break;
-    default: go(attn_split_kernel<8>); break;
+hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+  hipError_t e = hipSuccess;
+  if (p.many_tiles > 0) {
+    e = launch_attn_prompt(a, p, s);
+    if (e != hipSuccess) return e;
   }
-  hipError_t e = hipGetLastError();
+  if (p.few_tiles > 0) {
+    const dim3 grid((unsigned)(p.few_tiles * a.hkv), (unsigned)a.splits), block(64 * WAVES);
+    const auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, s, a); };
+    switch (a.d / 32) {
+      case 1: go(attn_split_kernel<1>); break;
+      case 2: go(attn_split_kernel<2>); break;
+      case 3: go(attn_split_kernel<3>); break;
+      case 4: go(attn_split_kernel<4>); break;
+      case 5: go(attn_split_kernel<5>); break;
+      case 6: go(attn_split_kernel<6>); break;
+      case 7: go(attn_split_kernel<7>); break;
+      default: go(attn_split_kernel<8>); break;
+    }
+    e = hipGetLastError();
+  }
   if (e != hipSuccess || a.splits == 1) return e;
   const int64_t n = (int64_t)a.tokens * a.hq * (a.d / 4);
   hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
