@@ -159,15 +159,20 @@ __device__ __forceinline__ half8_t query_order(half8_t v) {
   return __builtin_shufflevector(v, v, 0, 4, 1, 5, 2, 6, 3, 7);
 }
 
-// Maximum or sum over the four lane groups that hold one query's keys
-// (lanes l, l ^ 16, l ^ 32, l ^ 48).
+// Maximum over the four lane groups that hold one query's keys (lanes l,
+// l ^ 16, l ^ 32, l ^ 48): two row swaps, which stay in the vector unit where
+// a shuffle would go through LDS.
 __device__ __forceinline__ float groups_max(float v) {
-  v = fmaxf(v, __shfl_xor(v, 16, 64));
-  return fmaxf(v, __shfl_xor(v, 32, 64));
-}
-__device__ __forceinline__ float groups_sum(float v) {
-  v += __shfl_xor(v, 16, 64);
-  return v + __shfl_xor(v, 32, 64);
+  uint32_t x = __builtin_bit_cast(uint32_t, v);
+  auto r = __builtin_amdgcn_permlane32_swap(x, x, false, false);
+  // copies: __builtin_bit_cast of a vector's element reads element 0
+  uint32_t lo = r[0], hi = r[1];
+  v = fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
+  x = __builtin_bit_cast(uint32_t, v);
+  r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  lo = r[0];
+  hi = r[1];
+  return fmaxf(__builtin_bit_cast(float, lo), __builtin_bit_cast(float, hi));
 }
 
 // Query operands of one row for NB = d / 32 matrix steps: lane group g of

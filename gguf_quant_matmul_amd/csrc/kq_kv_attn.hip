@@ -373,12 +373,21 @@ AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_h
   if (p.few_rows == FEW_ROWS && p.few_tiles > n_seqs * (FEW_ROWS / 16)) p.few_tiles = n_seqs * (FEW_ROWS / 16);
   const int tile = attn_prompt_rows(d);
   p.many_tiles = p.few_rows == 0x7FFFFFFF ? 0 : all / tile + n_seqs;
-  // enough workgroups for three on each of 256 CUs, none with fewer than 256
-  // keys; never more than 4096 keys to one, whose length differs from others'
-  const int64_t tiles = p.many_tiles ? p.many_tiles : p.few_tiles;
-  const int64_t want = (768 + tiles * kv_heads - 1) / (tiles * kv_heads);
-  int64_t chunk = (max_kv + want - 1) / want;
-  chunk = chunk < 256 ? 256 : chunk > 4096 ? 4096 : chunk;
+  int64_t chunk;
+  if (p.many_tiles > 0) {
+    // prompt tiles: one workgroup to a CU.  Split rows write and read float32
+    // sums, which costs as much as some 500 keys, so only where tiles alone
+    // leave a good part of the CUs idle, and 1024 keys at least
+    const int64_t wgs = p.many_tiles * kv_heads, want = (256 + wgs - 1) / wgs;
+    chunk = wgs >= 192 ? max_kv : (max_kv + want - 1) / want;
+    chunk = chunk < 1024 ? 1024 : chunk;
+  } else {
+    // enough workgroups for three on each of 256 CUs, none with fewer than 256
+    // keys; never more than 4096 keys to one, whose length differs from others'
+    const int64_t wgs = p.few_tiles * kv_heads, want = (768 + wgs - 1) / wgs;
+    chunk = (max_kv + want - 1) / want;
+    chunk = chunk < 256 ? 256 : chunk > 4096 ? 4096 : chunk;
+  }
   p.chunk = (int)((chunk + 63) / 64 * 64);
   p.splits = (int)((max_kv + p.chunk - 1) / p.chunk);
   p.splits = p.splits < 1 ? 1 : p.splits > 256 ? 256 : p.splits;

@@ -2,9 +2,17 @@
 // as kq_kv_attn.hip, but a workgroup's eight waves share each 64-key step.  A
 // wave takes C 16-row tiles of its own; the step's keys and values are
 // unpacked to float16 once, by all waves together, into LDS in the order of
-// the matrix operands, and every wave reads them from there.  Two steps'
-// buffers: while one is multiplied the next is unpacked, and the one after
-// that is on its way from memory; one barrier a step.
+// the matrix operands, and every wave reads them from there.
+//
+// A step is K Q^T (matrix cores), the softmax (vector unit), V^T P^T (matrix
+// cores) and the unpacking of a coming step (vector unit).  Two waves share a
+// SIMD, and with one barrier a step at the same place they would want the
+// same unit at the same time.  So the second four waves meet the barrier
+// after their K Q^T instead of at the end of the step: in the round between
+// two barriers they run softmax, V^T P^T and unpacking of one step, then
+// K Q^T of the next, beside the first four's K Q^T, softmax, V^T P^T.  The
+// round of step r unpacks step r + 1 (two places for keys, three for values,
+// of which V(r - 1) and V(r) are being read) and fetches the one after.
 #include "kq_kv_attn.h"
 
 namespace kq {
@@ -20,7 +28,11 @@ struct Prompt {
   static constexpr int UNITS = (2 * NB + PW - 1) / PW;  // unpacking units of a wave: 64 pieces of 32 values
   static constexpr int HALF = STEP * 32 * NB * 2;       // float16 keys (or values) of a step
   static constexpr int RAW = STEP * 16 + STEP * 2;      // one block's codes and scales, on the way to the transposing read
-  static constexpr int LDS = 4 * HALF + NB * RAW;
+  // three places for values where 160 KB hold them; else two, and all waves
+  // meet at the end of the step
+  static constexpr bool OFFSET = 5 * HALF + NB * RAW <= 160 * 1024;
+  static constexpr int VB = OFFSET ? 3 : 2;
+  static constexpr int LDS = (2 + VB) * HALF + NB * RAW;
 };
 
 template <int NB>
@@ -70,46 +82,78 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
   const int steps = (keys.end - keys.lo + STEP - 1) / STEP;
   const int st0 = n_split ? (int)((int64_t)steps * split / n_split) : 0;
   const int st1 = n_split ? (int)((int64_t)steps * (split + 1) / n_split) : 0;
-  const auto* pages = (const __attribute__((address_space(4))) int32_t*)(a.table + (int64_t)s * a.width);
+  const int32_t* pages = a.table + (int64_t)s * a.width;
 
-  // the pieces of a step that this wave unpacks: unit u < NB is 64 pieces of
-  // keys (lanes on consecutive pieces), unit NB + b block b of 64 values rows
+  // Unpacking is shared out in units: unit u < NB is 64 pieces (32 values) of
+  // keys, lanes on consecutive pieces; unit NB + b block b of 64 value rows, a
+  // lane to a row.  Everything is asked for a step or more before it is
+  // needed: page ids, then codes and scales at the addresses they give, then
+  // (values) the write to LDS that the transposing read wants.
+  const int page_mask = (1 << a.page_shift) - 1;
+  const uint64_t page_bytes = (uint64_t)a.hkv * (uint64_t)a.page_head_bytes;
+  // the page id of key `lane` of a step (any id for keys behind the last)
+  const auto page_id = [&](int st) {
+    const int k = keys.lo + st * STEP + lane;
+    return pages[(k < keys.end ? k : keys.end - 1) >> a.page_shift];
+  };
+  // ... -1 where there is no such key or no such page
+  const auto checked = [&](int st, int id) {
+    return keys.lo + st * STEP + lane < keys.end && (uint32_t)id < (uint32_t)a.pages ? id : -1;
+  };
+  // offsets of the codes and scales of a row in the cache; page 0 for id -1
+  const auto row_at = [&](int key, int id, uint64_t& codes, uint64_t& scales) {
+    const uint64_t at = (uint64_t)(uint32_t)(id < 0 ? 0 : id) * page_bytes + (uint64_t)h * (uint64_t)a.page_head_bytes;
+    const uint32_t row = (uint32_t)(key & page_mask);
+    codes = at + row * (uint32_t)(D / 2);
+    scales = at + ((uint32_t)(D / 2) << a.page_shift) + row * (uint32_t)(D / 16);
+  };
   u32x4 raw[T::UNITS];
   uint16_t rsc[T::UNITS];
-  const auto fetch = [&](int st) {
-    int ids[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = keys.lo + st * STEP + 16 * i;
-      ids[i] = k < keys.end ? pages[k >> a.page_shift] : -1;
-    }
-    const int base = keys.lo + st * STEP;
-    const Groups gr = groups_of<D>(a, ids, base, keys.end, h);
+  const auto fetch_k = [&](int st, int id) {
 #pragma unroll
     for (int k = 0; k < T::UNITS; ++k) {
       const int u = wave + PW * k;
-      if (u < NB) {
-        const int piece = u * 64 + lane, key = piece / NB, b = piece % NB;
-        raw[k] = ld_16B(a.kc + pick4(gr.codes, key >> 4) + (uint32_t)((key & 15) * (D / 2) + 16 * b));
-        rsc[k] = (uint16_t)ld_u16(a.kc + pick4(gr.scales, key >> 4) + (uint32_t)((key & 15) * (D / 16) + 2 * b));
-      } else if (u < 2 * NB) {
-        const int b = u - NB;
-        raw[k] = ld_16B(a.vc + pick4(gr.codes, g) + (uint32_t)(col * (D / 2) + 16 * b));
-        const uint32_t sc = ld_u16(a.vc + pick4(gr.scales, g) + (uint32_t)(col * (D / 16) + 2 * b));
-        // bytes behind the last key are anything, NaN included: their values enter as 0 * code
-        rsc[k] = ((gr.ok >> g) & 1u) && base + lane < keys.end ? (uint16_t)sc : (uint16_t)0;
-      }
+      if (u >= NB) continue;
+      const int piece = u * 64 + lane, key = piece / NB, b = piece % NB;
+      uint64_t codes, scales;
+      row_at(keys.lo + st * STEP + key, __shfl(id, key, 64), codes, scales);
+      raw[k] = ld_16B(a.kc + codes + 16 * b);
+      rsc[k] = (uint16_t)ld_u16(a.kc + scales + 2 * b);
     }
-    return gr.ok;
   };
-  const auto unpack = [&](int buf) {
-    uint8_t* kbuf = lds + buf * 2 * T::HALF;
-    uint8_t* vbuf = kbuf + T::HALF;
+  uint32_t there = 0;  // all ones where the lane's value row is a key
+  const auto fetch_v = [&](int st, int id) {
 #pragma unroll
     for (int k = 0; k < T::UNITS; ++k) {
       const int u = wave + PW * k;
-      const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+      if (u < NB || u >= 2 * NB) continue;
+      uint64_t codes, scales;
+      row_at(keys.lo + st * STEP + lane, id, codes, scales);
+      raw[k] = ld_16B(a.vc + codes + 16 * (u - NB));
+      rsc[k] = (uint16_t)ld_u16(a.vc + scales + 2 * (u - NB));
+    }
+    there = id >= 0 ? 0xFFFFu : 0u;
+  };
+  const auto stage_v = [&]() {
+#pragma unroll
+    for (int k = 0; k < T::UNITS; ++k) {
+      const int u = wave + PW * k;
+      if (u < NB || u >= 2 * NB) continue;
+      uint8_t* rows16 = lds + (2 + T::VB) * T::HALF + (u - NB) * T::RAW;  // this unit's own
+      uint16_t* scales = (uint16_t*)(rows16 + STEP * 16);
+      *(u32x4*)(rows16 + (((lane >> 2) & 3) * 16 + g * 4 + (lane & 3)) * 16) = raw[k];
+      // bytes behind the last key are anything, NaN included: their values enter as 0 * code
+      scales[((lane >> 2) & 3) * 16 + (g >> 1) * 8 + (lane & 3) * 2 + (g & 1)] = (uint16_t)(rsc[k] & there);
+    }
+  };
+  const auto unpack = [&](int kb, int vb) {
+    uint8_t* kbuf = lds + kb * T::HALF;
+    uint8_t* vbuf = lds + (2 + vb) * T::HALF;
+#pragma unroll
+    for (int k = 0; k < T::UNITS; ++k) {
+      const int u = wave + PW * k;
       if (u < NB) {
+        const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
         const int piece = u * 64 + lane, key = piece / NB, b = piece % NB;
         const half_t sc = __builtin_bit_cast(half_t, rsc[k]);
         const half2_t s2 = half2_t{sc, sc};
@@ -124,25 +168,25 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
         }
       } else if (u < 2 * NB) {
         const int b = u - NB;
-        uint8_t* rows16 = lds + 4 * T::HALF + b * T::RAW;  // this unit's own
-        uint16_t* scales = (uint16_t*)(rows16 + STEP * 16);
-        *(u32x4*)(rows16 + (((lane >> 2) & 3) * 16 + g * 4 + (lane & 3)) * 16) = raw[k];
-        scales[((lane >> 2) & 3) * 16 + (g >> 1) * 8 + (lane & 3) * 2 + (g & 1)] = rsc[k];
+        const uint8_t* rows16 = lds + (2 + T::VB) * T::HALF + b * T::RAW;
+        const uint16_t* scales = (const uint16_t*)(rows16 + STEP * 16);
         const u32x4 s0 = *(const u32x4*)(scales + g * 16), s1 = *(const u32x4*)(scales + g * 16 + 8);
         const uint32_t vsc[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        typedef int v2i __attribute__((ext_vector_type(2)));
+        typedef v2i __attribute__((address_space(3))) lds_v2i;
+        v2i v[2];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          typedef int v2i __attribute__((ext_vector_type(2)));
-          typedef v2i __attribute__((address_space(3))) lds_v2i;
-          const v2i v = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i*)(rows16 + (g * 16 + col) * 16 + 8 * t));
+        for (int t = 0; t < 2; ++t)
+          v[t] = __builtin_amdgcn_ds_read_tr4_b64_v2i32((lds_v2i*)(rows16 + (g * 16 + col) * 16 + 8 * t));
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int mm = 0; mm < 2; ++mm) {
-            const H2x4 x = unpack8((uint32_t)v[mm]);
+            const H2x4 x = unpack8((uint32_t)v[t][mm]);
             *(half8_t*)(vbuf + (((b * 2 + t) * 2 + mm) * 64 + lane) * 16) =
                 operand(x.v[0] * as_h2(vsc[4 * mm]), x.v[1] * as_h2(vsc[4 * mm + 1]), x.v[2] * as_h2(vsc[4 * mm + 2]),
                         x.v[3] * as_h2(vsc[4 * mm + 3]));
           }
-        }
       }
     }
   };
@@ -158,36 +202,84 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
     slack[c] = 8.f / factor[c];  // probabilities may reach 2^8 before the sums are brought to a new maximum
   }
 
-  uint32_t ok = 0, ok_next = 0;
-  if (st0 < st1) {
-    ok = fetch(st0);
-    unpack(0);
-    if (st0 + 1 < st1) ok_next = fetch(st0 + 1);
+  // operands of key group i, of block b of the values
+  const auto read_k = [&](const uint8_t* kbuf, int i, half8_t (&f)[NB]) {
+#pragma unroll
+    for (int j = 0; j < NB; ++j)
+      f[j] = *(const half8_t*)(kbuf + ((i * NB + j) * 64 + g * 16 + (col ^ ((j & 3) * 4))) * 16);
+  };
+  const auto read_v = [&](const uint8_t* vbuf, int b, half8_t (&f)[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) f[j] = *(const half8_t*)(vbuf + ((b * 4 + j) * 64 + lane) * 16);
+  };
+
+  const int late = T::OFFSET && wave >= PW / 2 ? 1 : 0;
+  const int steps_here = st1 - st0;
+  uint64_t oks = 0;  // which key groups have a page: four bits a step, the current one lowest
+  const auto group_bits = [&](int id) -> uint64_t {
+    const uint64_t m = __ballot(id >= 0);  // a group's first key tells for all of it
+    return (m & 1) | (m >> 15 & 2) | (m >> 30 & 4) | (m >> 45 & 8);
+  };
+  // ids of the steps whose keys, and whose values, are fetched next; ids on their way
+  int id_k = 0, id_v = 0, id_next = 0;
+  if (steps_here > 0) {
+    // (steps behind the last are fetched from page 0 and unpacked to places that nothing reads)
+    int id = checked(st0, page_id(st0));
+    id_k = checked(st0 + 1, page_id(st0 + 1));
+    id_v = checked(st0 + 2, page_id(st0 + 2));
+    id_next = page_id(st0 + 3);
+    oks = group_bits(id) | group_bits(id_k) << 4 | group_bits(id_v) << 8;
+    fetch_k(st0, id);
+    fetch_v(st0, id);
+    stage_v();
+    fetch_v(st0 + 1, id_k);
+    unpack(0, 0);
+    stage_v();
+    fetch_k(st0 + 1, id_k);
+    fetch_v(st0 + 2, id_v);
+    if (late) {
+      unpack(1, 1);
+      stage_v();
+      id_k = id_v;
+      id_v = checked(st0 + 3, id_next);
+      id_next = page_id(st0 + 4);
+      oks |= group_bits(id_v) << 12;
+      fetch_k(st0 + 2, id_k);
+      fetch_v(st0 + 3, id_v);
+    }
   }
   __syncthreads();
-  for (int st = st0; st < st1; ++st) {
-    const int buf = (st - st0) & 1, base = keys.lo + st * STEP;
-    uint32_t ok_after = 0;
-    if (st + 1 < st1) {
-      unpack(buf ^ 1);
-      if (st + 2 < st1) ok_after = fetch(st + 2);
-    }
-    if (base <= p1 && (a.window <= 0 || base + STEP - 1 > p0 - a.window)) {
-      const uint8_t* kbuf = lds + buf * 2 * T::HALF;
-      const uint8_t* vbuf = kbuf + T::HALF;
-      // S^T
-      float4_t sc[C][4];
+  int vb = 0;  // step n's place among the values
+  for (int n = 0; n < steps_here; ++n) {
+    const int base = keys.lo + (st0 + n) * STEP;
+    const uint32_t ok = (uint32_t)oks & 15u;
+    const bool active = base <= p1 && (a.window <= 0 || base + STEP - 1 > p0 - a.window);
+    // S^T; each group's operands are read while the group before is multiplied
+    // (the scheduling barriers keep that order)
+    float4_t sc[C][4];
+    if (active) {
+      const uint8_t* kbuf = lds + (n & 1) * T::HALF;
+      half8_t kf[2][NB];
+      read_k(kbuf, 0, kf[0]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        if (i < 3) read_k(kbuf, i + 1, kf[(i + 1) & 1]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int c = 0; c < C; ++c) sc[c][i] = float4_t{0, 0, 0, 0};
 #pragma unroll
-        for (int j = 0; j < NB; ++j) {
-          const half8_t kf = *(const half8_t*)(kbuf + ((i * NB + j) * 64 + g * 16 + (col ^ ((j & 3) * 4))) * 16);
+        for (int j = 0; j < NB; ++j)
 #pragma unroll
-          for (int c = 0; c < C; ++c) sc[c][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, q[c][j], sc[c][i], 0, 0, 0);
-        }
+          for (int c = 0; c < C; ++c)
+            sc[c][i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[i & 1][j], q[c][j], sc[c][i], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
       }
+    }
+    if (late) __syncthreads();
+    if (active) {
+      const uint8_t* vbuf = lds + (2 + vb) * T::HALF;
+      half8_t vf[2][4];
+      read_v(vbuf, 0, vf[0]);
       if (base + STEP - 1 > p0 || (a.window > 0 && base <= p1 - a.window) || ok != 15u) {
 #pragma unroll
         for (int c = 0; c < C; ++c)
@@ -231,19 +323,34 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
         l4[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pt[c][0], l4[c], 0, 0, 0);
         l4[c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(ones, pt[c][1], l4[c], 0, 0, 0);
       }
-      // O^T += V^T P^T
+      // O^T += V^T P^T, read ahead likewise
 #pragma unroll
-      for (int t = 0; t < DT; ++t)
+      for (int b = 0; b < NB; ++b) {
+        if (b + 1 < NB) read_v(vbuf, b + 1, vf[(b + 1) & 1]);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int mm = 0; mm < 2; ++mm) {
-          const half8_t vf = *(const half8_t*)(vbuf + ((t * 2 + mm) * 64 + lane) * 16);
+        for (int j = 0; j < 4; ++j)
 #pragma unroll
-          for (int c = 0; c < C; ++c) o[t][c] = __builtin_amdgcn_mfma_f32_16x16x32_f16(vf, pt[c][mm], o[t][c], 0, 0, 0);
-        }
+          for (int c = 0; c < C; ++c)
+            o[2 * b + (j >> 1)][c] =
+                __builtin_amdgcn_mfma_f32_16x16x32_f16(vf[b & 1][j], pt[c][j & 1], o[2 * b + (j >> 1)][c], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    ok = ok_next;
-    ok_next = ok_after;
-    __syncthreads();
+    // the round's step + 1 is unpacked; its values were staged the round before
+    const int round = n + late;
+    int vn = vb + 1 + late;
+    vn = vn >= T::VB ? vn - T::VB : vn;
+    unpack((round + 1) & 1, vn);
+    stage_v();
+    id_k = id_v;
+    id_v = checked(st0 + round + 3, id_next);
+    id_next = page_id(st0 + round + 4);
+    oks = oks >> 4 | group_bits(id_v) << (4 * (2 + late));
+    fetch_k(st0 + round + 2, id_k);
+    fetch_v(st0 + round + 3, id_v);
+    vb = vb + 1 == T::VB ? 0 : vb + 1;
+    if (!late) __syncthreads();
   }
 
 #pragma unroll
