@@ -107,9 +107,11 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
     codes = at + row * (uint32_t)(D / 2);
     scales = at + ((uint32_t)(D / 2) << a.page_shift) + row * (uint32_t)(D / 16);
   };
-  u32x4 raw[T::UNITS];
-  uint16_t rsc[T::UNITS];
-  const auto fetch_k = [&](int st, int id) {
+  struct Pieces {
+    u32x4 raw[T::UNITS];
+    uint16_t scale[T::UNITS];
+  };
+  const auto fetch_k = [&](int st, int id, Pieces& x) {
 #pragma unroll
     for (int k = 0; k < T::UNITS; ++k) {
       const int u = wave + PW * k;
@@ -117,45 +119,43 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
       const int piece = u * 64 + lane, key = piece / NB, b = piece % NB;
       uint64_t codes, scales;
       row_at(keys.lo + st * STEP + key, __shfl(id, key, 64), codes, scales);
-      raw[k] = ld_16B(a.kc + codes + 16 * b);
-      rsc[k] = (uint16_t)ld_u16(a.kc + scales + 2 * b);
+      x.raw[k] = ld_16B(a.kc + codes + 16 * b);
+      x.scale[k] = (uint16_t)ld_u16(a.kc + scales + 2 * b);
     }
   };
-  uint32_t there = 0;  // all ones where the lane's value row is a key
-  const auto fetch_v = [&](int st, int id) {
+  const auto fetch_v = [&](int st, int id, Pieces& x) {
 #pragma unroll
     for (int k = 0; k < T::UNITS; ++k) {
       const int u = wave + PW * k;
       if (u < NB || u >= 2 * NB) continue;
       uint64_t codes, scales;
       row_at(keys.lo + st * STEP + lane, id, codes, scales);
-      raw[k] = ld_16B(a.vc + codes + 16 * (u - NB));
-      rsc[k] = (uint16_t)ld_u16(a.vc + scales + 2 * (u - NB));
+      x.raw[k] = ld_16B(a.vc + codes + 16 * (u - NB));
+      x.scale[k] = (uint16_t)ld_u16(a.vc + scales + 2 * (u - NB));
     }
-    there = id >= 0 ? 0xFFFFu : 0u;
   };
-  const auto stage_v = [&]() {
+  const auto stage_v = [&](const Pieces& x, int id) {
 #pragma unroll
     for (int k = 0; k < T::UNITS; ++k) {
       const int u = wave + PW * k;
       if (u < NB || u >= 2 * NB) continue;
       uint8_t* rows16 = lds + (2 + T::VB) * T::HALF + (u - NB) * T::RAW;  // this unit's own
       uint16_t* scales = (uint16_t*)(rows16 + STEP * 16);
-      *(u32x4*)(rows16 + (((lane >> 2) & 3) * 16 + g * 4 + (lane & 3)) * 16) = raw[k];
+      *(u32x4*)(rows16 + (((lane >> 2) & 3) * 16 + g * 4 + (lane & 3)) * 16) = x.raw[k];
       // bytes behind the last key are anything, NaN included: their values enter as 0 * code
-      scales[((lane >> 2) & 3) * 16 + (g >> 1) * 8 + (lane & 3) * 2 + (g & 1)] = (uint16_t)(rsc[k] & there);
+      scales[((lane >> 2) & 3) * 16 + (g >> 1) * 8 + (lane & 3) * 2 + (g & 1)] = (uint16_t)(id >= 0 ? x.scale[k] : 0);
     }
   };
-  const auto unpack = [&](int kb, int vb) {
+  const auto unpack = [&](int kb, int vb, const Pieces& y) {
     uint8_t* kbuf = lds + kb * T::HALF;
     uint8_t* vbuf = lds + (2 + vb) * T::HALF;
 #pragma unroll
     for (int k = 0; k < T::UNITS; ++k) {
       const int u = wave + PW * k;
       if (u < NB) {
-        const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+        const uint32_t w[4] = {y.raw[k].x, y.raw[k].y, y.raw[k].z, y.raw[k].w};
         const int piece = u * 64 + lane, key = piece / NB, b = piece % NB;
-        const half_t sc = __builtin_bit_cast(half_t, rsc[k]);
+        const half_t sc = __builtin_bit_cast(half_t, y.scale[k]);
         const half2_t s2 = half2_t{sc, sc};
         // operand (key group, block): lane group j holds values 8 j .. of the
         // block; keys are swizzled by the block so that neighbouring lanes'
@@ -215,37 +215,51 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
 
   const int late = T::OFFSET && wave >= PW / 2 ? 1 : 0;
   const int steps_here = st1 - st0;
+  // on equal terms the older waves of a SIMD win the vector unit, reach the
+  // barrier early and wait there for the others
+  if (late) __builtin_amdgcn_s_setprio(1);
   uint64_t oks = 0;  // which key groups have a page: four bits a step, the current one lowest
   const auto group_bits = [&](int id) -> uint64_t {
     const uint64_t m = __ballot(id >= 0);  // a group's first key tells for all of it
     return (m & 1) | (m >> 15 & 2) | (m >> 30 & 4) | (m >> 45 & 8);
   };
-  // ids of the steps whose keys, and whose values, are fetched next; ids on their way
+  // The pieces on their way are keys of step round + 2 and values of step
+  // round + 3; the ids of those steps and the one after.
+  Pieces x;
   int id_k = 0, id_v = 0, id_next = 0;
   if (steps_here > 0) {
     // (steps behind the last are fetched from page 0 and unpacked to places that nothing reads)
-    int id = checked(st0, page_id(st0));
-    id_k = checked(st0 + 1, page_id(st0 + 1));
-    id_v = checked(st0 + 2, page_id(st0 + 2));
-    id_next = page_id(st0 + 3);
-    oks = group_bits(id) | group_bits(id_k) << 4 | group_bits(id_v) << 8;
-    fetch_k(st0, id);
-    fetch_v(st0, id);
-    stage_v();
-    fetch_v(st0 + 1, id_k);
-    unpack(0, 0);
-    stage_v();
-    fetch_k(st0 + 1, id_k);
-    fetch_v(st0 + 2, id_v);
+    int id[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) id[i] = page_id(st0 + i);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) id[i] = checked(st0 + i, id[i]);
+    oks = group_bits(id[0]) | group_bits(id[1]) << 4 | group_bits(id[2]) << 8;
+    Pieces x0, x1;
+    fetch_k(st0, id[0], x0);
+    fetch_v(st0, id[0], x0);
+    fetch_k(st0 + 1, id[1], x1);
+    fetch_v(st0 + 1, id[1], x1);
+    fetch_v(st0 + 2, id[2], x);
+    stage_v(x0, id[0]);
+    unpack(0, 0, x0);
+    stage_v(x1, id[1]);
     if (late) {
-      unpack(1, 1);
-      stage_v();
-      id_k = id_v;
-      id_v = checked(st0 + 3, id_next);
-      id_next = page_id(st0 + 4);
-      oks |= group_bits(id_v) << 12;
-      fetch_k(st0 + 2, id_k);
-      fetch_v(st0 + 3, id_v);
+      unpack(1, 1, x1);
+      stage_v(x, id[2]);
+      fetch_k(st0 + 2, id[2], x);
+      fetch_v(st0 + 3, id[3], x);
+      oks |= group_bits(id[3]) << 12;
+      id_k = id[2];
+      id_v = id[3];
+      id_next = id[4];
+    } else {
+      id_k = id[1];
+      id_v = id[2];
+      id_next = page_id(st0 + 3);
+#pragma unroll
+      for (int k = 0; k < T::UNITS; ++k)
+        if (wave + PW * k < NB) { x.raw[k] = x1.raw[k]; x.scale[k] = x1.scale[k]; }
     }
   }
   __syncthreads();
@@ -341,14 +355,14 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
     const int round = n + late;
     int vn = vb + 1 + late;
     vn = vn >= T::VB ? vn - T::VB : vn;
-    unpack((round + 1) & 1, vn);
-    stage_v();
+    unpack((round + 1) & 1, vn, x);
+    stage_v(x, id_v);
     id_k = id_v;
     id_v = checked(st0 + round + 3, id_next);
     id_next = page_id(st0 + round + 4);
     oks = oks >> 4 | group_bits(id_v) << (4 * (2 + late));
-    fetch_k(st0 + round + 2, id_k);
-    fetch_v(st0 + round + 3, id_v);
+    fetch_k(st0 + round + 2, id_k, x);
+    fetch_v(st0 + round + 3, id_v, x);
     vb = vb + 1 == T::VB ? 0 : vb + 1;
     if (!late) __syncthreads();
   }
