@@ -633,7 +633,7 @@ int kq_kv_attention_workspace(int64_t tokens, int64_t n_seqs, int64_t q_heads, i
   const int st = check_attn_sizes(op, tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv);
   if (st) return st;
   if (!bytes) return fail(KQ_ERR_ARG, op, "null output");
-  *bytes = tokens == 0 || n_seqs == 0 ? 0 : kq::attn_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv).bytes;
+  *bytes = tokens == 0 || n_seqs == 0 ? 0 : kq::attn_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv, 0).bytes;
   return KQ_OK;
 }
 
@@ -669,7 +669,7 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
   const int64_t out_bytes = tokens * q_heads * d * elem_bytes(out_dtype);
   if (overlaps(q, ((tokens - 1) * q_stride + q_heads * d) * 2, out, out_bytes))
     return fail(KQ_ERR_ARG, op, "out overlaps q");
-  const kq::AttnPlan plan = kq::attn_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv);
+  const kq::AttnPlan plan = kq::attn_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv, window);
   if (plan.bytes > 0) {
     if (!workspace || workspace_bytes < plan.bytes)
       return fail(KQ_ERR_CAPACITY, op, "workspace of %lld bytes is below the %lld these sizes need",
@@ -685,7 +685,9 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
   a.kc = (const uint8_t*)k_cache;
   a.vc = (const uint8_t*)v_cache;
   a.out = out;
-  a.part = (float*)workspace;
+  a.many = (float*)workspace;
+  a.few = (float*)((uint8_t*)workspace + plan.few_at);
+  a.where = plan.bytes > 0 ? (int32_t*)((uint8_t*)workspace + plan.where_at) : nullptr;
   a.q_stride = q_stride;
   a.width = width;
   a.page_head_bytes = page * (d / 2 + d / 16);
@@ -701,10 +703,11 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
   a.scale = scale;
   a.q_bf16 = q_dtype == KQ_BF16;
   a.out_type = elem_id(out_dtype);
+  a.few_rows = plan.few_rows;
+  a.one_tile = plan.one_tile;
+  a.few_wgs = plan.few_wgs;
   a.splits = plan.splits;
   a.chunk = plan.chunk;
-  a.one_tile = plan.one_tile;
-  a.few_rows = plan.few_rows;
   return hip_status(op, kq::launch_kv_attention(a, plan, (hipStream_t)stream));
 }
 

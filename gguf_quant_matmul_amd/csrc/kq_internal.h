@@ -408,26 +408,32 @@ struct AttnArgs {
   const uint8_t* kc;
   const uint8_t* vc;
   void* out;
-  float* part;     // workspace: partial sums, then (maximum, sum) pairs, then split counts
+  // workspace (null without splits): sums of rows whose keys are shared, each
+  // part rows of d floats, then (maximum, sum) pairs; where a row's are
+  float* many;      // prompt tiles: row (split * tokens + t) * q_heads + h
+  float* few;       // 16-row tiles: row ((workgroup * kv_heads + h) * 2 + (a tile begins there)) * 16 + row of the tile
+  int32_t* where;   // [tokens][q_heads][2]
   int64_t q_stride, width, page_head_bytes;
   int tokens, n_seqs, hq, hkv, group, d;
   int pages, page_shift;
   int window;      // 0: none
   float scale;
   int q_bf16, out_type;
-  int splits;      // most workgroups that share one row's keys
-  int chunk;       // keys a workgroup takes before another one is worth it
-  int one_tile;    // a request's rows fit one 16-row tile: tile index = request
   int few_rows;    // requests of at most so many rows take 16-row tiles, others prompt tiles
+  int one_tile;    // 16-row tiles: a request's rows fit one, so that tile index = request
+  int few_wgs;     // workgroups a kv head that share all requests' 16-row tiles evenly (0: one to a tile)
+  int splits;      // prompt tiles: most workgroups that share a tile's keys
+  int chunk;       // prompt tiles: keys a workgroup takes before another one is worth it
 };
 // How a call's work is split, from its host-known sizes alone.
 struct AttnPlan {
-  int splits, chunk, one_tile, few_rows;
-  int64_t few_tiles, many_tiles;  // tiles of 16 rows, of a prompt tile's rows (bounds; 0: that kernel does not run)
+  int few_rows, one_tile, few_wgs, splits, chunk;
+  int64_t few_tiles, many_tiles;  // 16-row and prompt tiles (bounds; 0: that kernel does not run)
+  int64_t few_at, where_at;       // byte offsets into the workspace
   int64_t bytes;                  // workspace
 };
 AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
-                   int64_t max_kv);
+                   int64_t max_kv, int64_t window);
 hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
 int attn_prompt_rows(int64_t d);  // rows of a prompt tile
 hipError_t launch_attn_prompt(const AttnArgs& a, const AttnPlan& p, hipStream_t s);

@@ -18,12 +18,13 @@ struct Seq {
   int row0, n;  // first token row, new tokens
   int len;      // keys
 };
+typedef const __attribute__((address_space(4))) int32_t* ConstInts;  // read only here: scalar loads may fetch it
 __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int s) {
-  int b = a.cu[s], e = a.cu[s + 1];
+  int b = ((ConstInts)a.cu)[s], e = ((ConstInts)a.cu)[s + 1];
   b = b < 0 ? 0 : b > a.tokens ? a.tokens : b;
   e = e < b ? b : e > a.tokens ? a.tokens : e;
   const int64_t cap = a.width << a.page_shift;
-  int64_t len = a.lens[s];
+  int64_t len = ((ConstInts)a.lens)[s];
   len = len < 0 ? 0 : len > cap ? cap : len;
   return Seq{b, e - b, (int)len};
 }
@@ -40,7 +41,7 @@ __device__ __forceinline__ Keys key_range(const AttnArgs& a, const Seq& q, int r
   k.lo = (lo > 0 ? (int)lo : 0) & ~63;
   return k;
 }
-// Workgroups that share those keys.
+// Workgroups of the prompt kernel that share those keys.
 __device__ __forceinline__ int split_count(const AttnArgs& a, const Keys& k) {
   const int n = k.end - k.lo, s = n > 0 ? (int)(((int64_t)n + a.chunk - 1) / a.chunk) : 0;
   return s < a.splits ? s : a.splits;
@@ -93,13 +94,25 @@ __device__ __forceinline__ Groups groups_of(const AttnArgs& a, const int (&ids)[
   Groups r;
   r.ok = 0;
   const int mask = (1 << a.page_shift) - 1;
+  const int64_t behind = (int64_t)(D / 2) << a.page_shift;  // a page's scales follow its codes
+  if (a.page_shift >= 6) {  // a step lies in one page
+    const bool ok = ids[0] >= 0 && ids[0] < a.pages;
+    const int64_t at = ((int64_t)(ok ? ids[0] : 0) * a.hkv + h) * a.page_head_bytes;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      r.codes[i] = at + (int64_t)((base & mask) + 16 * i) * (D / 2);
+      r.scales[i] = at + behind + (int64_t)((base & mask) + 16 * i) * (D / 16);
+      r.ok |= ok && base + 16 * i < end ? 1u << i : 0u;
+    }
+    return r;
+  }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int k = base + 16 * i;
     const bool ok = k < end && ids[i] >= 0 && ids[i] < a.pages;
     const int64_t at = ((int64_t)(ok ? ids[i] : 0) * a.hkv + h) * a.page_head_bytes;
     r.codes[i] = at + (int64_t)(k & mask) * (D / 2);
-    r.scales[i] = at + ((int64_t)(D / 2) << a.page_shift) + (int64_t)(k & mask) * (D / 16);
+    r.scales[i] = at + behind + (int64_t)(k & mask) * (D / 16);
     r.ok |= ok ? 1u << i : 0u;
   }
   return r;
@@ -223,9 +236,6 @@ __device__ __forceinline__ void load_query(const AttnArgs& a, const void* row, b
   }
   factor = fmaxf(factor, 1.17549435e-38f);  // a zero factor would turn masked -inf into NaN
 }
-
-// where the workspace holds the split counts, pairs and partial sums
-__host__ __device__ __forceinline__ int64_t part_rows(int64_t tokens, int64_t hq, int64_t splits) { return tokens * hq * splits; }
 
 template <int OUT>
 __device__ __forceinline__ void store4(void* out, int64_t i, float4_t v) {

@@ -2,9 +2,10 @@
 //
 //   out = sum_j softmax_j(scale q . k_j) v_j,   k_j, v_j = D (c - 8)
 //
-// One pass over the keys with a running maximum and sum.  A workgroup takes
-// one 16-row tile of a (request, kv head); its four waves take 64-key steps in
-// turn, each with sums of its own, merged through LDS at the end.  Both
+// One pass over the keys with a running maximum and sum.  A workgroup takes a
+// run of 64-key steps of one 16-row tile of a (request, kv head); its four
+// waves take steps in turn, each with sums of its own, merged through LDS at
+// the end.  Both
 // products run on v_mfma_f32_16x16x32_f16, transposed so that nothing moves
 // between lanes in between:
 //   S^T [16 keys x 16 rows] = K [16 x d] Q^T; lane l holds row l % 16, keys
@@ -38,13 +39,35 @@ struct Stage {
   static constexpr int ONE = STEP * ROW + STEP * NB * 2;  // rows, then scales [block][64]
   static constexpr int BYTES = SHARED ? ONE : 2 * ONE;
 };
-// LDS to hand one wave's sums to another: O^T [d][16], then maximum and sum
+// A wave's part of LDS takes its steps, then its sums for the merge: 16 rows
+// of D floats, four apart more so that the rows of a lane group lie on
+// distinct banks.
 template <int NB>
-constexpr int merge_bytes() { return 16 * 32 * NB * 4 + 2 * 16 * 4; }
-template <int NB>
-constexpr int lds_bytes() {
-  constexpr int s = WAVES * Stage<NB>::BYTES, m = 2 * merge_bytes<NB>();
-  return s > m ? s : m;
+constexpr int region_bytes() {
+  constexpr int m = 16 * (32 * NB + 4) * 4;
+  return Stage<NB>::BYTES > m ? Stage<NB>::BYTES : m;
+}
+
+// 64-key steps of a 16-row tile of a request; a tile without keys counts as
+// one, so that someone writes its zeros.
+__device__ __forceinline__ int tile_steps(const AttnArgs& a, const Seq& q, int sub) {
+  const int rows = q.n * a.group, r0 = sub * 16, r1 = r0 + 15 < rows ? r0 + 15 : rows - 1;
+  const Keys k = key_range(a, q, r0, r1);
+  return k.end > k.lo ? (k.end - k.lo + STEP - 1) / STEP : 1;
+}
+__device__ __forceinline__ int request_steps(const AttnArgs& a, int s) {
+  if (s >= a.n_seqs) return 0;
+  const Seq q = load_seq(a, s);
+  const int rows = q.n * a.group;
+  if (rows > a.few_rows) return 0;
+  int n = 0;
+  for (int sub = 0; sub * 16 < rows; ++sub) n += tile_steps(a, q, sub);
+  return n;
+}
+
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32 |
+         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
 }
 
 template <int NB>
@@ -57,46 +80,98 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
   // K scales of a lane: one where its quarter row lies inside a block, one per
   // block where it covers whole ones, else one per dword
   constexpr int KS = NB == 1 || NB == 2 || NB == 4 ? 1 : NB == 8 ? 2 : NB;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[lds_bytes<NB>()];
+  constexpr int REGION = region_bytes<NB>();
+  __shared__ __attribute__((aligned(16))) uint8_t lds[WAVES * REGION];
+  __shared__ float merge_m[WAVES][16], merge_l[WAVES][16];
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = blockIdx.x % a.hkv, tile = blockIdx.x / a.hkv, split = blockIdx.y;
+  const int h = blockIdx.x % a.hkv, wg = blockIdx.x / a.hkv;
 
-  int s = tile, sub = 0;
-  if (!a.one_tile) {
-    if (!find_tile(a, tile, 16, 0, a.few_rows, s, sub)) return;
+  // Where the workgroup begins: tile `sub` of request s, whose steps begin at
+  // x among all (64-bit: garbage lengths may add up).  Steps x0 .. x1 - 1 are
+  // its own, `share` to a workgroup; or (few_wgs = 0) all of tile wg.
+  int s = wg, sub = 0;
+  uint64_t x = 0, x0 = 0, x1 = 0, share = 1;
+  if (a.few_wgs == 0) {
+    if (!a.one_tile && !find_tile(a, wg, 16, 0, a.few_rows, s, sub)) return;
+  } else {
+    uint64_t total = 0;
+    for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
+      uint64_t n = (uint64_t)request_steps(a, s0 + lane);
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o, 64);
+      total += n;
+    }
+    total = uniform64(total);
+    share = (total + a.few_wgs - 1) / (uint64_t)a.few_wgs;
+    share = share < WAVES ? WAVES : share;
+    x0 = share * (uint64_t)wg;
+    x1 = x0 + share < total ? x0 + share : total;
+    if (x0 >= total) return;
+    for (int s0 = 0;; s0 += 64) {
+      const uint64_t n = (uint64_t)request_steps(a, s0 + lane);
+      uint64_t incl = n;
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const uint64_t t = __shfl_up(incl, o, 64);
+        if (lane >= o) incl += t;
+      }
+      const uint64_t hit = __ballot(x + incl > x0);
+      if (hit) {  // total > x0: some request has it
+        const int l = __builtin_ctzll(hit);
+        s = s0 + l;
+        x += __shfl(incl, l, 64) - __shfl(n, l, 64);
+        break;
+      }
+      x += __shfl(incl, 63, 64);
+    }
+    s = __builtin_amdgcn_readfirstlane(s);
+    x = uniform64(x);
   }
-  const Seq sq = load_seq(a, s);
-  const int rows = sq.n * a.group;
-  // with one tile to a request, a request that has more walks its own
-  for (; sub * 16 < rows; ++sub) {
+
+  for (;; ++sub) {
+    const Seq sq = load_seq(a, s);
+    const int rows = sq.n * a.group;
+    if (sub * 16 >= rows || rows > a.few_rows) {  // (a request with one tile may have none, or more)
+      if (a.few_wgs == 0 || ++s >= a.n_seqs) return;
+      sub = -1;
+      continue;
+    }
     const int r0 = sub * 16, r1 = r0 + 15 < rows ? r0 + 15 : rows - 1;
     const Keys keys = key_range(a, sq, r0, r1);
-    const int n_split = split_count(a, keys);
-    const int row = r0 + col;
-    const bool live = row < rows;
-    const int tok = sq.row0 + row / a.group, head = h * a.group + row % a.group;
-    const int64_t orow = (int64_t)tok * a.hq + head;
-    // positions of this lane's row, of the tile's first and last
-    const int p = live ? sq.len - sq.n + row / a.group : -1;
-    const int p0 = sq.len - sq.n + r0 / a.group, p1 = sq.len - sq.n + r1 / a.group;
-
-    int32_t* counts = (int32_t*)(a.part + part_rows(a.tokens, a.hq, a.splits) * (D + 2));
-    if (a.splits > 1 && split == 0 && threadIdx.x < 16 && live) counts[orow] = n_split > 1 ? n_split : 0;
-    if (n_split == 0 && split == 0) {
-      for (int t = wave; t < DT; t += WAVES)
-        if (live) store4(a.out, a.out_type, orow * D + 16 * t + 4 * g, float4_t{0, 0, 0, 0});
+    const int steps = keys.end > keys.lo ? (keys.end - keys.lo + STEP - 1) / STEP : 0;
+    int st0 = 0, st1 = steps, pieces = 1, first = 0;
+    if (a.few_wgs > 0) {
+      const uint64_t x_end = x + (steps > 0 ? steps : 1);
+      if (x_end <= x0) {  // a tile before the workgroup's first
+        x = x_end;
+        continue;
+      }
+      if (x >= x1) return;
+      st0 = x0 > x ? (int)(x0 - x) : 0;
+      st1 = x1 < x_end ? (int)(x1 - x) : steps;
+      first = (int)(x / share);
+      pieces = (int)((x_end - 1) / share) - first + 1;
+      x = x_end;
     }
-    if (split < n_split) {
-      const int steps = (keys.end - keys.lo + STEP - 1) / STEP;
-      const int st0 = (int)((int64_t)steps * split / n_split), st1 = (int)((int64_t)steps * (split + 1) / n_split);
+    {
+      const int row = r0 + col;
+      const bool live = row < rows;
+      const int tok = sq.row0 + row / a.group, head = h * a.group + row % a.group;
+      // positions of this lane's row, of the tile's first and last
+      const int p = live ? sq.len - sq.n + row / a.group : -1;
+      const int p0 = sq.len - sq.n + r0 / a.group, p1 = sq.len - sq.n + r1 / a.group;
+      if (a.where && st0 == 0 && threadIdx.x < 16 && live) {
+        int32_t* w = a.where + 2 * ((int64_t)tok * a.hq + head);
+        w[0] = pieces > 1 ? -pieces : 0;
+        w[1] = first * 16 + col;
+      }
 
-      uint8_t* kcodes = lds + wave * Stage<NB>::BYTES;
+      uint8_t* kcodes = lds + wave * REGION;
       uint8_t* vcodes = kcodes + (Stage<NB>::SHARED ? 0 : Stage<NB>::ONE);
       uint16_t* kscales = (uint16_t*)(kcodes + STEP * Stage<NB>::ROW);
       uint16_t* vscales = (uint16_t*)(vcodes + STEP * Stage<NB>::ROW);
-      // read only here, so scalar loads may fetch it
-      const auto* pages = (const __attribute__((address_space(4))) int32_t*)(a.table + (int64_t)s * a.width);
+      const ConstInts pages = (ConstInts)(a.table + (int64_t)s * a.width);
 
       // registers of the step in flight
       u32x4 kw[NB], vw[NB];
@@ -105,7 +180,8 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int k = keys.lo + st * STEP + 16 * i;
-          ids[i] = st < st1 && k < keys.end ? pages[k >> a.page_shift] : -1;
+          // (below 64 keys a page a step's groups may lie in different ones)
+          ids[i] = st < st1 && k < keys.end && (i == 0 || a.page_shift < 6) ? pages[k >> a.page_shift] : -1;
         }
       };
       // codes in 16-byte pieces, lanes on consecutive ones; scales a lane to a key
@@ -274,82 +350,117 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
           }
         }
       }
-      float l = l4[0];
 
-      // merge: waves 2, 3 into 0, 1, then 1 into 0
+      // merge: every wave's sums into its part of LDS, then each thread joins
+      // the four of its values
+      // (indices from an opaque copy: nothing of this is computed ahead of the
+      // steps, where it would push their registers to memory)
+      int tid = threadIdx.x;
+      asm volatile("" : "+v"(tid));
+      const int mcol = tid & 15, mg = (tid & 63) >> 4;
+      float* mine = (float*)(lds + wave * REGION);
 #pragma unroll
-      for (int half = WAVES / 2; half > 0; half >>= 1) {
-        __syncthreads();
-        float* buf = (float*)(lds + (wave & (half - 1)) * merge_bytes<NB>());
-        if (wave >= half && wave < 2 * half) {
-#pragma unroll
-          for (int t = 0; t < DT; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) buf[(16 * t + 4 * g + j) * 16 + col] = o[t][j];
-          if (g == 0) { buf[D * 16 + col] = m; buf[D * 16 + 16 + col] = l; }
-        }
-        __syncthreads();
-        if (wave < half) {
-          const float m2 = buf[D * 16 + col], l2 = buf[D * 16 + 16 + col];
-          const float mx = fmaxf(m, m2), ref = mx == NEG_INF ? 0.f : mx;
-          const float c1 = __builtin_amdgcn_exp2f((m - ref) * factor), c2 = __builtin_amdgcn_exp2f((m2 - ref) * factor);
-          m = mx;
-          l = l * c1 + l2 * c2;
-#pragma unroll
-          for (int t = 0; t < DT; ++t)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) o[t][j] = o[t][j] * c1 + buf[(16 * t + 4 * g + j) * 16 + col] * c2;
-        }
+      for (int t = 0; t < DT; ++t) *(float4_t*)(mine + mcol * (D + 4) + 16 * t + 4 * mg) = o[t];
+      if (mg == 0) {
+        merge_m[wave][mcol] = m == NEG_INF ? NEG_INF : m * factor;  // in powers of two
+        merge_l[wave][mcol] = l4[0];
       }
-      if (wave == 0 && live) {
-        if (n_split == 1) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;  // no key seen: zeros
+      __syncthreads();
 #pragma unroll
-          for (int t = 0; t < DT; ++t) store4(a.out, a.out_type, orow * D + 16 * t + 4 * g, o[t] * inv);
+      for (int k = 0; k < (16 * D / 4 + 64 * WAVES - 1) / (64 * WAVES); ++k) {
+        const int i = k * 64 * WAVES + tid, r = i / (D / 4), c = i % (D / 4) * 4;
+        if (r >= 16 || r0 + r >= rows) break;
+        float mx = merge_m[0][r];
+#pragma unroll
+        for (int w = 1; w < WAVES; ++w) mx = fmaxf(mx, merge_m[w][r]);
+        const float ref = mx == NEG_INF ? 0.f : mx;
+        float l = 0.f;
+        float4_t v = {0, 0, 0, 0};
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) {
+          const float f = __builtin_amdgcn_exp2f(merge_m[w][r] - ref);
+          l += f * merge_l[w][r];
+          v += f * *(const float4_t*)((const float*)(lds + w * REGION) + r * (D + 4) + c);
+        }
+        if (pieces == 1) {
+          const int64_t orow = (int64_t)(sq.row0 + (r0 + r) / a.group) * a.hq + h * a.group + (r0 + r) % a.group;
+          store4(a.out, a.out_type, orow * D + c, v * (l == 0.f ? 0.f : 1.f / l));  // no key seen: zeros
         } else {
-          const int64_t pr = (int64_t)split * a.tokens * a.hq + orow;
-#pragma unroll
-          for (int t = 0; t < DT; ++t) store4<0>(a.part, pr * D + 16 * t + 4 * g, o[t]);
-          if (g == 0) {
-            float* ml = a.part + part_rows(a.tokens, a.hq, a.splits) * D + 2 * pr;
-            ml[0] = m == NEG_INF ? NEG_INF : m * factor;  // in powers of two, for the merge
+          const int64_t pr = (((int64_t)wg * a.hkv + h) * 2 + (st0 == 0 ? 1 : 0)) * 16 + r;
+          store4<0>(a.few, pr * D + c, v);
+          if (c == 0) {
+            float* ml = a.few + (int64_t)a.few_wgs * a.hkv * 32 * D + 2 * pr;
+            ml[0] = mx;
             ml[1] = l;
           }
         }
       }
       __syncthreads();  // the next tile reuses the LDS
     }
-    if (!a.one_tile) break;
+    if (a.few_wgs == 0 && !a.one_tile) return;
   }
 }
 
-// Joins the partial sums of split rows: a thread per 4 values of a row.
+// Joins the sums of rows whose keys several workgroups shared: d / 4 threads
+// to a piece; a workgroup takes one row with as many of its pieces side by
+// side as fit (SIDE: few rows, many pieces), or as many rows as fit.
+template <bool SIDE>
 __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
-  const int per = a.d / 4;
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, row = i / per;
-  const int c = (int)(i - row * per) * 4;
+  __shared__ float4_t part[SIDE ? 256 : 1];
   const int64_t n_rows = (int64_t)a.tokens * a.hq;
-  if (row >= n_rows) return;
-  int b = a.cu[0], e = a.cu[a.n_seqs];
-  b = b < 0 ? 0 : b;
-  const int tok = (int)(row / a.hq);
-  if (tok < b || tok >= e) return;  // no request's row: its count was not written
-  const int64_t pr = part_rows(a.tokens, a.hq, a.splits);
-  const int32_t* counts = (const int32_t*)(a.part + pr * (a.d + 2));
-  int n = counts[row];
-  n = n > a.splits ? a.splits : n;
-  if (n <= 1) return;  // written by the workgroup itself
-  const float* ml = a.part + pr * a.d;
-  float m = NEG_INF;
-  for (int s = 0; s < n; ++s) m = fmaxf(m, ml[2 * (s * n_rows + row)]);
-  const float ref = m == NEG_INF ? 0.f : m;
+  const int per = a.d / 4, fit = 256 / per, k = threadIdx.x / per, c = (threadIdx.x % per) * 4;
+  const int64_t row = SIDE ? blockIdx.x : (int64_t)blockIdx.x * fit + k;
+  if (!SIDE && (k >= fit || row >= n_rows)) return;
+  const int tok = (int)(row / a.hq), h = (int)(row - (int64_t)tok * a.hq) / a.group;
+  const int b = ((ConstInts)a.cu)[0], e = ((ConstInts)a.cu)[a.n_seqs];
+  if (tok < b || tok >= e) return;  // no request's row: nothing was written for it
+  int n = a.where[2 * row];
+  if (n == 0) return;  // written by the workgroup itself
+  const bool few = n < 0;
+  const int at = a.where[2 * row + 1];
+  n = few ? -n : n;
+  // (bounds for offsets that are not a batch's: rows no request owns hold anything)
+  const int most = few ? a.few_wgs - (at >> 4) : a.splits;
+  if (n > most || (few && (at < 0 || (at >> 4) >= a.few_wgs))) return;
+  const float* sums = few ? a.few : a.many;
+  const float* ml = sums + (few ? (int64_t)a.few_wgs * a.hkv * 32 : n_rows * a.splits) * a.d;
+  const auto piece = [&](int i) -> int64_t {
+    return few ? ((((int64_t)(at >> 4) + i) * a.hkv + h) * 2 + (i == 0 ? 1 : 0)) * 16 + (at & 15) : i * n_rows + row;
+  };
+  float m = NEG_INF, l = 0.f;
   float4_t o = {0, 0, 0, 0};
-  float l = 0.f;
-  for (int s = 0; s < n; ++s) {
-    const int64_t r = s * n_rows + row;
-    const float w = __builtin_amdgcn_exp2f(ml[2 * r] - ref);
-    l += w * ml[2 * r + 1];
-    o += w * *(const float4_t*)(a.part + r * a.d + c);
+  if constexpr (SIDE) {
+    // every wave finds the maximum and the sum for itself, 64 pieces at a time
+    const int lane = threadIdx.x & 63;
+    for (int i = lane; i < n; i += 64) m = fmaxf(m, ml[2 * piece(i)]);
+#pragma unroll
+    for (int x = 32; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor(m, x, 64));
+    const float ref = m == NEG_INF ? 0.f : m;
+    for (int i = lane; i < n; i += 64) l += __builtin_amdgcn_exp2f(ml[2 * piece(i)] - ref) * ml[2 * piece(i) + 1];
+#pragma unroll
+    for (int x = 32; x > 0; x >>= 1) l += __shfl_xor(l, x, 64);
+    if (k < fit) {
+#pragma unroll 4
+      for (int i = k; i < n; i += fit) {
+        const int64_t r = piece(i);
+        o += __builtin_amdgcn_exp2f(ml[2 * r] - ref) * *(const float4_t*)(sums + r * a.d + c);
+      }
+    }
+  } else {
+    for (int i = 0; i < n; ++i) m = fmaxf(m, ml[2 * piece(i)]);
+    const float ref = m == NEG_INF ? 0.f : m;
+    for (int i = 0; i < n; ++i) {
+      const int64_t r = piece(i);
+      const float w = __builtin_amdgcn_exp2f(ml[2 * r] - ref);
+      l += w * ml[2 * r + 1];
+      o += w * *(const float4_t*)(sums + r * a.d + c);
+    }
+  }
+  if constexpr (SIDE) {
+    part[threadIdx.x] = o;
+    __syncthreads();
+    if (k > 0) return;
+    for (int i = 1; i < fit && i < n; ++i) o += part[i * per + threadIdx.x];
   }
   store4(a.out, a.out_type, row * a.d + c, o * (l == 0.f ? 0.f : 1.f / l));
 }
@@ -361,8 +472,10 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 constexpr int FEW_ROWS = 32;
 
 AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
-                   int64_t max_kv) {
+                   int64_t max_kv, int64_t window) {
   AttnPlan p;
+  // keys that a request's rows see; a narrower bound never asks for more workspace
+  if (window > 0 && window + max_new < max_kv) max_kv = window + max_new;
   const int64_t group = q_heads / kv_heads, most = (max_new < tokens ? max_new : tokens) * group;
   p.one_tile = most <= 16;
   // Which kernels run.  Requests of few rows only: 16-row tiles.  One request
@@ -373,25 +486,31 @@ AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_h
   if (p.few_rows == FEW_ROWS && p.few_tiles > n_seqs * (FEW_ROWS / 16)) p.few_tiles = n_seqs * (FEW_ROWS / 16);
   const int tile = attn_prompt_rows(d);
   p.many_tiles = p.few_rows == 0x7FFFFFFF ? 0 : all / tile + n_seqs;
-  int64_t chunk;
+  // 16-row tiles: one workgroup to each where none has much work, or where
+  // they are so many that even unequal ones fill the GPU; else as many
+  // workgroups as run at once (three on each of 256 CUs, two with wide heads),
+  // each with the same number of steps
+  const int64_t at_once = d <= 128 ? 768 : 512;
+  p.few_wgs = 0;
+  if (p.few_tiles > 0 && max_kv > 1024 && n_seqs <= 1024 && p.few_tiles * kv_heads < 8 * at_once)
+    p.few_wgs = (int)((at_once + kv_heads - 1) / kv_heads);
+  // prompt tiles: one workgroup to a CU.  Split rows write and read float32
+  // sums, which costs as much as some 500 keys: 1024 keys at least where tiles
+  // alone leave a good part of the CUs idle, 4096 where unequal ones might
+  p.splits = 1;
+  p.chunk = 0x7FFFFFFF;
   if (p.many_tiles > 0) {
-    // prompt tiles: one workgroup to a CU.  Split rows write and read float32
-    // sums, which costs as much as some 500 keys, so only where tiles alone
-    // leave a good part of the CUs idle, and 1024 keys at least
     const int64_t wgs = p.many_tiles * kv_heads, want = (256 + wgs - 1) / wgs;
-    chunk = wgs >= 192 ? max_kv : (max_kv + want - 1) / want;
-    chunk = chunk < 1024 ? 1024 : chunk;
-  } else {
-    // enough workgroups for three on each of 256 CUs, none with fewer than 256
-    // keys; never more than 4096 keys to one, whose length differs from others'
-    const int64_t wgs = p.few_tiles * kv_heads, want = (768 + wgs - 1) / wgs;
-    chunk = (max_kv + want - 1) / want;
-    chunk = chunk < 256 ? 256 : chunk > 4096 ? 4096 : chunk;
+    int64_t chunk = wgs >= 1024 ? max_kv : wgs >= 192 ? 4096 : (max_kv + want - 1) / want;
+    chunk = chunk < 1024 ? 1024 : wgs < 1024 && chunk > 4096 ? 4096 : chunk;
+    p.chunk = (int)(chunk < 0x7FFFFFC0 ? (chunk + 63) / 64 * 64 : 0x7FFFFFC0);
+    const int64_t n = (max_kv + p.chunk - 1) / p.chunk;
+    p.splits = (int)(n < 1 ? 1 : n > 64 ? 64 : n);
   }
-  p.chunk = (int)((chunk + 63) / 64 * 64);
-  p.splits = (int)((max_kv + p.chunk - 1) / p.chunk);
-  p.splits = p.splits < 1 ? 1 : p.splits > 256 ? 256 : p.splits;
-  p.bytes = p.splits > 1 ? part_rows(tokens, q_heads, p.splits) * (d + 2) * 4 + tokens * q_heads * 4 : 0;
+  const int64_t many = p.splits > 1 ? tokens * q_heads * p.splits : 0, few = (int64_t)p.few_wgs * kv_heads * 32;
+  p.few_at = many * (d + 2) * 4;
+  p.where_at = p.few_at + few * (d + 2) * 4;
+  p.bytes = many + few > 0 ? p.where_at + tokens * q_heads * 8 : 0;
   return p;
 }
 
@@ -402,7 +521,7 @@ hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t
     if (e != hipSuccess) return e;
   }
   if (p.few_tiles > 0) {
-    const dim3 grid((unsigned)(p.few_tiles * a.hkv), (unsigned)a.splits), block(64 * WAVES);
+    const dim3 grid((unsigned)((a.few_wgs > 0 ? a.few_wgs : p.few_tiles) * a.hkv)), block(64 * WAVES);
     const auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, s, a); };
     switch (a.d / 32) {
       case 1: go(attn_split_kernel<1>); break;
@@ -416,9 +535,11 @@ hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t
     }
     e = hipGetLastError();
   }
-  if (e != hipSuccess || a.splits == 1) return e;
-  const int64_t n = (int64_t)a.tokens * a.hq * (a.d / 4);
-  hipLaunchKernelGGL(attn_join_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s, a);
+  if (e != hipSuccess || p.bytes == 0) return e;
+  const int64_t n_rows = (int64_t)a.tokens * a.hq, fit = 256 / (a.d / 4);
+  // (2048 rows of one or two pieces: 7.6 us side by side, 4.7 us packed; 128 rows of 24: packed 22 us)
+  if (n_rows <= 1024) hipLaunchKernelGGL(attn_join_kernel<true>, dim3((unsigned)n_rows), dim3(256), 0, s, a);
+  else hipLaunchKernelGGL(attn_join_kernel<false>, dim3((unsigned)((n_rows + fit - 1) / fit)), dim3(256), 0, s, a);
   return hipGetLastError();
 }
 

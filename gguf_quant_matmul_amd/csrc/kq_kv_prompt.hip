@@ -72,16 +72,15 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
                           factor[c]);
   }
   if (split >= (n_split > 0 ? n_split : 1)) return;
-  if (a.splits > 1 && split == 0 && g == 0) {
-    int32_t* counts = (int32_t*)(a.part + part_rows(a.tokens, a.hq, a.splits) * (D + 2));
+  if (a.where && split == 0 && g == 0) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
-      if (live[c]) counts[orow[c]] = n_split > 1 ? n_split : 0;
+      if (live[c]) a.where[2 * orow[c]] = n_split > 1 ? n_split : 0;
   }
 
   const int steps = (keys.end - keys.lo + STEP - 1) / STEP;
-  const int st0 = n_split ? (int)((int64_t)steps * split / n_split) : 0;
-  const int st1 = n_split ? (int)((int64_t)steps * (split + 1) / n_split) : 0;
+  const int st0 = n_split ? (int)((uint32_t)steps * (uint32_t)split / (uint32_t)n_split) : 0;
+  const int st1 = n_split ? (int)((uint32_t)steps * (uint32_t)(split + 1) / (uint32_t)n_split) : 0;
   const int32_t* pages = a.table + (int64_t)s * a.width;
 
   // Unpacking is shared out in units: unit u < NB is 64 pieces (32 values) of
@@ -376,12 +375,12 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
 #pragma unroll
       for (int t = 0; t < DT; ++t) store4(a.out, a.out_type, orow[c] * D + 16 * t + 4 * g, o[t][c] * inv);
     } else {
-      const int64_t pr = (int64_t)split * a.tokens * a.hq + orow[c];
+      const int64_t n_rows = (int64_t)a.tokens * a.hq, pr = split * n_rows + orow[c];
 #pragma unroll
-      for (int t = 0; t < DT; ++t) store4<0>(a.part, pr * D + 16 * t + 4 * g, o[t][c]);
+      for (int t = 0; t < DT; ++t) store4<0>(a.many, pr * D + 16 * t + 4 * g, o[t][c]);
       if (g == 0) {
-        float* ml = a.part + part_rows(a.tokens, a.hq, a.splits) * D + 2 * pr;
-        ml[0] = m[c] == NEG_INF ? NEG_INF : m[c] * factor[c];  // in powers of two, for the merge
+        float* ml = a.many + n_rows * a.splits * D + 2 * pr;
+        ml[0] = m[c] == NEG_INF ? NEG_INF : m[c] * factor[c];  // in powers of two, for the join
         ml[1] = l;
       }
     }
