@@ -1,7 +1,8 @@
 """Build libkq.so for gfx950 in-tree: ``python -m gguf_quant_matmul_amd.build``.
 
 Compiles every ``csrc/*.hip`` with hipcc (one process per file, in parallel)
-and links them into ``gguf_quant_matmul_amd/libkq.so``.
+and links them into ``gguf_quant_matmul_amd/libkq.so``; then the host module
+``_kqcall.so`` (``csrc/kq_call.cpp``), which passes Python tensors to it.
 """
 
 from __future__ import annotations
@@ -17,6 +18,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libkq.so")
+CALL = os.path.join(HERE, "_kqcall.so")
 ARCH = os.environ.get("KQ_OFFLOAD_ARCH", "gfx950")
 
 HIPCC = shutil.which("hipcc") or "/opt/rocm/bin/hipcc"
@@ -54,6 +56,32 @@ def _stale(src: str) -> bool:
     return os.path.getmtime(obj) < newest
 
 
+def _call_module(verbose: bool, incremental: bool) -> None:
+    """Compile csrc/kq_call.cpp (plain C++ against torch's headers) and link it to libkq.so beside it."""
+    import sysconfig
+
+    import torch
+
+    src = os.path.join(CSRC, "kq_call.cpp")
+    deps = [src, os.path.join(HERE, os.pardir, "include", "kq.h")]
+    if incremental and os.path.exists(CALL) and os.path.getmtime(CALL) >= max(map(os.path.getmtime, deps)):
+        return
+    root = os.path.dirname(torch.__file__)
+    inc = os.path.join(root, "include")
+    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+           "-I" + sysconfig.get_paths()["include"], src, "-o", CALL + ".tmp",
+           "-L" + HERE, "-l:libkq.so", "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+           "-Wl,-rpath,$ORIGIN"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"compiling {src} failed:\n{res.stdout}{res.stderr}")
+    os.replace(CALL + ".tmp", CALL)
+    if verbose:
+        print(f"built {CALL}")
+
+
 def build(verbose: bool = False, incremental: bool = False) -> str:
     """Compile every source and link libkq.so; with incremental=True only the
     sources whose object is older than the source or a header are compiled."""
@@ -72,6 +100,7 @@ def build(verbose: bool = False, incremental: bool = False) -> str:
     os.replace(tmp, LIB)
     if verbose:
         print(f"built {LIB}")
+    _call_module(verbose, incremental)
     return LIB
 
 

@@ -25,6 +25,8 @@ if not os.path.exists(LIB_PATH):
 import torch  # noqa: E402,F401
 
 _lib = ctypes.CDLL(LIB_PATH)
+# the cache operators' calls straight from tensors (csrc/kq_call.cpp, built with the library and linked to it)
+from . import _kqcall  # noqa: E402
 
 c_int, c_i64, c_vp, c_cp = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_char_p
 _P = ctypes.POINTER
@@ -115,15 +117,6 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is not None:
         return int(stream) if isinstance(stream, int) else stream.cuda_stream
-    return _current_stream()
-
-
-def _current_stream() -> int:
-    """The current device's current stream (torch's raw accessor where it has one: a tenth of the time that building
-    a Stream object takes)."""
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    if raw is not None:
-        return raw(torch.cuda.current_device())
     return torch.cuda.current_stream().cuda_stream
 
 
@@ -291,8 +284,9 @@ def kq_stream_read(src, out, nbytes: int | None = None, stream=None) -> None:
 # key/value cache in 4 bits
 # ---------------------------------------------------------------------------
 
-# These calls are often shorter than their Python side, so the checks are
-# written out: one attribute read each, no helper call on the good path.
+# These calls are often shorter than their Python side: tensors of the current
+# device on its current stream go through _kqcall, which makes the same checks
+# and returns None for everything it leaves to the code here.
 _INTS = (torch.int32, torch.uint32)
 _DTYPES = {torch.float32: KQ_F32, torch.float16: KQ_F16, torch.bfloat16: KQ_BF16}
 
@@ -375,6 +369,12 @@ def kq_block_tables(ctx_lens, new_lens, free_pages, free_head, page: int, table,
                     free_head_out, status=None, stream=None) -> None:
     """Pages and slots of a step's new tokens.  ctx_lens, new_lens, seq_lens int32 [n]; free_pages int32 [n_free] from
     free_head int32 [1]; table int32 [n, width]; slots int32 [tokens]; cu_new int32 [n + 1]; free_head_out, status [1]."""
+    if stream is None and ctx_lens.is_cuda:
+        dev = torch._C._cuda_getDevice()
+        st = _kqcall.block_tables(ctx_lens, new_lens, free_pages, free_head, page, table, slots, cu_new, seq_lens,
+                                  free_head_out, status, torch._C._cuda_getCurrentRawStream(dev), dev)
+        if st is not None:
+            return _check(st)
     op, n, dev = "kq_block_tables", ctx_lens.numel(), ctx_lens.get_device()
     if table.dim() != 2 or table.shape[0] != n:
         raise ValueError(f"{op}: table must be [{n}, width]")
@@ -390,6 +390,11 @@ def kq_block_tables(ctx_lens, new_lens, free_pages, free_head, page: int, table,
 def kq_kv_store(codec, k, v, slots, k_cache, v_cache, page: int, stream=None) -> None:
     """k, v float32/float16/bfloat16 [tokens, kv_heads, d] (dense rows, any row stride) into slots int32 [tokens] of
     k_cache, v_cache uint8 [pages, kv_heads, page_bytes]."""
+    if stream is None and k.is_cuda and (codec == "q4_0" or codec == KQ_Q4_0):
+        dev = torch._C._cuda_getDevice()
+        st = _kqcall.kv_store(k, v, slots, k_cache, v_cache, page, torch._C._cuda_getCurrentRawStream(dev), dev)
+        if st is not None:
+            return _check(st)
     op, shape, dt, dev = "kq_kv_store", k.shape, _DTYPES.get(k.dtype), k.get_device()
     if len(shape) != 3 or v.shape != shape or v.dtype is not k.dtype or dt is None or v.get_device() != dev:
         raise ValueError(f"{op}: k and v must be [tokens, kv_heads, d] of one float dtype and device")
@@ -403,6 +408,11 @@ def kq_kv_store(codec, k, v, slots, k_cache, v_cache, page: int, stream=None) ->
 
 def kq_kv_load(codec, k_cache, v_cache, slots, page: int, k, v, stream=None) -> None:
     """The rows at slots int32 [tokens] of the caches to k, v [tokens, kv_heads, d] (float32, float16 or bfloat16)."""
+    if stream is None and k.is_cuda and (codec == "q4_0" or codec == KQ_Q4_0):
+        dev = torch._C._cuda_getDevice()
+        st = _kqcall.kv_load(k_cache, v_cache, slots, page, k, v, torch._C._cuda_getCurrentRawStream(dev), dev)
+        if st is not None:
+            return _check(st)
     op, shape, dt, dev = "kq_kv_load", k.shape, _DTYPES.get(k.dtype), k.get_device()
     if (len(shape) != 3 or v.shape != shape or v.dtype is not k.dtype or dt is None or v.get_device() != dev
             or not k.is_contiguous() or not v.is_contiguous()):
@@ -429,6 +439,14 @@ def kq_kv_attention(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page: i
     [n], table int32 [n, width]; out [tokens, q_heads, d]; scale defaults to d^-0.5.  max_new and max_kv bound a
     request's new tokens and length (default: tokens, width * page).  workspace: uint8 of kq_kv_attention_workspace
     bytes; allocated on the current stream if left out."""
+    if stream is None and q.is_cuda and (codec == "q4_0" or codec == KQ_Q4_0) and max_new is not None \
+            and max_kv is not None:
+        dev = torch._C._cuda_getDevice()
+        st = _kqcall.kv_attention(q, cu_new, seq_lens, table, k_cache, v_cache, page, out,
+                                  q.size(-1) ** -0.5 if scale is None else scale, window, max_new, max_kv, workspace,
+                                  torch._C._cuda_getCurrentRawStream(dev), dev)
+        if st is not None:
+            return _check(st)
     op, n, shape, dev = "kq_kv_attention", seq_lens.numel(), q.shape, q.get_device()
     qdt, odt = _DTYPES.get(q.dtype), _DTYPES.get(out.dtype)
     if len(shape) != 3 or qdt is None or odt is None:
