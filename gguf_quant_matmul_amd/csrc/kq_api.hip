@@ -696,6 +696,7 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
   a.hq = (int)q_heads;
   a.hkv = (int)kv_heads;
   a.group = (int)(q_heads / kv_heads);
+  a.group_shift = (a.group & (a.group - 1)) ? -1 : __builtin_ctz((unsigned)a.group);
   a.d = (int)d;
   a.pages = (int)pages;
   a.page_shift = shift;

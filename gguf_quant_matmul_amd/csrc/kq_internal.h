@@ -415,6 +415,7 @@ struct AttnArgs {
   int32_t* where;   // [tokens][q_heads][2]
   int64_t q_stride, width, page_head_bytes;
   int tokens, n_seqs, hq, hkv, group, d;
+  int group_shift;  // log2(group), -1 if it is none
   int pages, page_shift;
   int window;      // 0: none
   float scale;

@@ -29,12 +29,18 @@ __device__ __forceinline__ Seq load_seq(const AttnArgs& a, int s) {
   return Seq{b, e - b, (int)len};
 }
 
+// Token of a request's row (a shift where the group is a power of two: an
+// integer division is some 25 instructions).
+__device__ __forceinline__ int token_of(const AttnArgs& a, int row) {
+  return a.group_shift >= 0 ? row >> a.group_shift : (int)((uint32_t)row / (uint32_t)a.group);
+}
+
 // Keys that rows r0 .. r1 of a request see: lo (64-aligned) .. end - 1.
 struct Keys {
   int lo, end;
 };
 __device__ __forceinline__ Keys key_range(const AttnArgs& a, const Seq& q, int r0, int r1) {
-  const int p0 = q.len - q.n + r0 / a.group, p1 = q.len - q.n + r1 / a.group;  // positions
+  const int p0 = q.len - q.n + token_of(a, r0), p1 = q.len - q.n + token_of(a, r1);  // positions
   Keys k;
   k.end = p1 + 1 > 0 ? p1 + 1 : 0;
   const int64_t lo = a.window > 0 ? (int64_t)p0 - a.window + 1 : 0;
@@ -195,24 +201,30 @@ __device__ __forceinline__ float groups_max(float v) {
 // back out of the products, times scale * log2(e).  A negative scale is put
 // into the queries' signs, so that factor > 0 and the largest product has the
 // largest weight.
+// In two parts, so that other loads can go out before the first is waited for.
 template <int NB, int GS, int SS>
-__device__ __forceinline__ void load_query(const AttnArgs& a, const void* row, bool live, int g, half8_t (&q)[NB],
-                                           float& factor) {
+__device__ __forceinline__ void load_query(const AttnArgs& a, int64_t tok, int head, bool live, int g, u32x4 (&raw)[NB]) {
+  const uint16_t* row = (const uint16_t*)a.q + tok * a.q_stride + (int64_t)head * (32 * NB) + g * GS;
+#pragma unroll
+  for (int s = 0; s < NB; ++s) raw[s] = live ? *(const u32x4*)(row + s * SS) : u32x4{0, 0, 0, 0};
+}
+template <int NB>
+__device__ __forceinline__ void query_operands(const AttnArgs& a, const u32x4 (&raw)[NB], half8_t (&q)[NB],
+                                               float& factor) {
   const float log2e = 1.4426950408889634f;
   const bool neg = a.scale < 0.f;
   factor = fabsf(a.scale) * log2e;
   if (a.q_bf16) {
-    typedef __bf16 b8 __attribute__((ext_vector_type(8)));
     float v[NB][8], amax = 0.f;
 #pragma unroll
-    for (int s = 0; s < NB; ++s) {
-      const b8 r = live ? *(const b8*)((const __bf16*)row + g * GS + s * SS) : b8{};
+    for (int s = 0; s < NB; ++s)
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[s][i] = (float)r[i];
-        amax = fmaxf(amax, fabsf(v[s][i]));
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t w = raw[s][i];
+        v[s][2 * i] = __builtin_bit_cast(float, w << 16);
+        v[s][2 * i + 1] = __builtin_bit_cast(float, w & 0xFFFF0000u);
+        amax = fmaxf(amax, fmaxf(fabsf(v[s][2 * i]), fabsf(v[s][2 * i + 1])));
       }
-    }
     amax = groups_max(amax);
     // NaN and infinities keep their places; a row of zeros keeps its size
     int e = amax > 0.f && amax < __builtin_inff() ? (int)((__builtin_bit_cast(uint32_t, amax) >> 23) & 255u) - 127 : 14;
@@ -229,7 +241,8 @@ __device__ __forceinline__ void load_query(const AttnArgs& a, const void* row, b
   } else {
 #pragma unroll
     for (int s = 0; s < NB; ++s) {
-      half8_t h = live ? *(const half8_t*)((const half_t*)row + g * GS + s * SS) : half8_t{};
+      const u32x4 w = raw[s];
+      half8_t h = __builtin_bit_cast(half8_t, w);
       if (neg) h = -h;
       q[s] = query_order(h);
     }

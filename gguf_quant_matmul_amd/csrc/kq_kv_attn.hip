@@ -85,7 +85,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
   __shared__ float merge_m[WAVES][16], merge_l[WAVES][16];
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = blockIdx.x % a.hkv, wg = blockIdx.x / a.hkv;
+  const int h = blockIdx.x, wg = blockIdx.y + gridDim.y * blockIdx.z;
 
   // Where the workgroup begins: tile `sub` of request s, whose steps begin at
   // x among all (64-bit: garbage lengths may add up).  Steps x0 .. x1 - 1 are
@@ -93,7 +93,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
   int s = wg, sub = 0;
   uint64_t x = 0, x0 = 0, x1 = 0, share = 1;
   if (a.few_wgs == 0) {
-    if (!a.one_tile && !find_tile(a, wg, 16, 0, a.few_rows, s, sub)) return;
+    if (a.one_tile ? s >= a.n_seqs : !find_tile(a, wg, 16, 0, a.few_rows, s, sub)) return;
   } else {
     uint64_t total = 0;
     for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
@@ -157,10 +157,10 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
     {
       const int row = r0 + col;
       const bool live = row < rows;
-      const int tok = sq.row0 + row / a.group, head = h * a.group + row % a.group;
+      const int qt = token_of(a, row), tok = sq.row0 + qt, head = h * a.group + row - qt * a.group;
       // positions of this lane's row, of the tile's first and last
-      const int p = live ? sq.len - sq.n + row / a.group : -1;
-      const int p0 = sq.len - sq.n + r0 / a.group, p1 = sq.len - sq.n + r1 / a.group;
+      const int p = live ? sq.len - sq.n + qt : -1;
+      const int p0 = sq.len - sq.n + token_of(a, r0), p1 = sq.len - sq.n + token_of(a, r1);
       if (a.where && st0 == 0 && threadIdx.x < 16 && live) {
         int32_t* w = a.where + 2 * ((int64_t)tok * a.hq + head);
         w[0] = pieces > 1 ? -pieces : 0;
@@ -230,9 +230,16 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
       int ids[4], ids_next[4];
       page_ids(st0 + wave, ids);
       page_ids(st0 + wave + WAVES, ids_next);
+      u32x4 q_raw[NB];
+      load_query<NB, 8 * NB, 8>(a, tok, head, live, g, q_raw);
+      Groups gr = groups_of<D>(a, ids, keys.lo + (st0 + wave) * STEP, keys.end, h);
+      if (st0 + wave < st1) {
+        load_rows(a.kc, gr, kw, ks);
+        load_rows(a.vc, gr, vw, vs);
+      }
       half8_t q[NB];
       float factor;
-      load_query<NB, 8 * NB, 8>(a, (const uint16_t*)a.q + (int64_t)tok * a.q_stride + (int64_t)head * D, live, g, q, factor);
+      query_operands<NB>(a, q_raw, q, factor);
       // probabilities may reach 2^8 before the sums are brought to a new maximum
       const float slack = 8.f / factor;
 
@@ -242,11 +249,6 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
       float4_t l4 = {0, 0, 0, 0};
       float m = NEG_INF;
 
-      Groups gr = groups_of<D>(a, ids, keys.lo + (st0 + wave) * STEP, keys.end, h);
-      if (st0 + wave < st1) {
-        load_rows(a.kc, gr, kw, ks);
-        load_rows(a.vc, gr, vw, vs);
-      }
       for (int st = st0 + wave; st < st1; st += WAVES) {
         const int base = keys.lo + st * STEP;
         const uint32_t ok = gr.ok;
@@ -383,7 +385,8 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 4 ? 3 : 2) void attn_split_kernel
           v += f * *(const float4_t*)((const float*)(lds + w * REGION) + r * (D + 4) + c);
         }
         if (pieces == 1) {
-          const int64_t orow = (int64_t)(sq.row0 + (r0 + r) / a.group) * a.hq + h * a.group + (r0 + r) % a.group;
+          const int t = token_of(a, r0 + r);
+          const int64_t orow = (int64_t)(sq.row0 + t) * a.hq + h * a.group + r0 + r - t * a.group;
           store4(a.out, a.out_type, orow * D + c, v * (l == 0.f ? 0.f : 1.f / l));  // no key seen: zeros
         } else {
           const int64_t pr = (((int64_t)wg * a.hkv + h) * 2 + (st0 == 0 ? 1 : 0)) * 16 + r;
@@ -411,7 +414,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   const int per = a.d / 4, fit = 256 / per, k = threadIdx.x / per, c = (threadIdx.x % per) * 4;
   const int64_t row = SIDE ? blockIdx.x : (int64_t)blockIdx.x * fit + k;
   if (!SIDE && (k >= fit || row >= n_rows)) return;
-  const int tok = (int)(row / a.hq), h = (int)(row - (int64_t)tok * a.hq) / a.group;
+  const int tok = (int)(row / a.hq), h = token_of(a, (int)(row - (int64_t)tok * a.hq));  // (a head's kv head likewise)
   const int b = ((ConstInts)a.cu)[0], e = ((ConstInts)a.cu)[a.n_seqs];
   if (tok < b || tok >= e) return;  // no request's row: nothing was written for it
   int n = a.where[2 * row];
@@ -521,7 +524,8 @@ hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t
     if (e != hipSuccess) return e;
   }
   if (p.few_tiles > 0) {
-    const dim3 grid((unsigned)((a.few_wgs > 0 ? a.few_wgs : p.few_tiles) * a.hkv)), block(64 * WAVES);
+    const int64_t n = a.few_wgs > 0 ? a.few_wgs : p.few_tiles, gy = n < 32768 ? n : 32768;
+    const dim3 grid((unsigned)a.hkv, (unsigned)gy, (unsigned)((n + gy - 1) / gy)), block(64 * WAVES);
     const auto go = [&](auto kern) { hipLaunchKernelGGL(kern, grid, block, 0, s, a); };
     switch (a.d / 32) {
       case 1: go(attn_split_kernel<1>); break;

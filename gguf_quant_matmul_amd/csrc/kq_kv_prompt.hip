@@ -55,21 +55,19 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
 
   // the wave's rows: positions of its first and last, none if w0 > w1
   const int w0 = r0 + wave * C * 16, w1 = w0 + C * 16 - 1 < rows ? w0 + C * 16 - 1 : rows - 1;
-  const int p0 = sq.len - sq.n + w0 / a.group, p1 = w0 <= w1 ? sq.len - sq.n + w1 / a.group : -1;
+  const int p0 = sq.len - sq.n + token_of(a, w0), p1 = w0 <= w1 ? sq.len - sq.n + token_of(a, w1) : -1;
   int64_t orow[C];
   int p[C];
   bool live[C];
-  half8_t q[C][NB];
-  float factor[C];
+  u32x4 q_raw[C][NB];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
     const int row = w0 + 16 * c + col;
     live[c] = row < rows;
-    const int tok = sq.row0 + row / a.group, head = h * a.group + row % a.group;
+    const int qt = token_of(a, row), tok = sq.row0 + qt, head = h * a.group + row - qt * a.group;
     orow[c] = (int64_t)tok * a.hq + head;
-    p[c] = live[c] ? sq.len - sq.n + row / a.group : -1;
-    load_query<NB, 8, 32>(a, (const uint16_t*)a.q + (int64_t)tok * a.q_stride + (int64_t)head * D, live[c], g, q[c],
-                          factor[c]);
+    p[c] = live[c] ? sq.len - sq.n + qt : -1;
+    load_query<NB, 8, 32>(a, tok, head, live[c], g, q_raw[c]);
   }
   if (split >= (n_split > 0 ? n_split : 1)) return;
   if (a.where && split == 0 && g == 0) {
@@ -190,6 +188,10 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
     }
   };
 
+  half8_t q[C][NB];
+  float factor[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) query_operands<NB>(a, q_raw[c], q[c], factor[c]);
   float4_t o[DT][C], l4[C];
   float m[C], slack[C];
 #pragma unroll
