@@ -429,6 +429,7 @@ struct AttnArgs {
 // How a call's work is split, from its host-known sizes alone.
 struct AttnPlan {
   int few_rows, one_tile, few_wgs, splits, chunk;
+  int more_waves;                 // eight-wave workgroups for the 16-row tiles
   int64_t few_tiles, many_tiles;  // 16-row and prompt tiles (bounds; 0: that kernel does not run)
   int64_t few_at, where_at;       // byte offsets into the workspace
   int64_t bytes;                  // workspace
