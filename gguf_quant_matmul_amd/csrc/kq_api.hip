@@ -477,7 +477,7 @@ int kq_gather_qmm_seg_bf16(int codec, const void* w, int64_t n_experts, int64_t 
 // ---- key/value cache in 4 bits ----
 namespace {
 
-constexpr int64_t kMaxSeqs = (int64_t)1 << 20;
+constexpr int64_t kMaxSeqs = 65536;
 
 // codec, page, row size and kv heads of a cache; fills log2(page)
 int check_cache(const char* op, int codec, int64_t page, int64_t d, int64_t heads, int* shift) {
@@ -604,6 +604,11 @@ int kq_kv_store(int codec, const void* k, const void* v, int x_dtype, int64_t to
   if (!k || !v || !slots) return fail(KQ_ERR_ARG, op, "null pointer (k=%p v=%p slots=%p)", k, v, (const void*)slots);
   if (!aligned(k, 16) || !aligned(v, 16)) return fail(KQ_ERR_ALIGN, op, "k=%p, v=%p are not 16-byte aligned", k, v);
   if (!aligned(slots, 4)) return fail(KQ_ERR_ALIGN, op, "slots=%p is not 4-byte aligned", (const void*)slots);
+  const int64_t es = elem_bytes(x_dtype), row = kv_heads * d;
+  for (const void* c : {k_cache, v_cache})
+    if (overlaps(k, ((tokens - 1) * k_stride + row) * es, c, cache) ||
+        overlaps(v, ((tokens - 1) * v_stride + row) * es, c, cache) || overlaps(slots, 4 * tokens, c, cache))
+      return fail(KQ_ERR_ARG, op, "k, v or slots overlap a cache");
   return hip_status(op, kq::launch_kv_store(k, v, elem_id(x_dtype), tokens, kv_heads, d, k_stride, v_stride, slots,
                                             (uint8_t*)k_cache, (uint8_t*)v_cache, pages, shift, (hipStream_t)stream));
 }
@@ -623,6 +628,10 @@ int kq_kv_load(int codec, const void* k_cache, const void* v_cache, int64_t page
   if (!aligned(slots, 4)) return fail(KQ_ERR_ALIGN, op, "slots=%p is not 4-byte aligned", (const void*)slots);
   const int64_t bytes = tokens * kv_heads * d * elem_bytes(out_dtype);
   if (overlaps(k, bytes, v, bytes)) return fail(KQ_ERR_ARG, op, "k and v overlap");
+  const int64_t cache = pages * kv_heads * page * (d / 2 + d / 16);
+  for (const void* o : {k, v})
+    if (overlaps(o, bytes, k_cache, cache) || overlaps(o, bytes, v_cache, cache) || overlaps(o, bytes, slots, 4 * tokens))
+      return fail(KQ_ERR_ARG, op, "k or v overlaps a cache or slots");
   return hip_status(op, kq::launch_kv_load((const uint8_t*)k_cache, (const uint8_t*)v_cache, pages, shift, kv_heads, d,
                                            slots, tokens, k, v, elem_id(out_dtype), (hipStream_t)stream));
 }
@@ -667,8 +676,14 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
   if (!aligned(cu_new, 4) || !aligned(seq_lens, 4) || !aligned(table, 4))
     return fail(KQ_ERR_ALIGN, op, "cu_new, seq_lens and table must be 4-byte aligned");
   const int64_t out_bytes = tokens * q_heads * d * elem_bytes(out_dtype);
-  if (overlaps(q, ((tokens - 1) * q_stride + q_heads * d) * 2, out, out_bytes))
-    return fail(KQ_ERR_ARG, op, "out overlaps q");
+  // what the call reads, against what it writes
+  const int64_t cache = pages * kv_heads * page * (d / 2 + d / 16);
+  const struct { const char* name; const void* p; int64_t bytes; } in[] = {
+      {"q", q, ((tokens - 1) * q_stride + q_heads * d) * 2}, {"cu_new", cu_new, 4 * (n_seqs + 1)},
+      {"seq_lens", seq_lens, 4 * n_seqs}, {"table", table, 4 * n_seqs * width}, {"k_cache", k_cache, cache},
+      {"v_cache", v_cache, cache}};
+  for (const auto& r : in)
+    if (r.bytes > 0 && overlaps(r.p, r.bytes, out, out_bytes)) return fail(KQ_ERR_ARG, op, "out overlaps %s", r.name);
   const kq::AttnPlan plan = kq::attn_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv, window);
   if (plan.bytes > 0) {
     if (!workspace || workspace_bytes < plan.bytes)
@@ -676,6 +691,9 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
                   (long long)(workspace ? workspace_bytes : 0), (long long)plan.bytes);
     if (!aligned(workspace, 16)) return fail(KQ_ERR_ALIGN, op, "workspace=%p is not 16-byte aligned", workspace);
     if (overlaps(workspace, plan.bytes, out, out_bytes)) return fail(KQ_ERR_ARG, op, "workspace overlaps out");
+    for (const auto& r : in)
+      if (r.bytes > 0 && overlaps(r.p, r.bytes, workspace, plan.bytes))
+        return fail(KQ_ERR_ARG, op, "workspace overlaps %s", r.name);
   }
   kq::AttnArgs a;
   a.q = q;

@@ -309,8 +309,9 @@ int kq_kv_page_bytes(int codec, int64_t page, int64_t d, int64_t* page_bytes);
  * A request refused for its width, rows or lengths takes no pages; once
  * pages run out, later requests that need any are refused too.  Ids read
  * from the table and the free list are not checked here: a token whose page
- * id is negative, or whose slot does not fit 31 bits, gets slot -1.  Outputs
- * must not overlap inputs or each other (KQ_ERR_ARG). */
+ * id is negative, or whose slot does not fit 31 bits, gets slot -1.  At most
+ * 65536 requests.  Outputs must not overlap inputs or each other
+ * (KQ_ERR_ARG). */
 int kq_block_tables(const int32_t* ctx_lens, const int32_t* new_lens, int64_t n_seqs, int64_t page,
                     const int32_t* free_pages, int64_t n_free, const int32_t* free_head,
                     int32_t* table, int64_t width, int32_t* slots, int64_t tokens, int32_t* cu_new,
@@ -330,7 +331,8 @@ int kq_block_tables(const int32_t* ctx_lens, const int32_t* new_lens, int64_t n_
  * [tokens][kv_heads][d] dense; each is D * (c - 8), rounded once.  Rows whose
  * slot is outside the cache are left unwritten.
  * k, v are 16-byte aligned, strides multiples of 8 elements and >=
- * kv_heads * d (KQ_ERR_ALIGN, KQ_ERR_SHAPE). */
+ * kv_heads * d (KQ_ERR_ALIGN, KQ_ERR_SHAPE); tokens * kv_heads * d is below
+ * 2^34; what a call writes must not overlap what it reads (KQ_ERR_ARG). */
 int kq_kv_store(int codec, const void* k, const void* v, int x_dtype, int64_t tokens, int64_t kv_heads, int64_t d,
                 int64_t k_stride, int64_t v_stride, const int32_t* slots, void* k_cache, void* v_cache,
                 int64_t pages, int64_t page, void* stream);
@@ -363,9 +365,14 @@ int kq_kv_load(int codec, const void* k_cache, const void* v_cache, int64_t page
  * workspace (16-byte aligned) holds partial results where the keys of a row
  * are split over workgroups: kq_kv_attention_workspace gives its bytes (0:
  * none needed, workspace may be NULL; KQ_ERR_CAPACITY if it is too small) for
- * the same sizes.  Its contents mean nothing between calls; calls that may run
- * at the same time need one each.  Results are deterministic for given sizes
- * and lengths. */
+ * the same sizes, whatever the window.  Its contents mean nothing between
+ * calls; calls that may run at the same time need one each.  Results are
+ * deterministic for given sizes, bounds and lengths; how a row's keys are split,
+ * and so the last bits of its result, goes by the whole batch's lengths.
+ * q_heads and kv_heads are at most 4096, tokens * q_heads below 2^25, n_seqs
+ * at most 65536 and n_seqs * kv_heads below 2^22, width * page below 2^30.
+ * out and workspace must not overlap what is read, or each other
+ * (KQ_ERR_ARG). */
 int kq_kv_attention_workspace(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d,
                               int64_t max_new, int64_t max_kv, int64_t* bytes);
 int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64_t q_heads, int64_t kv_heads,

@@ -324,6 +324,77 @@ def test_drafts_and_bounds_that_do_not_hold(kq):
     _check(kq, c, "bounds of one token and one key", "f16", max_new=1, max_kv=1)
 
 
+@pytest.mark.parametrize("d, hq, kv, page", [(64, 4, 2, 16), (128, 8, 2, 128), (96, 3, 3, 64), (256, 4, 2, 4096)])
+def test_shared_steps_of_many_requests(kq, d, hq, kv, page):
+    # more than 64 requests whose steps are shared out evenly, idle ones among them, first and last included
+    rng = np.random.default_rng(160 + d)
+    n = 90
+    lens = rng.integers(0, 300, n)
+    lens[[0, 1, 40, 41, 42, 89]] = 0
+    lens[[7, 50]] = [1500, 2300]
+    c = _case(160 + d, rng.integers(0, 3, n), lens, hq, kv, d, page, "bf16" if d == 96 else "f16", extra_tokens=2)
+    _check(kq, c, "shared", "f32", max_new=2, max_kv=2300)
+    _check(kq, c, "bounds that do not hold", "f16", max_new=1, max_kv=1025)
+    _check(kq, c, "uniform", "f32", scale=0.0, max_new=2, max_kv=100000)
+
+
+def test_shared_steps_of_rows_past_the_bound(kq):
+    c = _case(170, [40, 1, 70, 5], [1400, 30, 900, 5], 8, 2, 64, 16)
+    _check(kq, c, "16-row tiles of long requests", "f16", max_new=1, max_kv=1400)
+    _check(kq, c, "window", "f16", max_new=1, max_kv=1400, window=1100)
+
+
+def test_more_requests_than_share_steps(kq):
+    rng = np.random.default_rng(171)
+    lens = rng.integers(0, 40, 1100)
+    lens[5] = 1300
+    _check(kq, _case(171, [1] * 1100, lens, 2, 1, 32, 16), "one workgroup to a request", "f16", max_new=1, max_kv=1300)
+
+
+@pytest.mark.parametrize("d, hq, kv, q_dtype", [(128, 8, 1, "f16"), (64, 7, 1, "bf16"), (256, 4, 1, "f16"), (160, 3, 1, "bf16")])
+def test_prompts_whose_keys_are_split(kq, d, hq, kv, q_dtype):
+    # prompt tiles and 16-row tiles in one batch, both with shared keys
+    c = _case(180 + d, [20, 1, 45, 2, 0, 33], [2500, 1700, 45, 2100, 10, 1300], hq, kv, d, 64, q_dtype, extra_tokens=1)
+    _check(kq, c, "split", q_dtype, max_new=45, max_kv=2500)
+    _check(kq, c, "split, wide bound", "f32", max_new=45, max_kv=200000)
+    _check(kq, c, "window", q_dtype, max_new=45, max_kv=2500, window=700)
+    _check(kq, c, "uniform", "f32", scale=0.0, max_new=45, max_kv=2500)
+
+
+@pytest.mark.parametrize("d, hq, kv, n", [(128, 4, 1, 200), (128, 16, 2, 70), (192, 5, 1, 130), (32, 1, 1, 300)])
+def test_prompts_over_several_tiles(kq, d, hq, kv, n):
+    c = _case(190 + d + n, [n], [n + 77], hq, kv, d, 32)
+    _check(kq, c, "prompt", "f16", max_new=n, max_kv=n + 77)
+    _check(kq, c, "window", "f32", max_new=n, max_kv=n + 77, window=50)
+    c = _case(191 + d + n, [n], [n], hq, kv, d, 32, "bf16")
+    _check(kq, c, "from the first token", "bf16", max_new=n, max_kv=n)
+
+
+def test_strided_queries_and_results_repeat(kq):
+    import torch
+
+    c = _case(200, [1, 60, 1, 4], [3000, 900, 1, 1200], 6, 3, 128, 16)
+    wide = torch.full((66, 14, 128), 3.0, dtype=torch.float16, device="cuda")
+    wide[:, 5:11] = c["q"]
+    first = None
+    for q in (c["q"], wide[:, 5:11]):
+        for _ in range(3):
+            got = _attn(kq, dict(c, q=q), "f16", max_new=60, max_kv=3000)
+            first = got.clone() if first is None else first
+            assert torch.equal(got, first)
+
+
+def test_workspace_that_is_too_small(kq):
+    import torch
+
+    c = _case(210, [1, 1], [3000, 900], 4, 2, 64, 16)
+    with pytest.raises(kq.KQError) as e:
+        _attn(kq, c, "f16", max_new=1, max_kv=3000, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == kq.KQ_ERR_CAPACITY
+    with pytest.raises(ValueError, match="cu_new has 2"):
+        _attn(kq, dict(c, cu=c["cu"][:2]), "f16", max_new=1, max_kv=3000)
+
+
 def test_signs_and_sizes_of_scale_and_queries(kq):
     for q_dtype, q_scale, scale in (("f16", 1.0, -0.2), ("bf16", 1e-20, 1e19), ("bf16", 1e20, 1e-21), ("bf16", 300.0, -1e-3),
                                     ("f16", 1e-3, 50.0), ("bf16", 1.0, 1e-38)):

@@ -89,6 +89,13 @@ ARG, CODEC, SHAPE, ALIGN, CAP = kq.KQ_ERR_ARG, kq.KQ_ERR_CODEC, kq.KQ_ERR_SHAPE,
     (load, dict(v=ADDR["k"] + 16), ARG, "overlap"),
     (load, dict(k=ADDR["k"] + 4), ALIGN, "16-byte"),
     (load, dict(slots=None), ARG, "null"),
+    (tables, dict(n=65537), ARG, "n_seqs"),
+    (store, dict(kc=ADDR["k"] + 64), ARG, "overlap a cache"),
+    (store, dict(slots=ADDR["vc"] + 4), ARG, "overlap a cache"),
+    (load, dict(k=ADDR["vc"] + 16), ARG, "overlaps a cache"),
+    (attn, dict(out=ADDR["kc"] + 16), ARG, "out overlaps k_cache"),
+    (attn, dict(table=ADDR["out"] + 16), ARG, "out overlaps table"),
+    (attn, dict(max_kv=1 << 20, q=ADDR["ws"] + 4096, ws_bytes=1 << 40), ARG, "workspace overlaps q"),
     (attn, dict(codec=3), CODEC, "q4_0"),
     (attn, dict(qdt=0), ARG, "query dtype"),
     (attn, dict(odt=4), ARG, "output dtype"),
