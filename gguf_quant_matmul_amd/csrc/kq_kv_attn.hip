@@ -23,6 +23,8 @@
 // mantissa, times the block's scale.
 #include "kq_kv_attn.h"
 
+#include <math.h>
+
 namespace kq {
 namespace {
 
@@ -491,10 +493,13 @@ AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_h
   if (window > 0 && window + max_new < max_kv) max_kv = window + max_new;
   const int64_t group = q_heads / kv_heads, most = (max_new < tokens ? max_new : tokens) * group;
   p.one_tile = most <= 16;
-  // Which kernels run.  Requests of few rows only: 16-row tiles.  One request
-  // of many rows: prompt tiles.  Else each request goes where its rows fit.
-  p.few_rows = most <= 64 ? 0x7FFFFFFF : n_seqs == 1 ? 0 : FEW_ROWS;
   const int64_t all = tokens * group;
+  // Which kernels run.  Few rows a request, or short requests whose 16-row
+  // tiles have CUs to themselves (100 tokens, 8 kv heads: 10 us against 15):
+  // 16-row tiles.  One request of many rows: prompt tiles.  Else each request
+  // goes where its rows fit.
+  const bool brief = max_kv <= 512 && (all / 16 + n_seqs) * kv_heads <= 512;
+  p.few_rows = most <= 64 || brief ? 0x7FFFFFFF : n_seqs == 1 ? 0 : FEW_ROWS;
   p.few_tiles = p.one_tile ? n_seqs : p.few_rows == 0 ? 0 : all / 16 + n_seqs;
   if (p.few_rows == FEW_ROWS && p.few_tiles > n_seqs * (FEW_ROWS / 16)) p.few_tiles = n_seqs * (FEW_ROWS / 16);
   const int tile = attn_prompt_rows(d);
@@ -509,19 +514,25 @@ AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_h
     p.few_wgs = (int)((at_once + kv_heads - 1) / kv_heads);
   // eight waves to a workgroup where each has a CU or so to itself
   p.more_waves = p.few_wgs == 0 && p.few_tiles * kv_heads <= 512 && max_kv > STEP * WAVES;
-  // prompt tiles: one workgroup to a CU.  Split rows write and read float32
-  // sums, which costs as much as some 500 keys: 1024 keys at least where tiles
-  // alone leave a good part of the CUs idle, 4096 where unequal ones might
+  // Prompt tiles: one workgroup to a CU, some 2 us a step.  Where they leave
+  // CUs idle, a tile's keys are split over `n` workgroups: steps / n * 2 us,
+  // plus float32 sums of n * rows * d written and read at 4 TB/s, least at n =
+  // sqrt(2 us steps / (2 us rows d / 10^6)).  And 4096 keys at most where
+  // unequal requests might leave a few tiles to the end.  (Each is a growing
+  // function of max_kv, so that the workspace is.)
   p.splits = 1;
-  p.chunk = 0x7FFFFFFF;
   if (p.many_tiles > 0) {
-    const int64_t wgs = p.many_tiles * kv_heads, want = (256 + wgs - 1) / wgs;
-    int64_t chunk = wgs >= 1024 ? max_kv : wgs >= 192 ? 4096 : (max_kv + want - 1) / want;
-    chunk = chunk < 1024 ? 1024 : wgs < 1024 && chunk > 4096 ? 4096 : chunk;
-    p.chunk = (int)(chunk < 0x7FFFFFC0 ? (chunk + 63) / 64 * 64 : 0x7FFFFFC0);
-    const int64_t n = (max_kv + p.chunk - 1) / p.chunk;
+    const int64_t wgs = p.many_tiles * kv_heads, steps = (max_kv + STEP - 1) / STEP;
+    int64_t n = 256 / wgs;
+    const int64_t best = (int64_t)sqrt(1e6 * (double)steps / ((double)tokens * q_heads * d));
+    n = n < best ? n : best;
+    n = n < steps / 2 ? n : steps / 2;
+    const int64_t equal = wgs < 1024 ? (max_kv + 4095) / 4096 : 1;
+    n = n > equal ? n : equal;
     p.splits = (int)(n < 1 ? 1 : n > 64 ? 64 : n);
   }
+  const int64_t chunk = (max_kv + p.splits - 1) / p.splits;
+  p.chunk = (int)(chunk < 0x7FFFFFC0 ? (chunk + STEP - 1) / STEP * STEP : 0x7FFFFFC0);
   const int64_t many = p.splits > 1 ? tokens * q_heads * p.splits : 0, few = (int64_t)p.few_wgs * kv_heads * 32;
   p.few_at = many * (d + 2) * 4;
   p.where_at = p.few_at + few * (d + 2) * 4;
