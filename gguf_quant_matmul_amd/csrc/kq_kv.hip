@@ -73,6 +73,7 @@ __global__ __launch_bounds__(BT_THREADS) void block_tables_kernel(
     total = (int)t;
     return (uint32_t)(t - h);
   };
+  const int64_t head = free_head[0];
   uint32_t rows = 0, need = 0;
   for (int s = s0; s < s1; ++s) {
     const int c = ctx_lens[s], n = new_lens[s];
@@ -81,7 +82,6 @@ __global__ __launch_bounds__(BT_THREADS) void block_tables_kernel(
     need = add_sat(need, want(c, n, held, total, bad));
     rows = add_sat(rows, n > 0 ? n : 0);
   }
-  const int64_t head = free_head[0];
   const uint32_t rows_incl = wave_scan_sat(rows), need_incl = wave_scan_sat(need);
   if (lane == 63) { wrows[wave] = rows_incl; wneed[wave] = need_incl; }
   __syncthreads();
@@ -113,17 +113,17 @@ __global__ __launch_bounds__(BT_THREADS) void block_tables_kernel(
     row = end;
   }
   if (blockIdx.x == 0 && blockIdx.y == 0) {
+    // (sums only grow, so the last lane that took pages has the wave's count)
+    const uint64_t took = __ballot(taken > 0);
+    const uint32_t most = took ? __builtin_amdgcn_readlane(taken, 63 - __builtin_clzll(took)) : 0u;
+    uint32_t all = 0;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) {
-      flags |= __shfl_xor(flags, o, 64);
-      const uint32_t t = __shfl_xor(taken, o, 64);
-      taken = t > taken ? t : taken;
-    }
-    if (lane == 0) { wflag[wave] = flags; wtaken[wave] = taken; }
+    for (int i = 0; i < 4; ++i) all |= __ballot(flags >> i & 1u) ? 1u << i : 0u;
+    if (lane == 0) { wflag[wave] = all; wtaken[wave] = most; }
   }
   __syncthreads();
   if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
-    for (int w = 1; w < BT_WAVES; ++w) {
+    for (int w = 0; w < BT_WAVES; ++w) {
       flags |= wflag[w];
       taken = wtaken[w] > taken ? wtaken[w] : taken;
     }
