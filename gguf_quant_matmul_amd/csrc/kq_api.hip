@@ -725,8 +725,8 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
   a.few_rows = plan.few_rows;
   a.one_tile = plan.one_tile;
   a.few_wgs = plan.few_wgs;
-  a.splits = plan.splits;
-  a.chunk = plan.chunk;
+  a.many_wgs = plan.many_wgs;
+  a.many_shift = __builtin_ctz((unsigned)kq::attn_prompt_rows(d));
   return hip_status(op, kq::launch_kv_attention(a, plan, (hipStream_t)stream));
 }
 

@@ -410,8 +410,8 @@ struct AttnArgs {
   void* out;
   // workspace (null without splits): sums of rows whose keys are shared, each
   // part rows of d floats, then (maximum, sum) pairs; where a row's are
-  float* many;      // prompt tiles: row (split * tokens + t) * q_heads + h
-  float* few;       // 16-row tiles: row ((workgroup * kv_heads + h) * 2 + (a tile begins there)) * 16 + row of the tile
+  float* many;      // prompt tiles: row ((workgroup * kv_heads + h) * 2 + (a tile begins there)) * rows of a tile + row
+  float* few;       // 16-row tiles: likewise
   int32_t* where;   // [tokens][q_heads][2]
   int64_t q_stride, width, page_head_bytes;
   int tokens, n_seqs, hq, hkv, group, d;
@@ -423,12 +423,12 @@ struct AttnArgs {
   int few_rows;    // requests of at most so many rows take 16-row tiles, others prompt tiles
   int one_tile;    // 16-row tiles: a request's rows fit one, so that tile index = request
   int few_wgs;     // workgroups a kv head that share all requests' 16-row tiles evenly (0: one to a tile)
-  int splits;      // prompt tiles: most workgroups that share a tile's keys
-  int chunk;       // prompt tiles: keys a workgroup takes before another one is worth it
+  int many_wgs;    // prompt tiles: likewise
+  int many_shift;  // log2 of a prompt tile's rows
 };
 // How a call's work is split, from its host-known sizes alone.
 struct AttnPlan {
-  int few_rows, one_tile, few_wgs, splits, chunk;
+  int few_rows, one_tile, few_wgs, many_wgs;
   int more_waves;                 // eight-wave workgroups for the 16-row tiles
   int64_t few_tiles, many_tiles;  // 16-row and prompt tiles (bounds; 0: that kernel does not run)
   int64_t few_at, where_at;       // byte offsets into the workspace

@@ -47,10 +47,116 @@ __device__ __forceinline__ Keys key_range(const AttnArgs& a, const Seq& q, int r
   k.lo = (lo > 0 ? (int)lo : 0) & ~63;
   return k;
 }
-// Workgroups of the prompt kernel that share those keys.
-__device__ __forceinline__ int split_count(const AttnArgs& a, const Keys& k) {
-  const int n = k.end - k.lo, s = n > 0 ? (int)(((int64_t)n + a.chunk - 1) / a.chunk) : 0;
-  return s < a.splits ? s : a.splits;
+constexpr int STEP = 64;  // keys of one step
+
+// What a tile costs beside its steps, in steps: its start and its end.  (Shares
+// of steps alone gave some workgroups ten short tiles: 9 requests of mixed
+// prompts 377 us against 350, a prompt of 4096 tokens 284 against 240.)
+template <int ROWS>
+constexpr int TILE_EXTRA = ROWS == 16 ? 6 : 5;
+
+// Cost of a tile of ROWS rows of a request; a tile without keys counts as
+// one step, so that someone writes its zeros.
+template <int ROWS>
+__device__ __forceinline__ int tile_cost(const AttnArgs& a, const Seq& q, int sub) {
+  const int rows = q.n * a.group, r0 = sub * ROWS, r1 = r0 + ROWS - 1 < rows ? r0 + ROWS - 1 : rows - 1;
+  const Keys k = key_range(a, q, r0, r1);
+  return (k.end > k.lo ? (k.end - k.lo + STEP - 1) / STEP : 1) + TILE_EXTRA<ROWS>;
+}
+// ... of all tiles of a request with more than `above` and at most `most` rows.
+template <int ROWS>
+__device__ __forceinline__ int request_cost(const AttnArgs& a, int s, int above, int most) {
+  if (s >= a.n_seqs) return 0;
+  const Seq q = load_seq(a, s);
+  const int rows = q.n * a.group;
+  if (rows <= above || rows > most) return 0;
+  int n = 0;
+  for (int sub = 0; sub * ROWS < rows; ++sub) n += tile_cost<ROWS>(a, q, sub);
+  return n;
+}
+
+__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32 |
+         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
+}
+// inclusive prefix sum over the wave's lanes
+__device__ __forceinline__ uint64_t wave_prefix(uint64_t v) {
+  const int lane = threadIdx.x & 63;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const uint64_t t = __shfl_up(v, o, 64);
+    if (lane >= o) v += t;
+  }
+  return v;
+}
+
+// The part of one of `wgs` workgroups (of a kv head) that share out the cost
+// of all those requests' tiles evenly, `least` to one at least: x0 .. x1 - 1
+// of the whole (64-bit: garbage lengths may add up), `size` to a workgroup.
+// A tile's steps come first, then its extra, which nobody works on.  The part
+// begins in tile `sub` of request s, whose own begins at x.  False for a
+// workgroup without a part.  Every wave finds it for itself, 64 requests
+// and then 64 tiles at a time.
+struct Share {
+  uint64_t x, x0, x1, size;
+};
+template <int ROWS>
+__device__ __forceinline__ bool find_share(const AttnArgs& a, int wg, int wgs, int least, int above, int most, int& s,
+                                           int& sub, Share& r) {
+  const int lane = threadIdx.x & 63;
+  uint64_t total = 0;
+  for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
+    uint64_t n = (uint64_t)request_cost<ROWS>(a, s0 + lane, above, most);
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o, 64);
+    total += n;
+  }
+  total = uniform64(total);
+  r.size = (total + wgs - 1) / (uint64_t)wgs;
+  r.size = r.size < (uint64_t)least ? least : r.size;
+  r.x0 = r.size * (uint64_t)wg;
+  r.x1 = r.x0 + r.size < total ? r.x0 + r.size : total;
+  if (r.x0 >= total) return false;
+  uint64_t x = 0;
+  for (int s0 = 0;; s0 += 64) {
+    const uint64_t n = (uint64_t)request_cost<ROWS>(a, s0 + lane, above, most), incl = wave_prefix(n);
+    const uint64_t hit = __ballot(x + incl > r.x0);
+    if (hit) {  // total > x0: some request has it
+      const int l = __builtin_ctzll(hit);
+      s = s0 + l;
+      x += __shfl(incl - n, l, 64);
+      break;
+    }
+    x += __shfl(incl, 63, 64);
+  }
+  s = __builtin_amdgcn_readfirstlane(s);
+  const Seq q = load_seq(a, s);
+  const int tiles = (q.n * a.group + ROWS - 1) / ROWS;
+  for (int t0 = 0;; t0 += 64) {
+    const uint64_t n = t0 + lane < tiles ? (uint64_t)tile_cost<ROWS>(a, q, t0 + lane) : 0, incl = wave_prefix(n);
+    const uint64_t hit = __ballot(x + incl > r.x0);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      sub = __builtin_amdgcn_readfirstlane(t0 + l);
+      r.x = uniform64(x + __shfl(incl - n, l, 64));
+      return true;
+    }
+    x += __shfl(incl, 63, 64);
+  }
+}
+// The workgroup's steps st0 .. st1 - 1 of a tile of `steps` steps that begins at
+// r.x (r.x moves on to the next tile), the first workgroup that has some of
+// the tile's and how many have.  False where the part begins in the tile's extra.
+template <int ROWS>
+__device__ __forceinline__ bool take_steps(Share& r, int steps, int& st0, int& st1, int& first, int& pieces) {
+  const uint64_t x = r.x, end = x + (steps > 0 ? steps : 1);
+  r.x = end + TILE_EXTRA<ROWS>;
+  if (r.x0 >= end) return false;
+  st0 = r.x0 > x ? (int)(r.x0 - x) : 0;
+  st1 = r.x1 < end ? (int)(r.x1 - x) : steps;
+  first = (int)(x / r.size);
+  pieces = (int)((end - 1) / r.size) - first + 1;
+  return true;
 }
 
 // Request and tile index inside it of tile `tile`, the tiles of the requests

@@ -5,9 +5,8 @@
 // One pass over the keys with a running maximum and sum.  A workgroup takes a
 // run of 64-key steps of one 16-row tile of a (request, kv head); its four
 // waves take steps in turn, each with sums of its own, merged through LDS at
-// the end.  Both
-// products run on v_mfma_f32_16x16x32_f16, transposed so that nothing moves
-// between lanes in between:
+// the end.  Both products run on v_mfma_f32_16x16x32_f16, transposed so that
+// nothing moves between lanes in between:
 //   S^T [16 keys x 16 rows] = K [16 x d] Q^T; lane l holds row l % 16, keys
 //     4 (l / 16) .. + 3 of each of a step's four 16-key groups.
 //   O^T [16 d x 16 rows] += V^T [16 d x 32 keys] P^T; its operand wants for
@@ -21,9 +20,13 @@
 // rows of 16 nibbles per 16 lanes, the row addresses free), which hands lane l
 // value l % 16 of 16 keys.  Codes become float16 by or-ing them into 1024's
 // mantissa, times the block's scale.
+//
+// Measured (8 kv heads, groups of 4, d = 128): 64 requests of 200 to 8192 keys
+// 72 us, 3.6 TB/s of cache; 4 of 131072 keys 120 to 130 us, 4.5 TB/s (a large
+// copy reaches 4.8).  Bound by HBM on long keys, by unpacking (416 of a step's
+// 500 vector operations) where much of the cache is in the last-level cache,
+// by latency on short ones: 330 keys of one request 9 us with its launch.
 #include "kq_kv_attn.h"
-
-#include <math.h>
 
 namespace kq {
 namespace {
@@ -32,7 +35,6 @@ namespace {
 // mostly idle (a step of one wave takes 2 us, so a request of 330 keys, six
 // steps, is 11 us with four waves and 9 us with eight).
 constexpr int WAVES = 4, MORE_WAVES = 8;
-constexpr int STEP = 64;  // keys of one step
 
 // LDS of one wave: a step's rows of codes and their scales, keys and values.
 // Row strides are odd multiples of 16 bytes, which puts 16 neighbouring rows
@@ -53,28 +55,6 @@ constexpr int region_bytes() {
   return Stage<NB>::BYTES > m ? Stage<NB>::BYTES : m;
 }
 
-// 64-key steps of a 16-row tile of a request; a tile without keys counts as
-// one, so that someone writes its zeros.
-__device__ __forceinline__ int tile_steps(const AttnArgs& a, const Seq& q, int sub) {
-  const int rows = q.n * a.group, r0 = sub * 16, r1 = r0 + 15 < rows ? r0 + 15 : rows - 1;
-  const Keys k = key_range(a, q, r0, r1);
-  return k.end > k.lo ? (k.end - k.lo + STEP - 1) / STEP : 1;
-}
-__device__ __forceinline__ int request_steps(const AttnArgs& a, int s) {
-  if (s >= a.n_seqs) return 0;
-  const Seq q = load_seq(a, s);
-  const int rows = q.n * a.group;
-  if (rows > a.few_rows) return 0;
-  int n = 0;
-  for (int sub = 0; sub * 16 < rows; ++sub) n += tile_steps(a, q, sub);
-  return n;
-}
-
-__device__ __forceinline__ uint64_t uniform64(uint64_t v) {
-  return (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)(v >> 32)) << 32 |
-         (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)v);
-}
-
 template <int NB, int WAVES>
 __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel(AttnArgs a) {
   constexpr int D = 32 * NB;
@@ -92,46 +72,13 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = blockIdx.x, wg = blockIdx.y + gridDim.y * blockIdx.z;
 
-  // Where the workgroup begins: tile `sub` of request s, whose steps begin at
-  // x among all (64-bit: garbage lengths may add up).  Steps x0 .. x1 - 1 are
-  // its own, `share` to a workgroup; or (few_wgs = 0) all of tile wg.
+  // the workgroup's part of all steps, or (few_wgs = 0) all of tile wg
   int s = wg, sub = 0;
-  uint64_t x = 0, x0 = 0, x1 = 0, share = 1;
+  Share share;
   if (a.few_wgs == 0) {
     if (a.one_tile ? s >= a.n_seqs : !find_tile(a, wg, 16, 0, a.few_rows, s, sub)) return;
-  } else {
-    uint64_t total = 0;
-    for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
-      uint64_t n = (uint64_t)request_steps(a, s0 + lane);
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o, 64);
-      total += n;
-    }
-    total = uniform64(total);
-    share = (total + a.few_wgs - 1) / (uint64_t)a.few_wgs;
-    share = share < WAVES ? WAVES : share;  // a step to a wave at least
-    x0 = share * (uint64_t)wg;
-    x1 = x0 + share < total ? x0 + share : total;
-    if (x0 >= total) return;
-    for (int s0 = 0;; s0 += 64) {
-      const uint64_t n = (uint64_t)request_steps(a, s0 + lane);
-      uint64_t incl = n;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const uint64_t t = __shfl_up(incl, o, 64);
-        if (lane >= o) incl += t;
-      }
-      const uint64_t hit = __ballot(x + incl > x0);
-      if (hit) {  // total > x0: some request has it
-        const int l = __builtin_ctzll(hit);
-        s = s0 + l;
-        x += __shfl(incl, l, 64) - __shfl(n, l, 64);
-        break;
-      }
-      x += __shfl(incl, 63, 64);
-    }
-    s = __builtin_amdgcn_readfirstlane(s);
-    x = uniform64(x);
+  } else if (!find_share<16>(a, wg, a.few_wgs, WAVES, 0, a.few_rows, s, sub, share)) {
+    return;
   }
 
   for (;; ++sub) {
@@ -147,17 +94,8 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
     const int steps = keys.end > keys.lo ? (keys.end - keys.lo + STEP - 1) / STEP : 0;
     int st0 = 0, st1 = steps, pieces = 1, first = 0;
     if (a.few_wgs > 0) {
-      const uint64_t x_end = x + (steps > 0 ? steps : 1);
-      if (x_end <= x0) {  // a tile before the workgroup's first
-        x = x_end;
-        continue;
-      }
-      if (x >= x1) return;
-      st0 = x0 > x ? (int)(x0 - x) : 0;
-      st1 = x1 < x_end ? (int)(x1 - x) : steps;
-      first = (int)(x / share);
-      pieces = (int)((x_end - 1) / share) - first + 1;
-      x = x_end;
+      if (share.x >= share.x1) return;
+      if (!take_steps<16>(share, steps, st0, st1, first, pieces)) continue;
     }
     {
       const int row = r0 + col;
@@ -431,16 +369,16 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
   if (tok < b || tok >= e) return;  // no request's row: nothing was written for it
   int n = a.where[2 * row];
   if (n == 0) return;  // written by the workgroup itself
+  // shared by n workgroups, the first of them and the row of its tile in `at`
   const bool few = n < 0;
-  const int at = a.where[2 * row + 1];
   n = few ? -n : n;
+  const int at = a.where[2 * row + 1], shift = few ? 4 : a.many_shift, wgs = few ? a.few_wgs : a.many_wgs;
   // (bounds for offsets that are not a batch's: rows no request owns hold anything)
-  const int most = few ? a.few_wgs - (at >> 4) : a.splits;
-  if (n > most || (few && (at < 0 || (at >> 4) >= a.few_wgs))) return;
+  if (at < 0 || (at >> shift) >= wgs || n > wgs - (at >> shift)) return;
   const float* sums = few ? a.few : a.many;
-  const float* ml = sums + (few ? (int64_t)a.few_wgs * a.hkv * 32 : n_rows * a.splits) * a.d;
+  const float* ml = sums + (((int64_t)wgs * a.hkv * 2) << shift) * a.d;
   const auto piece = [&](int i) -> int64_t {
-    return few ? ((((int64_t)(at >> 4) + i) * a.hkv + h) * 2 + (i == 0 ? 1 : 0)) * 16 + (at & 15) : i * n_rows + row;
+    return (((((int64_t)(at >> shift) + i) * a.hkv + h) * 2 + (i == 0 ? 1 : 0)) << shift) + (at & ((1 << shift) - 1));
   };
   float m = NEG_INF, l = 0.f;
   float4_t o = {0, 0, 0, 0};
@@ -514,26 +452,27 @@ AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_h
     p.few_wgs = (int)((at_once + kv_heads - 1) / kv_heads);
   // eight waves to a workgroup where each has a CU or so to itself
   p.more_waves = p.few_wgs == 0 && p.few_tiles * kv_heads <= 512 && max_kv > STEP * WAVES;
-  // Prompt tiles: one workgroup to a CU, some 2 us a step.  Where they leave
-  // CUs idle, a tile's keys are split over `n` workgroups: steps / n * 2 us,
-  // plus float32 sums of n * rows * d written and read at 4 TB/s, least at n =
-  // sqrt(2 us steps / (2 us rows d / 10^6)).  And 4096 keys at most where
-  // unequal requests might leave a few tiles to the end.  (Each is a growing
-  // function of max_kv, so that the workspace is.)
-  p.splits = 1;
-  if (p.many_tiles > 0) {
-    const int64_t wgs = p.many_tiles * kv_heads, steps = (max_kv + STEP - 1) / STEP;
-    int64_t n = 256 / wgs;
-    const int64_t best = (int64_t)sqrt(1e6 * (double)steps / ((double)tokens * q_heads * d));
-    n = n < best ? n : best;
-    n = n < steps / 2 ? n : steps / 2;
-    const int64_t equal = wgs < 1024 ? (max_kv + 4095) / 4096 : 1;
-    n = n > equal ? n : equal;
-    p.splits = (int)(n < 1 ? 1 : n > 64 ? 64 : n);
+  // Prompt tiles: one workgroup to a CU, 2 us a step.  A workgroup to a tile, a
+  // request's longest first, needs no sums joined; even shares leave no CU
+  // idle, at some 25 us, or 50 where each has several tiles.  What they save,
+  // in steps, with `full` steps in the longest tile and `fresh` fewer in the
+  // shortest: all CUs' work but the tiles', where the tiles are fewer; else the last
+  // round of equal tiles, and more where requests are unequal.  (1024 tokens
+  // after 16000, 8 kv heads: 336 us against 536; 128 after 4000 47 against
+  // 136; but prompts of 1024 and 4096 tokens 53 and 238 against 46 and 193.)
+  // It grows with max_kv, so that the workspace does.
+  p.many_wgs = 0;
+  if (p.many_tiles > 0 && kv_heads <= 64) {
+    const int64_t wgs = 256 / kv_heads * kv_heads, all_tiles = p.many_tiles * kv_heads;
+    const int64_t seen = window + tile / group + 1;  // keys of a tile's rows under a window
+    const double full = (double)(((window > 0 && seen < max_kv ? seen : max_kv) + STEP - 1) / STEP);
+    const double news = (double)(max_new < tokens ? max_new : tokens) / STEP, fresh = news < full ? news : full;
+    const double each = (double)all_tiles / wgs, rounds = (double)((all_tiles + wgs - 1) / wgs);
+    const double saved = each < 1 ? full - each * (full - fresh / 2)
+                                  : (rounds - each) * (full - fresh) + (n_seqs > 1 ? 0.3 * full : 0.);
+    if (saved > (each < 1 ? 12 : 24)) p.many_wgs = (int)(256 / kv_heads);
   }
-  const int64_t chunk = (max_kv + p.splits - 1) / p.splits;
-  p.chunk = (int)(chunk < 0x7FFFFFC0 ? (chunk + STEP - 1) / STEP * STEP : 0x7FFFFFC0);
-  const int64_t many = p.splits > 1 ? tokens * q_heads * p.splits : 0, few = (int64_t)p.few_wgs * kv_heads * 32;
+  const int64_t many = (int64_t)p.many_wgs * kv_heads * 2 * tile, few = (int64_t)p.few_wgs * kv_heads * 32;
   p.few_at = many * (d + 2) * 4;
   p.where_at = p.few_at + few * (d + 2) * 4;
   p.bytes = many + few > 0 ? p.where_at + tokens * q_heads * 8 : 0;

@@ -361,6 +361,21 @@ def test_prompts_whose_keys_are_split(kq, d, hq, kv, q_dtype):
     _check(kq, c, "uniform", "f32", scale=0.0, max_new=45, max_kv=2500)
 
 
+@pytest.mark.parametrize("d, hq, kv, q_dtype", [(32, 64, 32, "f16"), (128, 40, 40, "bf16"), (224, 48, 16, "f16")])
+def test_prompts_in_even_shares(kq, d, hq, kv, q_dtype):
+    # few workgroups to a head: each has a piece of one prompt's tile, several whole ones and a piece of another
+    rng = np.random.default_rng(185 + d)
+    new = np.concatenate((rng.integers(34, 150, 9), [0, 0, 35, 300, 1, 270]))
+    lens = new + rng.integers(0, 200, len(new)) * (rng.random(len(new)) < 0.6)
+    lens[3], lens[9], lens[12] = 20, 0, 333  # rows before the first key, an idle request, a longer one
+    c = _case(185 + d, new, lens, hq, kv, d, 16, q_dtype, extra_tokens=3)
+    for max_kv in (700, 300000):
+        _check(kq, c, f"max_kv {max_kv}", "f16", max_new=300, max_kv=max_kv)
+    _check(kq, c, "window", "f32", max_new=300, max_kv=300000, window=90)
+    c = _case(186 + d, [301], [411], hq, kv, d, 32, q_dtype)
+    _check(kq, c, "one request", "f16", max_new=301, max_kv=300000)
+
+
 @pytest.mark.parametrize("d, hq, kv, n", [(128, 4, 1, 200), (128, 16, 2, 70), (192, 5, 1, 130), (32, 1, 1, 300)])
 def test_prompts_over_several_tiles(kq, d, hq, kv, n):
     c = _case(190 + d + n, [n], [n + 77], hq, kv, d, 32)
