@@ -117,11 +117,14 @@ __device__ __forceinline__ bool find_share(const AttnArgs& a, int wg, int wgs, i
   r.x0 = r.size * (uint64_t)wg;
   r.x1 = r.x0 + r.size < total ? r.x0 + r.size : total;
   if (r.x0 >= total) return false;
+  // (both searches find their place, total > x0, unless someone changes the
+  // lengths meanwhile; they end even so)
   uint64_t x = 0;
-  for (int s0 = 0;; s0 += 64) {
+  s = -1;
+  for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
     const uint64_t n = (uint64_t)request_cost<ROWS>(a, s0 + lane, above, most), incl = wave_prefix(n);
     const uint64_t hit = __ballot(x + incl > r.x0);
-    if (hit) {  // total > x0: some request has it
+    if (hit) {
       const int l = __builtin_ctzll(hit);
       s = s0 + l;
       x += __shfl(incl - n, l, 64);
@@ -130,9 +133,10 @@ __device__ __forceinline__ bool find_share(const AttnArgs& a, int wg, int wgs, i
     x += __shfl(incl, 63, 64);
   }
   s = __builtin_amdgcn_readfirstlane(s);
+  if (s < 0) return false;
   const Seq q = load_seq(a, s);
   const int tiles = (q.n * a.group + ROWS - 1) / ROWS;
-  for (int t0 = 0;; t0 += 64) {
+  for (int t0 = 0; t0 < tiles; t0 += 64) {
     const uint64_t n = t0 + lane < tiles ? (uint64_t)tile_cost<ROWS>(a, q, t0 + lane) : 0, incl = wave_prefix(n);
     const uint64_t hit = __ballot(x + incl > r.x0);
     if (hit) {
@@ -143,6 +147,7 @@ __device__ __forceinline__ bool find_share(const AttnArgs& a, int wg, int wgs, i
     }
     x += __shfl(incl, 63, 64);
   }
+  return false;
 }
 // The workgroup's steps st0 .. st1 - 1 of a tile of `steps` steps that begins at
 // r.x (r.x moves on to the next tile), the first workgroup that has some of
