@@ -22,8 +22,8 @@
 // mantissa, times the block's scale.
 //
 // Measured (8 kv heads, groups of 4, d = 128): 64 requests of 200 to 8192 keys
-// 72 us, 3.6 TB/s of cache; 4 of 131072 keys 120 to 130 us, 4.5 TB/s (a large
-// copy reaches 4.8).  Bound by HBM on long keys, by unpacking (416 of a step's
+// 66 us, 4.0 TB/s of cache; 4 of 131072 keys 113 us, 5.2 TB/s (reads alone
+// reach 5.5).  Bound by HBM on long keys, by unpacking (416 of a step's
 // 500 vector operations) where much of the cache is in the last-level cache,
 // by latency on short ones: 330 keys of one request 9 us with its launch.
 #include "kq_kv_attn.h"

@@ -14,9 +14,9 @@
 // round of step r unpacks step r + 1 (two places for keys, three for values,
 // of which V(r - 1) and V(r) are being read) and fetches the one after.
 //
-// Measured: a prompt of 4096 tokens (8 kv heads, groups of 4, d = 128) 165 to
-// 200 us, 690 to 840 TFLOP/s of its causal products (a large library product
-// reaches 1160); 2048 tokens after 30000 1.05 ms, 980 TFLOP/s.  A step of a
+// Measured: a prompt of 4096 tokens (8 kv heads, groups of 4, d = 128) 156 to
+// 195 us, 700 to 880 TFLOP/s of its causal products (a large library product
+// reaches 1160; less after an idle spell); 2048 tokens after 30000 1.05 ms, 980 TFLOP/s.  A step of a
 // workgroup takes 2 us.  Bound by the vector unit: softmax and unpacking run
 // about as long as the matrix products, and beside them only in part.
 #include "kq_kv_attn.h"
