@@ -324,7 +324,7 @@ __device__ __forceinline__ void query_operands(const AttnArgs& a, const u32x4 (&
                                                float& factor) {
   const float log2e = 1.4426950408889634f;
   const bool neg = a.scale < 0.f;
-  factor = fabsf(a.scale) * log2e;
+  factor = fabsf(a.scale);
   if (a.q_bf16) {
     float v[NB][8], amax = 0.f;
 #pragma unroll
@@ -358,7 +358,34 @@ __device__ __forceinline__ void query_operands(const AttnArgs& a, const u32x4 (&
       q[s] = query_order(h);
     }
   }
-  factor = fmaxf(factor, 1.17549435e-38f);  // a zero factor would turn masked -inf into NaN
+  // a zero factor would turn masked -inf into NaN; above 2^80 products, whole
+  // multiples of 2^-48 below 2^40, give the weights they give at 2^80 (unequal
+  // ones are at least 2^32 apart), and their logits could pass float32
+  factor = fminf(fmaxf(factor * log2e, 1.17549435e-38f), 0x1p80f);
+}
+
+// A row's softmax over the steps: weights are 2^(product * factor + bias), of
+// products up to `limit`, with bias = -m * factor for a running maximum m.
+// Moves m, limit and bias for a step whose largest product passes the limit
+// (NaN does); returns what the sums so far are to be multiplied by.
+//   The limit is above m by 2^8 in weights, so that few steps move m.
+//   Where m * factor is so large that a float32 there is 1/2 or more from the
+// next, the bias would be off by its rounding, and weights that should be at
+// most 1 come out infinite, or all of them zero.  Such a row takes m off the
+// products themselves, which is exact near it, and has no limit above it: all
+// its steps come here (every row doing so would be one more vector operation a
+// weight: prompts 4% slower, as with a branch of its own in the step).
+__device__ __forceinline__ float move_maximum(float mx, float factor, float4_t (&sc)[4], float& m, float& limit,
+                                              float& bias) {
+  mx = fmaxf(mx, m);
+  const float corr = mx == NEG_INF ? 1.f : __builtin_amdgcn_exp2f((m - mx) * factor);
+  m = mx;
+  const bool none = m == NEG_INF, far = !none && fabsf(m * factor) >= 4194304.f;
+  limit = none || far ? NEG_INF : m + 8.f * __builtin_amdgcn_rcpf(factor);
+  bias = none || far ? 0.f : -m * factor;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) sc[i >> 2][i & 3] -= far ? m : 0.f;
+  return corr;
 }
 
 template <int OUT>

@@ -189,14 +189,12 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
       half8_t q[NB];
       float factor;
       query_operands<NB>(a, q_raw, q, factor);
-      // probabilities may reach 2^8 before the sums are brought to a new maximum
-      const float slack = 8.f / factor;
 
       float4_t o[DT];
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[t] = float4_t{0, 0, 0, 0};
       float4_t l4 = {0, 0, 0, 0};
-      float m = NEG_INF;
+      float m = NEG_INF, limit = NEG_INF, bias = 0.f;
 
       for (int st = st0 + wave; st < st1; st += WAVES) {
         const int base = keys.lo + st * STEP, after = st + WAVES;
@@ -257,15 +255,12 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
 #pragma unroll
         for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[i >> 2][i & 3]);
         mx = groups_max(mx);
-        if (__any(!(mx <= m + slack))) {
-          mx = fmaxf(mx, m);
-          const float corr = mx == NEG_INF ? 1.f : __builtin_amdgcn_exp2f((m - mx) * factor);
-          m = mx;
+        if (__any(!(mx <= limit))) {
+          const float corr = move_maximum(mx, factor, sc, m, limit, bias);
           l4 *= corr;
 #pragma unroll
           for (int t = 0; t < DT; ++t) o[t] *= corr;
         }
-        const float bias = m == NEG_INF ? 0.f : -m * factor;
         // P^T operands: places (2 s, 2 s + 1) hold keys s of groups 2 m and 2 m + 1
         half8_t pt[2];
 #pragma unroll

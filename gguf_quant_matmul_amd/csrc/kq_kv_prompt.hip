@@ -214,14 +214,14 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
 #pragma unroll
     for (int c = 0; c < C; ++c) query_operands<NB>(a, q_raw[c], q[c], factor[c]);
     float4_t o[DT][C], l4[C];
-    float m[C], slack[C];
+    float m[C], limit[C], bias[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) {
 #pragma unroll
       for (int t = 0; t < DT; ++t) o[t][c] = float4_t{0, 0, 0, 0};
       l4[c] = float4_t{0, 0, 0, 0};
-      m[c] = NEG_INF;
-      slack[c] = 8.f / factor[c];  // probabilities may reach 2^8 before the sums are brought to a new maximum
+      m[c] = limit[c] = NEG_INF;
+      bias[c] = 0.f;
     }
 
     // operands of key group i, of block b of the values
@@ -336,22 +336,19 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
 #pragma unroll
           for (int i = 1; i < 16; ++i) mx = fmaxf(mx, sc[c][i >> 2][i & 3]);
           mx = groups_max(mx);
-          if (__any(!(mx <= m[c] + slack[c]))) {
-            mx = fmaxf(mx, m[c]);
-            const float corr = mx == NEG_INF ? 1.f : __builtin_amdgcn_exp2f((m[c] - mx) * factor[c]);
-            m[c] = mx;
+          if (__any(!(mx <= limit[c]))) {
+            const float corr = move_maximum(mx, factor[c], sc[c], m[c], limit[c], bias[c]);
             l4[c] *= corr;
 #pragma unroll
             for (int t = 0; t < DT; ++t) o[t][c] *= corr;
           }
-          const float bias = m[c] == NEG_INF ? 0.f : -m[c] * factor[c];
           // P^T operands: places (2 s, 2 s + 1) hold keys s of groups 2 m and 2 m + 1
 #pragma unroll
           for (int mm = 0; mm < 2; ++mm)
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              pt[c][mm][2 * j] = (half_t)__builtin_amdgcn_exp2f(fmaf(sc[c][2 * mm][j], factor[c], bias));
-              pt[c][mm][2 * j + 1] = (half_t)__builtin_amdgcn_exp2f(fmaf(sc[c][2 * mm + 1][j], factor[c], bias));
+              pt[c][mm][2 * j] = (half_t)__builtin_amdgcn_exp2f(fmaf(sc[c][2 * mm][j], factor[c], bias[c]));
+              pt[c][mm][2 * j + 1] = (half_t)__builtin_amdgcn_exp2f(fmaf(sc[c][2 * mm + 1][j], factor[c], bias[c]));
             }
           // sums of the (rounded) probabilities: one more row tile of V^T, all ones
           const half_t one = (half_t)1.f;
