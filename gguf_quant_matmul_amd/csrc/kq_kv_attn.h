@@ -48,6 +48,7 @@ __device__ __forceinline__ Keys key_range(const AttnArgs& a, const Seq& q, int r
   return k;
 }
 constexpr int STEP = 64;  // keys of one step
+constexpr float HEADROOM = 7.f;  // log2 of the weight of a running maximum
 
 // What a tile costs beside its steps, in steps: its start and its end.  (Shares
 // of steps alone gave some workgroups ten short tiles: 9 requests of mixed
@@ -365,9 +366,15 @@ __device__ __forceinline__ void query_operands(const AttnArgs& a, const u32x4 (&
 }
 
 // A row's softmax over the steps: weights are 2^(product * factor + bias), of
-// products up to `limit`, with bias = -m * factor for a running maximum m.
+// products up to `limit`, with bias = 7 - m * factor for a running maximum m.
 // Moves m, limit and bias for a step whose largest product passes the limit
 // (NaN does); returns what the sums so far are to be multiplied by.
+//   Weights enter the matrix cores as float16, each off by half a step, 2^-11
+// of itself.  The 2^7 at the maximum (with the 2^8 below, half of what float16
+// holds) is for the small ones: those of 2^-21 of it and more keep that
+// precision and nothing above 2^-32 is lost, where 1 would lose all below
+// 2^-25; 131072 keys of 2^-25 each are 0.4% of a row.  It is in the sums too,
+// and goes out with the quotient.
 //   The limit is above m by 2^8 in weights, so that few steps move m.
 //   Where m * factor is so large that a float32 there is 1/2 or more from the
 // next, the bias would be off by its rounding, and weights that should be at
@@ -382,10 +389,16 @@ __device__ __forceinline__ float move_maximum(float mx, float factor, float4_t (
   m = mx;
   const bool none = m == NEG_INF, far = !none && fabsf(m * factor) >= 4194304.f;
   limit = none || far ? NEG_INF : m + 8.f * __builtin_amdgcn_rcpf(factor);
-  bias = none || far ? 0.f : -m * factor;
+  bias = none ? 0.f : far ? HEADROOM : fmaf(-m, factor, HEADROOM);
 #pragma unroll
   for (int i = 0; i < 16; ++i) sc[i >> 2][i & 3] -= far ? m : 0.f;
   return corr;
+}
+
+// log2 of what a row's sums are to be multiplied by beside others of the row:
+// the very bias of its weights, negative.
+__device__ __forceinline__ float sums_at(float m, float factor) {
+  return m == NEG_INF ? NEG_INF : fmaf(m, factor, -HEADROOM);
 }
 
 template <int OUT>

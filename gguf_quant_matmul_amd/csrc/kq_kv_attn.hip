@@ -309,7 +309,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
 #pragma unroll
       for (int t = 0; t < DT; ++t) *(float4_t*)(mine + mcol * (D + 4) + 16 * t + 4 * mg) = o[t];
       if (mg == 0) {
-        merge_m[wave][mcol] = m == NEG_INF ? NEG_INF : m * factor;  // in powers of two
+        merge_m[wave][mcol] = sums_at(m, factor);
         merge_l[wave][mcol] = l4[0];
       }
       __syncthreads();

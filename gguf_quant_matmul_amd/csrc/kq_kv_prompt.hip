@@ -404,7 +404,7 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
         for (int t = 0; t < DT; ++t) store4<0>(a.many, pr * D + 16 * t + 4 * g, o[t][c]);
         if (g == 0) {
           float* ml = a.many + (int64_t)a.many_wgs * a.hkv * 2 * T::ROWS * D + 2 * pr;
-          ml[0] = m[c] == NEG_INF ? NEG_INF : m[c] * factor[c];  // in powers of two, for the join
+          ml[0] = sums_at(m[c], factor[c]);  // for the join
           ml[1] = l;
         }
       }

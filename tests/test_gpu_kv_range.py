@@ -8,7 +8,7 @@ import pytest
 
 from _gpu import dev
 from oracle import kvcache
-from test_gpu_kv import _attn, _close, _f64, _tdt
+from test_gpu_kv import HALF_STEP, _attn, _close, _f64, _tdt
 
 pytestmark = pytest.mark.gpu
 
@@ -64,3 +64,41 @@ def test_large_logits_pick_the_largest(kq, new, lens, max_kv, q_dtype, q_size, s
     got = _f64(_attn(kq, c, "f32", scale, max_new=max(new), max_kv=max_kv))
     vmax = np.abs(kvcache.load(c["vc"], page, d, np.arange(c["vc"].shape[0] * page))).max()
     _close(got, ref, np.full(ref.shape, (2.0 ** -11 + 2.0 ** -16) * vmax), f"{q_dtype} {q_size} scale {scale}")
+
+
+@pytest.mark.parametrize("gap", [10.0, 16.0, 17.5, 20.0])
+@pytest.mark.parametrize("hq, kv, d, q_dtype", [(4, 2, 128, "f16"), (6, 1, 64, "bf16")])
+@pytest.mark.parametrize("new, lens, max_kv, at", [([1], [4096], 512, 0), ([1, 1], [4096, 3000], 4096, 0),
+                                                   ([130], [4000], 200000, 0), ([130], [4000], 4000, 1500),
+                                                   ([40, 1, 35], [4000, 3000, 2100], 4000, 70)])
+def test_many_small_weights_beside_a_large_one(kq, new, lens, max_kv, at, hq, kv, d, q_dtype, gap):
+    # Key `at` has logit `gap` and value 0, all others logit 0: the output is
+    # what the small weights add up to.  A probability is off by 2^-11 of
+    # itself or, as a subnormal float16, by 2^-25 where the largest is 2^7, so
+    # by 2^-32 of the largest, in the sum over values and in the sum of
+    # weights; logits, values, float32 sums and the store as in the parity
+    # tests.
+    page = 64
+    rng = np.random.default_rng(7)
+
+    def keys(s):
+        k = np.zeros((lens[s], kv, d))
+        k[at] = 7.0  # (code 15 of scale 1)
+        return k
+
+    def values(s):
+        v = rng.standard_normal((lens[s], kv, d)) + 2.0
+        v[at] = 0
+        return v
+
+    scale = gap / (7 * d)
+    c = _batch(new, lens, hq, kv, d, page, keys, values, np.ones((sum(new), hq, d)), q_dtype)
+    ref, absv, mag, count = kvcache.attention(_f64(c["q"]), c["cu"], c["lens"], c["table"], c["kc"], c["vc"], page,
+                                              float(np.float32(scale)), detail=True)
+    got = _f64(_attn(kq, c, "f32", scale, max_new=max(new), max_kv=max_kv))
+    vmax = np.abs(kvcache.load(c["vc"], page, d, np.arange(c["vc"].shape[0] * page))).max()
+    # keys, queries and their products are exact here: a logit is off by the rounding of scale * log2(e) and of the
+    # exponent's sum, 2^-22 of itself
+    p = absv * (np.expm1(2 * 2.0 ** -22 * mag[..., None]) + 2 * 2.0 ** -11 + 2.0 ** -11 + 2.0 ** -16) * 1.01
+    bound = p + 2 * count[..., None] * 2.0 ** -32 * vmax
+    _close(got, ref, bound + HALF_STEP["f32"] * (np.abs(ref) + bound), f"gap {gap}")
