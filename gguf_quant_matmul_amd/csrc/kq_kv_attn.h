@@ -64,15 +64,16 @@ __device__ __forceinline__ int tile_cost(const AttnArgs& a, const Seq& q, int su
   const Keys k = key_range(a, q, r0, r1);
   return (k.end > k.lo ? (k.end - k.lo + STEP - 1) / STEP : 1) + TILE_EXTRA<ROWS>;
 }
-// ... of all tiles of a request with more than `above` and at most `most` rows.
+// ... of all tiles of a request with more than `above` and at most `most` rows
+// (64-bit: 2^21 tiles of 2^24 steps are within the bounds on a call's sizes).
 template <int ROWS>
-__device__ __forceinline__ int request_cost(const AttnArgs& a, int s, int above, int most) {
+__device__ __forceinline__ uint64_t request_cost(const AttnArgs& a, int s, int above, int most) {
   if (s >= a.n_seqs) return 0;
   const Seq q = load_seq(a, s);
   const int rows = q.n * a.group;
   if (rows <= above || rows > most) return 0;
-  int n = 0;
-  for (int sub = 0; sub * ROWS < rows; ++sub) n += tile_cost<ROWS>(a, q, sub);
+  uint64_t n = 0;
+  for (int sub = 0; sub * ROWS < rows; ++sub) n += (uint32_t)tile_cost<ROWS>(a, q, sub);
   return n;
 }
 
@@ -93,7 +94,7 @@ __device__ __forceinline__ uint64_t wave_prefix(uint64_t v) {
 
 // The part of one of `wgs` workgroups (of a kv head) that share out the cost
 // of all those requests' tiles evenly, `least` to one at least: x0 .. x1 - 1
-// of the whole (64-bit: garbage lengths may add up), `size` to a workgroup.
+// of the whole, `size` to a workgroup.
 // A tile's steps come first, then its extra, which nobody works on.  The part
 // begins in tile `sub` of request s, whose own begins at x.  False for a
 // workgroup without a part.  Every wave finds it for itself, 64 requests
@@ -107,7 +108,7 @@ __device__ __forceinline__ bool find_share(const AttnArgs& a, int wg, int wgs, i
   const int lane = threadIdx.x & 63;
   uint64_t total = 0;
   for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
-    uint64_t n = (uint64_t)request_cost<ROWS>(a, s0 + lane, above, most);
+    uint64_t n = request_cost<ROWS>(a, s0 + lane, above, most);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o, 64);
     total += n;
@@ -123,7 +124,7 @@ __device__ __forceinline__ bool find_share(const AttnArgs& a, int wg, int wgs, i
   uint64_t x = 0;
   s = -1;
   for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
-    const uint64_t n = (uint64_t)request_cost<ROWS>(a, s0 + lane, above, most), incl = wave_prefix(n);
+    const uint64_t n = request_cost<ROWS>(a, s0 + lane, above, most), incl = wave_prefix(n);
     const uint64_t hit = __ballot(x + incl > r.x0);
     if (hit) {
       const int l = __builtin_ctzll(hit);

@@ -102,3 +102,25 @@ def test_many_small_weights_beside_a_large_one(kq, new, lens, max_kv, at, hq, kv
     p = absv * (np.expm1(2 * 2.0 ** -22 * mag[..., None]) + 2 * 2.0 ** -11 + 2.0 ** -11 + 2.0 ** -16) * 1.01
     bound = p + 2 * count[..., None] * 2.0 ** -32 * vmax
     _close(got, ref, bound + HALF_STEP["f32"] * (np.abs(ref) + bound), f"gap {gap}")
+
+
+def test_more_steps_to_share_than_32_bits_count(kq):
+    # One request of 2^30 - 4096 keys, one page over and over, 132 tiles of 16
+    # rows: 2.2e9 steps.  Keys are 0 and the values the same in every key, so
+    # that a row is these values, whoever does its steps.  A wave adds up
+    # n = 2.2e9 * 64 / 4096 = 2^25.05 keys of one weight.  The matrix cores
+    # align an instruction's products to its largest term, the sum so far, and
+    # keep three bits below its last place: the product for key i is off by at
+    # most i 2^-26 of itself, their sum by n 2^-27 = 0.26 of itself.  Joining
+    # 4096 such sums adds 2^-12 at most.
+    import torch
+
+    hq, d, page, tokens = 64, 32, 4096, 33
+    width = (1 << 30) // page - 1
+    kc, vc = (np.zeros((1, 1, kvcache.page_bytes(page, d)), np.uint8) for _ in range(2))
+    v = np.arange(d) % 15 - 7.0  # (scale 1)
+    kvcache.store(vc, page, np.arange(page), *kvcache.encode(np.broadcast_to(v, (page, 1, d)).astype(np.float32)))
+    q = torch.ones((tokens, hq, d), dtype=torch.float16, device="cuda")
+    c = dict(q=q, cu=[0, tokens], lens=[width * page], table=np.zeros((1, width)), kc=kc, vc=vc, page=page)
+    got = _f64(_attn(kq, c, "f32", max_new=1, max_kv=width * page))
+    assert (np.abs(got - v) <= 0.2605 * np.abs(v)).all()
