@@ -310,9 +310,16 @@ def _index(op: str, name: str, t, n: int | None, device: int) -> int:
     return t.data_ptr()
 
 
+def _on_gpu(op: str, device: int) -> None:
+    """Raise for tensors of the host (device -1): a kernel that reads their addresses faults."""
+    if device < 0:
+        raise ValueError(f"{op}: tensors must be on the GPU")
+
+
 def _call_on(device: int, stream, fn, *args) -> None:
     """fn(*args, stream) with `device` current: on the given stream, else on that device's current one."""
-    if device < 0 or device == torch.cuda.current_device():
+    _on_gpu(fn.__name__, device)
+    if device == torch.cuda.current_device():
         status = fn(*args, _stream(stream))
     else:
         with torch.cuda.device(device):
@@ -467,6 +474,7 @@ def kq_kv_attention(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page: i
         need = kq_kv_attention_workspace(tokens, n, heads, kv_heads, d, max_new, max_kv)
         ws = None
         if need:
+            _on_gpu(op, dev)
             if stream is not None and _stream(stream) != torch.cuda.current_stream(q.device).cuda_stream:
                 raise ValueError(f"{op}: a call on another stream than the current one needs its own workspace")
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
