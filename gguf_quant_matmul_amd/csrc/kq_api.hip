@@ -667,6 +667,7 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
     return fail(KQ_ERR_ARG, op, "width=%lld out of range (width * page below 2^30)", (long long)width);
   if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(KQ_ERR_ARG, op, "scale=%g is not finite", (double)scale);
   if (window < 0) return fail(KQ_ERR_ARG, op, "window=%lld is negative", (long long)window);
+  if (window >= (int64_t)1 << 30) window = 0;  // no request is that long
   if ((st = check_pages(op, k_cache, v_cache, pages, page))) return st;
   if (tokens == 0 || n_seqs == 0) return KQ_OK;
   if (!q || !out || !cu_new || !seq_lens || (width > 0 && !table))
@@ -718,7 +719,7 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
   a.d = (int)d;
   a.pages = (int)pages;
   a.page_shift = shift;
-  a.window = window < (int64_t)1 << 30 ? (int)window : 0;  // no request is that long
+  a.window = (int)window;
   a.scale = scale;
   a.q_bf16 = q_dtype == KQ_BF16;
   a.out_type = elem_id(out_dtype);
