@@ -69,7 +69,7 @@ def _call_module(verbose: bool, incremental: bool) -> None:
     root = os.path.dirname(torch.__file__)
     inc = os.path.join(root, "include")
     cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DKQ_TORCH="{torch.__version__}"',
            "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
            "-I" + sysconfig.get_paths()["include"], src, "-o", CALL + ".tmp",
            "-L" + HERE, "-l:libkq.so", "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",

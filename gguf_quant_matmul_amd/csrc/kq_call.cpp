@@ -173,4 +173,9 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kqcall", nullptr, -1, methods, nu
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__kqcall(void) { return PyModule_Create(&module); }
+PyMODINIT_FUNC PyInit__kqcall(void) {
+  PyObject* m = PyModule_Create(&module);
+  // the torch whose tensors this code reads
+  if (m && PyModule_AddStringConstant(m, "TORCH", KQ_TORCH) < 0) Py_CLEAR(m);
+  return m;
+}

@@ -1,7 +1,8 @@
-"""Thin ctypes binding of libkq (include/kq.h): same names, argument marshalling only.
+"""Thin ctypes binding of libkq (include/kq.h): same names, argument marshalling.
 
 Every function here forwards device pointers, sizes and the current HIP stream
-to the C ABI; all work runs in libkq's HIP kernels.  PyTorch supplies device
+to the C ABI; all work runs in libkq's HIP kernels.  The cache operators also
+check their tensors, and go through the host module _kqcall where it is there.  PyTorch supplies device
 memory and streams.  There is no fallback: if libkq.so is missing the import
 fails, and a failing call raises ``KQError`` with the library's message.
 """
@@ -10,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "libkq.so")
@@ -25,8 +27,26 @@ if not os.path.exists(LIB_PATH):
 import torch  # noqa: E402,F401
 
 _lib = ctypes.CDLL(LIB_PATH)
-# the cache operators' calls straight from tensors (csrc/kq_call.cpp, built with the library and linked to it)
-from . import _kqcall  # noqa: E402
+
+
+def _host_module():
+    """_kqcall (csrc/kq_call.cpp): the cache operators' calls straight from tensors.  None where it is not built, or for
+    another torch, whose tensors it would misread; the calls then go through ctypes as all others do."""
+    try:
+        from . import _kqcall as mod
+    except ImportError as e:
+        why = str(e)
+    else:
+        built = getattr(mod, "TORCH", None)
+        if built == torch.__version__:
+            return mod
+        why = f"built for torch {built}, this is {torch.__version__}"
+    warnings.warn(f"_kqcall cannot be used ({why}): calls of the cache operators take 4 to 7 us longer; run "
+                  "`python -m gguf_quant_matmul_amd.build`", RuntimeWarning, stacklevel=2)
+    return None
+
+
+_kqcall = _host_module()
 
 c_int, c_i64, c_vp, c_cp = ctypes.c_int, ctypes.c_int64, ctypes.c_void_p, ctypes.c_char_p
 _P = ctypes.POINTER
@@ -376,7 +396,7 @@ def kq_block_tables(ctx_lens, new_lens, free_pages, free_head, page: int, table,
                     free_head_out, status=None, stream=None) -> None:
     """Pages and slots of a step's new tokens.  ctx_lens, new_lens, seq_lens int32 [n]; free_pages int32 [n_free] from
     free_head int32 [1]; table int32 [n, width]; slots int32 [tokens]; cu_new int32 [n + 1]; free_head_out, status [1]."""
-    if stream is None and ctx_lens.is_cuda:
+    if _kqcall is not None and stream is None and ctx_lens.is_cuda:
         dev = torch._C._cuda_getDevice()
         st = _kqcall.block_tables(ctx_lens, new_lens, free_pages, free_head, page, table, slots, cu_new, seq_lens,
                                   free_head_out, status, torch._C._cuda_getCurrentRawStream(dev), dev)
@@ -397,7 +417,7 @@ def kq_block_tables(ctx_lens, new_lens, free_pages, free_head, page: int, table,
 def kq_kv_store(codec, k, v, slots, k_cache, v_cache, page: int, stream=None) -> None:
     """k, v float32/float16/bfloat16 [tokens, kv_heads, d] (dense rows, any row stride) into slots int32 [tokens] of
     k_cache, v_cache uint8 [pages, kv_heads, page_bytes]."""
-    if stream is None and k.is_cuda and (codec == "q4_0" or codec == KQ_Q4_0):
+    if _kqcall is not None and stream is None and k.is_cuda and (codec == "q4_0" or codec == KQ_Q4_0):
         dev = torch._C._cuda_getDevice()
         st = _kqcall.kv_store(k, v, slots, k_cache, v_cache, page, torch._C._cuda_getCurrentRawStream(dev), dev)
         if st is not None:
@@ -415,7 +435,7 @@ def kq_kv_store(codec, k, v, slots, k_cache, v_cache, page: int, stream=None) ->
 
 def kq_kv_load(codec, k_cache, v_cache, slots, page: int, k, v, stream=None) -> None:
     """The rows at slots int32 [tokens] of the caches to k, v [tokens, kv_heads, d] (float32, float16 or bfloat16)."""
-    if stream is None and k.is_cuda and (codec == "q4_0" or codec == KQ_Q4_0):
+    if _kqcall is not None and stream is None and k.is_cuda and (codec == "q4_0" or codec == KQ_Q4_0):
         dev = torch._C._cuda_getDevice()
         st = _kqcall.kv_load(k_cache, v_cache, slots, page, k, v, torch._C._cuda_getCurrentRawStream(dev), dev)
         if st is not None:
@@ -446,8 +466,8 @@ def kq_kv_attention(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page: i
     [n], table int32 [n, width]; out [tokens, q_heads, d]; scale defaults to d^-0.5.  max_new and max_kv bound a
     request's new tokens and length (default: tokens, width * page).  workspace: uint8 of kq_kv_attention_workspace
     bytes; allocated on the current stream if left out."""
-    if stream is None and q.is_cuda and (codec == "q4_0" or codec == KQ_Q4_0) and max_new is not None \
-            and max_kv is not None:
+    if _kqcall is not None and stream is None and q.is_cuda and (codec == "q4_0" or codec == KQ_Q4_0) \
+            and max_new is not None and max_kv is not None:
         dev = torch._C._cuda_getDevice()
         st = _kqcall.kv_attention(q, cu_new, seq_lens, table, k_cache, v_cache, page, out,
                                   q.size(-1) ** -0.5 if scale is None else scale, window, max_new, max_kv, workspace,

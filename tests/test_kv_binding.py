@@ -1,5 +1,9 @@
 """The Python side of the 4-bit cache operators: which tensors and modules it takes (no GPU needed)."""
 
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -35,3 +39,43 @@ def test_host_tensors_are_refused_before_a_workspace_is_made():
     with pytest.raises(ValueError, match="on the GPU"):
         kq.kq_kv_attention("q4_0", q, i32(2), i32(1), i32(1, 2), kc, vc, 16, q.clone(), max_new=1, max_kv=100000,
                            stream=0)
+
+
+CHILD = """
+import sys, types, warnings
+what = sys.argv[1]
+if what == "missing":
+    sys.modules["gguf_quant_matmul_amd._kqcall"] = None  # its import raises ImportError
+else:  # built against other headers than the torch that runs
+    import gguf_quant_matmul_amd
+    fake = types.ModuleType("gguf_quant_matmul_amd._kqcall")
+    fake.TORCH = "1.0.0"
+    sys.modules[fake.__name__] = gguf_quant_matmul_amd._kqcall = fake
+with warnings.catch_warnings(record=True) as seen:
+    warnings.simplefilter("always")
+    from gguf_quant_matmul_amd import kq
+import torch
+assert any("_kqcall" in str(w.message) for w in seen), seen
+assert kq.kq_row_bytes("q4_k", 256) == 144 and kq.kq_kv_page_bytes("q4_0", 16, 64) == 16 * 36
+sys.path.insert(0, "tests")
+import test_kv_binding as t
+for name in ("tables", "store", "load", "attention"):
+    try:
+        t._call(name, "cpu")
+    except ValueError as e:
+        assert "on the GPU" in str(e)
+    else:
+        raise SystemExit(name)
+print("ok")
+"""
+
+
+@pytest.mark.parametrize("what", ["missing", "other torch"])
+def test_the_library_works_without_its_host_module(what):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    res = subprocess.run([sys.executable, "-c", CHILD, what], cwd=root, capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0 and res.stdout.strip().endswith("ok"), res.stderr
+
+
+def test_the_host_module_is_built_for_this_torch():
+    assert kq._kqcall is not None and kq._kqcall.TORCH == torch.__version__
