@@ -167,11 +167,14 @@ __global__ __launch_bounds__(BT_THREADS) void block_tables_kernel(
 //
 // A thread takes 8 consecutive values (one dword of codes), four neighbouring
 // lanes a block; their maximum goes round by two DPP quad exchanges.  Long
-// calls are bound by HBM: each row is read and written once, with 16- or
-// 32-byte loads and stores; the kernels' 4-byte code stores of neighbouring
+// calls are bound by HBM, the store also by the vector units (82% busy while it
+// works): each row is read and written once, with 16- or 32-byte loads and
+// stores; the kernels' 4-byte code stores of neighbouring
 // lanes make up whole 64-byte lines from head size 128 on.  A decode step's
 // are bound by the launch and two dependent loads.  Measured, store and load
-// together: 8192 rows of 8 heads, d = 128, 20.6 us, 3.7 TB/s; 64 rows 9.3 us.
+// together: 8192 bfloat16 rows of 8 heads, d = 128, 20.6 us, 3.7 TB/s; 64 rows
+// 8.6 us.  Apart and on rows not in cache: 13.1 and 12.5 us, float32 ones 19.7
+// and 23.0 us, 3.9 and 3.3 TB/s.
 constexpr int KV_THREADS = 256;
 template <int T> struct Elem;
 template <> struct Elem<0> { typedef float type; };

@@ -5,6 +5,14 @@
 // The rows of a (request, kv head) are its new tokens times the group of
 // query heads that share the kv head: row r is token r / group, query head
 // kv_head * group + r % group.
+//
+// Three things are rounded to float16, half a step (2^-11) each, because the
+// matrix cores take them so: keys and values, whose exact D (c - 8) has up to
+// 14 bits, and probabilities, which are summed as rounded.  A float16 result is
+// then 4e-4 from the exact one, of which its own rounding is 2.1e-4.  Exact
+// keys would need the scales applied behind the products, block by block (one
+// more vector operation for every product sum of 32 values and row), exact
+// values and probabilities these in two terms, twice the matrix work.
 #pragma once
 
 #include "kq_internal.h"

@@ -22,10 +22,12 @@
 // mantissa, times the block's scale.
 //
 // Measured (8 kv heads, groups of 4, d = 128): 64 requests of 200 to 8192 keys
-// 66 us, 4.0 TB/s of cache; 4 of 131072 keys 113 us, 5.2 TB/s (reads alone
-// reach 5.5).  Bound by HBM on long keys, by unpacking (416 of a step's
-// 500 vector operations) where much of the cache is in the last-level cache,
-// by latency on short ones: 330 keys of one request 9 us with its launch.
+// 67 us, 4.0 TB/s of cache; 4 of 131072 keys 121 us, 4.9 TB/s (a plain read of
+// as many bytes 43 and 91 us).  Every byte is fetched once; the vector units
+// are busy 52 and 59% of the time (416 of a step's 500 operations unpack),
+// waves wait 32 and 24% of theirs: two waves a SIMD do not hide all of a step's
+// loads and LDS trips behind the other's unpacking.  Short ones are bound by
+// latency: 330 keys of one request 9 us with its launch.
 #include "kq_kv_attn.h"
 
 namespace kq {

@@ -14,11 +14,12 @@
 // round of step r unpacks step r + 1 (two places for keys, three for values,
 // of which V(r - 1) and V(r) are being read) and fetches the one after.
 //
-// Measured: a prompt of 4096 tokens (8 kv heads, groups of 4, d = 128) 156 to
-// 195 us, 700 to 880 TFLOP/s of its causal products (a large library product
-// reaches 1160; less after an idle spell); 2048 tokens after 30000 1.05 ms, 980 TFLOP/s.  A step of a
-// workgroup takes 2 us.  Bound by the vector unit: softmax and unpacking run
-// about as long as the matrix products, and beside them only in part.
+// Measured: a prompt of 4096 tokens (8 kv heads, groups of 4, d = 128) 162 us
+// among others, 850 TFLOP/s of its causal products (a large library product
+// reaches 1190), 200 us by itself; 2048 tokens after 30000 1.04 ms, 1000
+// TFLOP/s.  A step of a workgroup takes 2 us.  Bound by the vector units, busy
+// 52% of the time with softmax and unpacking, and the matrix cores, busy 38%,
+// which run beside each other only in part.
 #include "kq_kv_attn.h"
 
 namespace kq {

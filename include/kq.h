@@ -346,15 +346,17 @@ int kq_kv_load(int codec, const void* k_cache, const void* v_cache, int64_t page
  * seq_lens[s] - 1 of the pages table[s][0 ..] (int32 [n_seqs][width]), new
  * tokens included (store them first).  Row i of the request stands at
  * position p = seq_lens[s] - n + i and sees the keys j <= p, with window > 0
- * only those with j > p - window.  Query head h reads kv head
+ * only those with j > p - window (2^30 and more, like 0: all of them).  Query head h reads kv head
  * h / (q_heads / kv_heads).
  *   out[t][h] = sum_j softmax_j(scale * q[t][h] . k_j) v_j
  * out [tokens][q_heads][d] dense, out_dtype KQ_F32, KQ_F16 or KQ_BF16.  A
  * row that sees no key (a request of length 0, p < 0) is all zeros; rows
  * outside cu_new[0] .. cu_new[n_seqs] - 1 are left unwritten.  Keys and values
  * enter the matrix cores as float16, rounded once from their exact values;
- * queries exactly (bfloat16 ones scaled by a power of two per row); products,
- * softmax statistics and sums are float32, probabilities float16.
+ * queries exactly (bfloat16 ones scaled by a power of two per row, which is
+ * exact down to 2^-28 of the row's largest); products, softmax statistics and
+ * sums are float32.  Probabilities are float16, to 2^-11 of themselves, or
+ * 2^-32 of the row's largest where that is more.  So it is for every out_dtype.
  * Device data is bounded, not trusted: cu_new entries are clamped to 0 ..
  * tokens, a length to 0 .. width * page, and keys whose table entry is not a
  * page of the cache are left out.  The cache is expected to hold finite
