@@ -13,6 +13,8 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -57,26 +59,36 @@ def _stale(src: str) -> bool:
 
 
 def _call_module(verbose: bool, incremental: bool) -> None:
-    """Compile csrc/kq_call.cpp (plain C++ against torch's headers) and link it to libkq.so beside it."""
-    import sysconfig
+    """Compile csrc/kq_call.cpp (plain C++ against torch's headers) and link it to libkq.so beside it.
 
-    import torch
-
+    The library is whole without it (kq.py then calls through ctypes), so a machine that cannot build it, for want of
+    torch, a C++ compiler or Python's headers, gets a warning; a module of an earlier build does not stay behind."""
     src = os.path.join(CSRC, "kq_call.cpp")
     deps = [src, os.path.join(HERE, os.pardir, "include", "kq.h")]
     if incremental and os.path.exists(CALL) and os.path.getmtime(CALL) >= max(map(os.path.getmtime, deps)):
         return
-    root = os.path.dirname(torch.__file__)
-    inc = os.path.join(root, "include")
-    cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
-           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DKQ_TORCH="{torch.__version__}"',
-           "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
-           "-I" + sysconfig.get_paths()["include"], src, "-o", CALL + ".tmp",
-           "-L" + HERE, "-l:libkq.so", "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
-           "-Wl,-rpath,$ORIGIN"]
-    res = subprocess.run(cmd, capture_output=True, text=True)
-    if res.returncode != 0:
-        raise RuntimeError(f"compiling {src} failed:\n{res.stdout}{res.stderr}")
+    if os.path.exists(CALL):
+        os.remove(CALL)
+    try:
+        import torch
+
+        root = os.path.dirname(torch.__file__)
+        inc = os.path.join(root, "include")
+        cmd = [shutil.which("g++") or "c++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w",
+               f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", f'-DKQ_TORCH="{torch.__version__}"',
+               "-I" + inc, "-I" + os.path.join(inc, "torch", "csrc", "api", "include"),
+               "-I" + sysconfig.get_paths()["include"], src, "-o", CALL + ".tmp",
+               "-L" + HERE, "-l:libkq.so", "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10",
+               "-Wl,-rpath,$ORIGIN"]
+        res = subprocess.run(cmd, capture_output=True, text=True)
+    except (ImportError, OSError) as e:  # no torch, no compiler
+        why = str(e)
+    else:
+        why = res.stdout + res.stderr if res.returncode != 0 else ""
+    if why:
+        warnings.warn(f"{os.path.basename(CALL)} is not built, calls of the cache operators will go through ctypes:\n{why}",
+                      RuntimeWarning, stacklevel=2)
+        return
     os.replace(CALL + ".tmp", CALL)
     if verbose:
         print(f"built {CALL}")
