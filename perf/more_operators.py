@@ -483,13 +483,13 @@ def _plain_free(st):
     pages = refs.numel()
     col = torch.arange(table.shape[1], device="cuda").unsqueeze(0)
     given = (col >= st["first"].unsqueeze(1)) & (col < st["last"].unsqueeze(1))
-    bad = given & ((table < 0) | (table >= pages))
-    refs.index_add_(0, table.clamp(0, pages - 1).flatten().long(), -(given & ~bad).flatten().int())
+    given &= (table >= 0) & (table < pages)
+    refs.index_add_(0, table.clamp(0, pages - 1).flatten().long(), -given.flatten().int())
     dead = refs < 0
     rank = dead.long().cumsum(0)
     count, head = rank[-1], st["head"].long()
     place = head - count + rank - 1
-    status = bad.any().int() + 2 * (refs < -1).any().int() + 4 * (count > head).any().int()
+    status = (refs < -1).any().int() + 2 * (count > head).any().int()
     refs.clamp_(min=0)
     # (one place more takes what is not written)
     room = torch.cat((free, free[:1]))
@@ -529,7 +529,7 @@ def _plain_compact(st):
     head = n_free - (pages - count)
     st["free_out"].copy_(torch.where(at >= head, count + at - head, st["free"].long()))
     st["head_out"].copy_(head)
-    st["status"].copy_((listed.sum() + st["head"] != n_free) + 2 * (head != st["head"]))
+    st["status"].copy_(head != st["head"])
     _copy(st)
     return tuple(st[x] for x in ("table_out", "refs_out", "free_out", "remap", "src", "dst", "head_out", "status",
                                  "k_cache", "v_cache"))
