@@ -11,6 +11,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <cmath>
 #include <string>
 
 #include "kq_internal.h"
@@ -646,89 +647,475 @@ int kq_kv_attention_workspace(int64_t tokens, int64_t n_seqs, int64_t q_heads, i
   return KQ_OK;
 }
 
+namespace {
+
+// What kq_kv_attention, kq_kv_attention_sinks and kq_kv_attention_prefix are
+// called with; the latter two's own are 0 and null elsewhere.
+struct AttnCall {
+  int codec;
+  const void* q;
+  int q_dtype;
+  int64_t tokens, q_heads, kv_heads, d, q_stride;
+  const int32_t *cu_new, *seq_lens;
+  int64_t n_seqs;
+  const int32_t* table;
+  int64_t width;
+  const void *k_cache, *v_cache;
+  int64_t pages, page;
+  float scale;
+  int64_t window, sinks;
+  const int32_t* prefix;
+  int64_t n_prefix, max_new, max_kv;
+  void* out;
+  int out_dtype;
+  void* workspace;
+  int64_t workspace_bytes;
+  hipStream_t stream;
+};
+
+// A prefix of n_prefix pages: its keys, and the plan of the keys behind it.
+kq::AttnPlan tail_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
+                       int64_t max_kv, int64_t prefix_len) {
+  const int64_t own = max_kv > prefix_len ? max_kv - prefix_len : 1;
+  return kq::attn_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, own, 0);
+}
+
+int check_prefix(const char* op, int64_t prefix_len) {
+  if (prefix_len < 1 || prefix_len >= (int64_t)1 << 30)
+    return fail(KQ_ERR_ARG, op, "a prefix of %lld keys is out of range (1 .. 2^30 - 1)", (long long)prefix_len);
+  return KQ_OK;
+}
+
+int attention(const char* op, const AttnCall& c) {
+  int shift;
+  int st = check_cache(op, c.codec, c.page, c.d, c.kv_heads, &shift);
+  if (st) return st;
+  if ((st = check_attn_sizes(op, c.tokens, c.n_seqs, c.q_heads, c.kv_heads, c.d, c.max_new, c.max_kv))) return st;
+  if (c.q_dtype != KQ_F16 && c.q_dtype != KQ_BF16)
+    return fail(KQ_ERR_ARG, op, "query dtype %d is not KQ_F16 or KQ_BF16", c.q_dtype);
+  if ((st = check_any_dtype(op, "output", c.out_dtype))) return st;
+  if (c.q_stride < c.q_heads * c.d || c.q_stride >= kMaxDim)
+    return fail(KQ_ERR_SHAPE, op, "row stride %lld out of range (q_heads * d = %lld)", (long long)c.q_stride,
+                (long long)(c.q_heads * c.d));
+  if (c.q_stride % 8) return fail(KQ_ERR_ALIGN, op, "row stride %lld is not a multiple of 8", (long long)c.q_stride);
+  if (c.width < 0 || c.width * c.page >= (int64_t)1 << 30 || c.width >= (int64_t)1 << 30)
+    return fail(KQ_ERR_ARG, op, "width=%lld out of range (width * page below 2^30)", (long long)c.width);
+  if (!(c.scale >= -3.0e38f && c.scale <= 3.0e38f))
+    return fail(KQ_ERR_ARG, op, "scale=%g is not finite", (double)c.scale);
+  if (c.window < 0) return fail(KQ_ERR_ARG, op, "window=%lld is negative", (long long)c.window);
+  if (c.sinks < 0) return fail(KQ_ERR_ARG, op, "sinks=%lld is negative", (long long)c.sinks);
+  // no request is that long
+  const int64_t window = c.window >= (int64_t)1 << 30 || c.sinks >= (int64_t)1 << 30 ? 0 : c.window;
+  const int64_t sinks = window > 0 ? c.sinks : 0;
+  int64_t prefix_len = 0;
+  if (c.prefix) {
+    if (c.n_prefix < 1 || c.n_prefix >= (int64_t)1 << 30)
+      return fail(KQ_ERR_ARG, op, "n_prefix=%lld out of range", (long long)c.n_prefix);
+    prefix_len = c.n_prefix * c.page;
+    if ((st = check_prefix(op, prefix_len))) return st;
+  }
+  if ((st = check_pages(op, c.k_cache, c.v_cache, c.pages, c.page))) return st;
+  if (c.tokens == 0 || c.n_seqs == 0) return KQ_OK;
+  if (!c.q || !c.out || !c.cu_new || !c.seq_lens || (c.width > 0 && !c.table))
+    return fail(KQ_ERR_ARG, op, "null pointer (q=%p out=%p cu_new=%p seq_lens=%p table=%p)", c.q, c.out,
+                (const void*)c.cu_new, (const void*)c.seq_lens, (const void*)c.table);
+  if (!aligned(c.q, 16) || !aligned(c.out, 16))
+    return fail(KQ_ERR_ALIGN, op, "q=%p, out=%p are not 16-byte aligned", c.q, c.out);
+  if (!aligned(c.cu_new, 4) || !aligned(c.seq_lens, 4) || !aligned(c.table, 4) || !aligned(c.prefix, 4))
+    return fail(KQ_ERR_ALIGN, op, "cu_new, seq_lens and table must be 4-byte aligned");
+  const int64_t out_bytes = c.tokens * c.q_heads * c.d * elem_bytes(c.out_dtype);
+  // what the call reads, against what it writes
+  const int64_t cache = c.pages * c.kv_heads * c.page * (c.d / 2 + c.d / 16);
+  const struct { const char* name; const void* p; int64_t bytes; } in[] = {
+      {"q", c.q, ((c.tokens - 1) * c.q_stride + c.q_heads * c.d) * 2}, {"cu_new", c.cu_new, 4 * (c.n_seqs + 1)},
+      {"seq_lens", c.seq_lens, 4 * c.n_seqs}, {"table", c.table, 4 * c.n_seqs * c.width}, {"k_cache", c.k_cache, cache},
+      {"v_cache", c.v_cache, cache}, {"prefix", c.prefix, 4 * c.n_prefix}};
+  for (const auto& r : in)
+    if (r.bytes > 0 && overlaps(r.p, r.bytes, c.out, out_bytes)) return fail(KQ_ERR_ARG, op, "out overlaps %s", r.name);
+  // (the sinks widen what a row sees as so many keys more of its window do)
+  const kq::AttnPlan plan =
+      c.prefix ? tail_plan(c.tokens, c.n_seqs, c.q_heads, c.kv_heads, c.d, c.max_new, c.max_kv, prefix_len)
+               : kq::attn_plan(c.tokens, c.n_seqs, c.q_heads, c.kv_heads, c.d, c.max_new, c.max_kv, window + sinks);
+  kq::PrefixPlan flat = {0, 0, 0, 0};
+  if (c.prefix) flat = kq::prefix_plan(c.tokens, c.q_heads, c.kv_heads, c.d, prefix_len);
+  const int64_t need = flat.bytes + plan.bytes;
+  if (need > 0) {
+    if (!c.workspace || c.workspace_bytes < need)
+      return fail(KQ_ERR_CAPACITY, op, "workspace of %lld bytes is below the %lld these sizes need",
+                  (long long)(c.workspace ? c.workspace_bytes : 0), (long long)need);
+    if (!aligned(c.workspace, 16)) return fail(KQ_ERR_ALIGN, op, "workspace=%p is not 16-byte aligned", c.workspace);
+    if (overlaps(c.workspace, need, c.out, out_bytes)) return fail(KQ_ERR_ARG, op, "workspace overlaps out");
+    for (const auto& r : in)
+      if (r.bytes > 0 && overlaps(r.p, r.bytes, c.workspace, need))
+        return fail(KQ_ERR_ARG, op, "workspace overlaps %s", r.name);
+  }
+  uint8_t* ws = (uint8_t*)c.workspace;
+  kq::AttnArgs a;
+  a.q = c.q;
+  a.cu = c.cu_new;
+  a.lens = c.seq_lens;
+  a.table = c.table;
+  a.kc = (const uint8_t*)c.k_cache;
+  a.vc = (const uint8_t*)c.v_cache;
+  a.out = c.out;
+  a.many = (float*)(ws + flat.bytes);
+  a.few = (float*)(ws + flat.bytes + plan.few_at);
+  a.where = plan.bytes > 0 ? (int32_t*)(ws + flat.bytes + plan.where_at) : nullptr;
+  a.q_stride = c.q_stride;
+  a.width = c.width;
+  a.page_head_bytes = c.page * (c.d / 2 + c.d / 16);
+  a.tokens = (int)c.tokens;
+  a.n_seqs = (int)c.n_seqs;
+  a.hq = (int)c.q_heads;
+  a.hkv = (int)c.kv_heads;
+  a.group = (int)(c.q_heads / c.kv_heads);
+  a.group_shift = (a.group & (a.group - 1)) ? -1 : __builtin_ctz((unsigned)a.group);
+  a.d = (int)c.d;
+  a.pages = (int)c.pages;
+  a.page_shift = shift;
+  a.window = (int)window;
+  a.scale = c.scale;
+  a.q_bf16 = c.q_dtype == KQ_BF16;
+  a.out_type = elem_id(c.out_dtype);
+  a.few_rows = plan.few_rows;
+  a.one_tile = plan.one_tile;
+  a.few_wgs = plan.few_wgs;
+  a.many_wgs = plan.many_wgs;
+  a.many_shift = __builtin_ctz((unsigned)kq::attn_prompt_rows(c.d));
+  a.sinks = (int)sinks;
+  a.prefix = c.prefix;
+  a.prefix_len = (int)prefix_len;
+  a.splits = flat.splits;
+  a.prefix_sums = (float*)ws;
+  if (c.prefix) return hip_status(op, kq::launch_kv_attention_prefix(a, plan, flat, c.stream));
+  if (sinks > 0) return hip_status(op, kq::launch_kv_attention_sinks(a, plan, c.stream));
+  return hip_status(op, kq::launch_kv_attention(a, plan, c.stream));
+}
+
+}  // namespace
+
 int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64_t q_heads, int64_t kv_heads,
                     int64_t d, int64_t q_stride, const int32_t* cu_new, const int32_t* seq_lens, int64_t n_seqs,
                     const int32_t* table, int64_t width, const void* k_cache, const void* v_cache, int64_t pages,
                     int64_t page, float scale, int64_t window, int64_t max_new, int64_t max_kv, void* out,
                     int out_dtype, void* workspace, int64_t workspace_bytes, void* stream) {
-  const char* op = "kq_kv_attention";
-  int shift;
-  int st = check_cache(op, codec, page, d, kv_heads, &shift);
+  return attention("kq_kv_attention",
+                   AttnCall{codec, q, q_dtype, tokens, q_heads, kv_heads, d, q_stride, cu_new, seq_lens, n_seqs, table,
+                            width, k_cache, v_cache, pages, page, scale, window, 0, nullptr, 0, max_new, max_kv, out,
+                            out_dtype, workspace, workspace_bytes, (hipStream_t)stream});
+}
+
+int kq_kv_attention_sinks(int codec, const void* q, int q_dtype, int64_t tokens, int64_t q_heads, int64_t kv_heads,
+                          int64_t d, int64_t q_stride, const int32_t* cu_new, const int32_t* seq_lens, int64_t n_seqs,
+                          const int32_t* table, int64_t width, const void* k_cache, const void* v_cache, int64_t pages,
+                          int64_t page, float scale, int64_t window, int64_t sinks, int64_t max_new, int64_t max_kv,
+                          void* out, int out_dtype, void* workspace, int64_t workspace_bytes, void* stream) {
+  return attention("kq_kv_attention_sinks",
+                   AttnCall{codec, q, q_dtype, tokens, q_heads, kv_heads, d, q_stride, cu_new, seq_lens, n_seqs, table,
+                            width, k_cache, v_cache, pages, page, scale, window, sinks, nullptr, 0, max_new, max_kv,
+                            out, out_dtype, workspace, workspace_bytes, (hipStream_t)stream});
+}
+
+int kq_kv_attention_prefix_workspace(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d,
+                                     int64_t prefix_len, int64_t max_new, int64_t max_kv, int64_t* bytes) {
+  const char* op = "kq_kv_attention_prefix_workspace";
+  int st = check_attn_sizes(op, tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv);
   if (st) return st;
-  if ((st = check_attn_sizes(op, tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv))) return st;
-  if (q_dtype != KQ_F16 && q_dtype != KQ_BF16)
-    return fail(KQ_ERR_ARG, op, "query dtype %d is not KQ_F16 or KQ_BF16", q_dtype);
-  if ((st = check_any_dtype(op, "output", out_dtype))) return st;
-  if (q_stride < q_heads * d || q_stride >= kMaxDim)
-    return fail(KQ_ERR_SHAPE, op, "row stride %lld out of range (q_heads * d = %lld)", (long long)q_stride,
-                (long long)(q_heads * d));
-  if (q_stride % 8) return fail(KQ_ERR_ALIGN, op, "row stride %lld is not a multiple of 8", (long long)q_stride);
-  if (width < 0 || width * page >= (int64_t)1 << 30 || width >= (int64_t)1 << 30)
-    return fail(KQ_ERR_ARG, op, "width=%lld out of range (width * page below 2^30)", (long long)width);
-  if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(KQ_ERR_ARG, op, "scale=%g is not finite", (double)scale);
-  if (window < 0) return fail(KQ_ERR_ARG, op, "window=%lld is negative", (long long)window);
-  if (window >= (int64_t)1 << 30) window = 0;  // no request is that long
-  if ((st = check_pages(op, k_cache, v_cache, pages, page))) return st;
-  if (tokens == 0 || n_seqs == 0) return KQ_OK;
-  if (!q || !out || !cu_new || !seq_lens || (width > 0 && !table))
-    return fail(KQ_ERR_ARG, op, "null pointer (q=%p out=%p cu_new=%p seq_lens=%p table=%p)", q, out,
-                (const void*)cu_new, (const void*)seq_lens, (const void*)table);
-  if (!aligned(q, 16) || !aligned(out, 16)) return fail(KQ_ERR_ALIGN, op, "q=%p, out=%p are not 16-byte aligned", q, out);
-  if (!aligned(cu_new, 4) || !aligned(seq_lens, 4) || !aligned(table, 4))
-    return fail(KQ_ERR_ALIGN, op, "cu_new, seq_lens and table must be 4-byte aligned");
-  const int64_t out_bytes = tokens * q_heads * d * elem_bytes(out_dtype);
-  // what the call reads, against what it writes
-  const int64_t cache = pages * kv_heads * page * (d / 2 + d / 16);
-  const struct { const char* name; const void* p; int64_t bytes; } in[] = {
-      {"q", q, ((tokens - 1) * q_stride + q_heads * d) * 2}, {"cu_new", cu_new, 4 * (n_seqs + 1)},
-      {"seq_lens", seq_lens, 4 * n_seqs}, {"table", table, 4 * n_seqs * width}, {"k_cache", k_cache, cache},
-      {"v_cache", v_cache, cache}};
-  for (const auto& r : in)
-    if (r.bytes > 0 && overlaps(r.p, r.bytes, out, out_bytes)) return fail(KQ_ERR_ARG, op, "out overlaps %s", r.name);
-  const kq::AttnPlan plan = kq::attn_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv, window);
-  if (plan.bytes > 0) {
-    if (!workspace || workspace_bytes < plan.bytes)
-      return fail(KQ_ERR_CAPACITY, op, "workspace of %lld bytes is below the %lld these sizes need",
-                  (long long)(workspace ? workspace_bytes : 0), (long long)plan.bytes);
-    if (!aligned(workspace, 16)) return fail(KQ_ERR_ALIGN, op, "workspace=%p is not 16-byte aligned", workspace);
-    if (overlaps(workspace, plan.bytes, out, out_bytes)) return fail(KQ_ERR_ARG, op, "workspace overlaps out");
-    for (const auto& r : in)
-      if (r.bytes > 0 && overlaps(r.p, r.bytes, workspace, plan.bytes))
-        return fail(KQ_ERR_ARG, op, "workspace overlaps %s", r.name);
+  if ((st = check_prefix(op, prefix_len))) return st;
+  if (!bytes) return fail(KQ_ERR_ARG, op, "null output");
+  *bytes = tokens == 0 || n_seqs == 0
+               ? 0
+               : kq::prefix_plan(tokens, q_heads, kv_heads, d, prefix_len).bytes +
+                     tail_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv, prefix_len).bytes;
+  return KQ_OK;
+}
+
+int kq_kv_attention_prefix(int codec, const void* q, int q_dtype, int64_t tokens, int64_t q_heads, int64_t kv_heads,
+                           int64_t d, int64_t q_stride, const int32_t* cu_new, const int32_t* seq_lens, int64_t n_seqs,
+                           const int32_t* table, int64_t width, const int32_t* prefix, int64_t n_prefix,
+                           const void* k_cache, const void* v_cache, int64_t pages, int64_t page, float scale,
+                           int64_t max_new, int64_t max_kv, void* out, int out_dtype, void* workspace,
+                           int64_t workspace_bytes, void* stream) {
+  if (!prefix) return fail(KQ_ERR_ARG, "kq_kv_attention_prefix", "null prefix");
+  return attention("kq_kv_attention_prefix",
+                   AttnCall{codec, q, q_dtype, tokens, q_heads, kv_heads, d, q_stride, cu_new, seq_lens, n_seqs, table,
+                            width, k_cache, v_cache, pages, page, scale, 0, 0, prefix, n_prefix, max_new, max_kv, out,
+                            out_dtype, workspace, workspace_bytes, (hipStream_t)stream});
+}
+
+// ---- pages of the cache ----
+
+namespace {
+
+// Device arrays of 32-bit integers of a call: alignment, and no output over an
+// input or another output (`same` inputs may be the output of that index).
+struct Ints {
+  const char* name;
+  const void* p;
+  int64_t n;
+  int out;       // 0 read, 1 written
+  int in_place;  // 1 + index of the entry that this output may be
+};
+int check_ints(const char* op, const Ints* x, int n) {
+  for (int i = 0; i < n; ++i) {
+    if (x[i].n <= 0 || !x[i].p) continue;
+    if (!aligned(x[i].p, 4)) return fail(KQ_ERR_ALIGN, op, "%s=%p is not 4-byte aligned", x[i].name, x[i].p);
+    if (!x[i].out) continue;
+    for (int j = 0; j < n; ++j) {
+      if (j == i || x[j].n <= 0 || !x[j].p || (x[i].in_place == 1 + j && x[i].p == x[j].p)) continue;
+      if (x[j].out && j > i) continue;  // seen from there
+      if (overlaps(x[j].p, 4 * x[j].n, x[i].p, 4 * x[i].n))
+        return fail(KQ_ERR_ARG, op, "%s overlaps %s", x[i].name, x[j].name);
+    }
   }
-  kq::AttnArgs a;
+  return KQ_OK;
+}
+int check_count(const char* op, const char* name, int64_t n, int64_t least, int64_t most) {
+  if (n < least || n > most)
+    return fail(KQ_ERR_ARG, op, "%s=%lld out of %lld..%lld", name, (long long)n, (long long)least, (long long)most);
+  return KQ_OK;
+}
+int check_table(const char* op, int64_t n_seqs, int64_t width) {
+  int st = check_count(op, "n_seqs", n_seqs, 0, kMaxSeqs);
+  if (st || (st = check_count(op, "width", width, 0, kMaxDim - 1))) return st;
+  return n_seqs * width >= kMaxElems ? fail(KQ_ERR_ARG, op, "width=%lld out of range", (long long)width) : KQ_OK;
+}
+
+}  // namespace
+
+int kq_kv_fork(const int32_t* parents, const int32_t* children, const int32_t* lens, int64_t n, int64_t page,
+               int32_t* table, int64_t n_seqs, int64_t width, int32_t* refs, int64_t pages, const int32_t* free_pages,
+               int64_t n_free, const int32_t* free_head, int32_t* copy_src, int32_t* copy_dst, int32_t* free_head_out,
+               uint32_t* status, void* stream) {
+  const char* op = "kq_kv_fork";
+  int shift;
+  int st = check_cache(op, KQ_Q4_0, page, 32, 1, &shift);
+  if (st || (st = check_count(op, "n", n, 0, kMaxSeqs)) || (st = check_table(op, n_seqs, width)) ||
+      (st = check_count(op, "pages", pages, 1, kMaxDim - 1)) || (st = check_count(op, "n_free", n_free, 0, kMaxDim - 1)))
+    return st;
+  if (!free_head || !free_head_out) return fail(KQ_ERR_ARG, op, "null free_head or free_head_out");
+  if (n > 0 && (!parents || !children || !lens || !copy_src || !copy_dst || !refs || (n_seqs * width > 0 && !table)))
+    return fail(KQ_ERR_ARG, op, "null parents, children, lens, table, refs, copy_src or copy_dst");
+  if (n_free > 0 && !free_pages) return fail(KQ_ERR_ARG, op, "null free_pages");
+  const Ints x[] = {{"parents", parents, n, 0, 0}, {"children", children, n, 0, 0}, {"lens", lens, n, 0, 0},
+                    {"free_pages", free_pages, n_free, 0, 0}, {"free_head", free_head, 1, 0, 0},
+                    {"table", table, n_seqs * width, 1, 0}, {"refs", refs, pages, 1, 0}, {"copy_src", copy_src, n, 1, 0},
+                    {"copy_dst", copy_dst, n, 1, 0}, {"free_head_out", free_head_out, 1, 1, 0}, {"status", status, 1, 1, 0}};
+  if ((st = check_ints(op, x, 11))) return st;
+  return hip_status(op, kq::launch_kv_fork(parents, children, lens, n, shift, table, n_seqs, width, refs, pages, free_pages,
+                                           n_free, free_head, copy_src, copy_dst, free_head_out, status,
+                                           (hipStream_t)stream));
+}
+
+int kq_kv_free(const int32_t* first, const int32_t* last, int64_t n_seqs, const int32_t* table, int64_t width,
+               int32_t* refs, int64_t pages, int32_t* free_pages, int64_t n_free, const int32_t* free_head,
+               int32_t* free_head_out, uint32_t* status, void* stream) {
+  const char* op = "kq_kv_free";
+  int st = check_table(op, n_seqs, width);
+  if (st || (st = check_count(op, "pages", pages, 1, kMaxDim - 1)) || (st = check_count(op, "n_free", n_free, 0, kMaxDim - 1)))
+    return st;
+  if (!refs || !free_head || !free_head_out) return fail(KQ_ERR_ARG, op, "null refs, free_head or free_head_out");
+  if (n_seqs > 0 && (!first || !last || (width > 0 && !table))) return fail(KQ_ERR_ARG, op, "null first, last or table");
+  if (n_free > 0 && !free_pages) return fail(KQ_ERR_ARG, op, "null free_pages");
+  const Ints x[] = {{"first", first, n_seqs, 0, 0}, {"last", last, n_seqs, 0, 0}, {"table", table, n_seqs * width, 0, 0},
+                    {"free_head", free_head, 1, 0, 0}, {"refs", refs, pages, 1, 0}, {"free_pages", free_pages, n_free, 1, 0},
+                    {"free_head_out", free_head_out, 1, 1, 0}, {"status", status, 1, 1, 0}};
+  if ((st = check_ints(op, x, 8))) return st;
+  return hip_status(op, kq::launch_kv_free(first, last, n_seqs, table, width, refs, pages, free_pages, n_free, free_head,
+                                           free_head_out, status, (hipStream_t)stream));
+}
+
+int kq_kv_compact(const int32_t* free_pages, int64_t n_free, const int32_t* free_head, const int32_t* table,
+                  int64_t n_entries, const int32_t* refs, int64_t pages, int32_t* table_out, int32_t* refs_out,
+                  int32_t* free_out, int32_t* remap, int32_t* copy_src, int32_t* copy_dst, int64_t n_copy,
+                  int32_t* free_head_out, uint32_t* status, void* stream) {
+  const char* op = "kq_kv_compact";
+  int st = check_count(op, "pages", pages, 1, kq::COMPACT_PAGES);
+  if (st || (st = check_count(op, "n_free", n_free, 0, kMaxDim - 1)) ||
+      (st = check_count(op, "n_entries", n_entries, 0, kMaxElems - 1)) ||
+      (st = check_count(op, "n_copy", n_copy, 0, kMaxDim - 1)))
+    return st;
+  const int64_t most = pages / 2 < n_free ? pages / 2 : n_free;
+  if (n_copy < most)
+    return fail(KQ_ERR_CAPACITY, op, "n_copy=%lld is below the %lld pages that may move", (long long)n_copy, (long long)most);
+  if (!free_head || !free_head_out || !remap || !refs || !refs_out)
+    return fail(KQ_ERR_ARG, op, "null free_head, free_head_out, remap, refs or refs_out");
+  if ((n_free > 0 && (!free_pages || !free_out)) || (n_entries > 0 && (!table || !table_out)) ||
+      (n_copy > 0 && (!copy_src || !copy_dst)))
+    return fail(KQ_ERR_ARG, op, "null free_pages, free_out, table, table_out, copy_src or copy_dst");
+  const Ints x[] = {{"free_pages", free_pages, n_free, 0, 0}, {"free_head", free_head, 1, 0, 0},
+                    {"table", table, n_entries, 0, 0}, {"refs", refs, pages, 0, 0}, {"table_out", table_out, n_entries, 1, 3},
+                    {"refs_out", refs_out, pages, 1, 4}, {"free_out", free_out, n_free, 1, 1}, {"remap", remap, pages, 1, 0},
+                    {"copy_src", copy_src, n_copy, 1, 0}, {"copy_dst", copy_dst, n_copy, 1, 0},
+                    {"free_head_out", free_head_out, 1, 1, 2}, {"status", status, 1, 1, 0}};
+  if ((st = check_ints(op, x, 12))) return st;
+  return hip_status(op, kq::launch_kv_compact(free_pages, n_free, free_head, table, n_entries, refs, pages, table_out,
+                                              refs_out, free_out, remap, copy_src, copy_dst, n_copy, free_head_out,
+                                              status, (hipStream_t)stream));
+}
+
+int kq_kv_copy_pages(const int32_t* src, const int32_t* dst, int64_t n, void* k_cache, void* v_cache, int64_t pages,
+                     int64_t bytes, void* stream) {
+  const char* op = "kq_kv_copy_pages";
+  int st = check_count(op, "n", n, 0, kMaxDim - 1);
+  if (st || (st = check_count(op, "pages", pages, 1, kMaxDim - 1))) return st;
+  if (bytes < 16 || bytes >= kMaxDim || bytes % 16)
+    return fail(KQ_ERR_SHAPE, op, "bytes=%lld of a page is not a multiple of 16 below 2^31", (long long)bytes);
+  if (!k_cache || !v_cache) return fail(KQ_ERR_ARG, op, "null cache (k_cache=%p v_cache=%p)", k_cache, v_cache);
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return fail(KQ_ERR_ALIGN, op, "caches must be 16-byte aligned");
+  const int64_t cache = pages * bytes;
+  if (overlaps(k_cache, cache, v_cache, cache)) return fail(KQ_ERR_ARG, op, "k_cache and v_cache overlap");
+  if (n == 0) return KQ_OK;
+  if (!src || !dst) return fail(KQ_ERR_ARG, op, "null src or dst");
+  if (!aligned(src, 4) || !aligned(dst, 4)) return fail(KQ_ERR_ALIGN, op, "src and dst must be 4-byte aligned");
+  for (const void* c : {k_cache, v_cache})
+    if (overlaps(src, 4 * n, c, cache) || overlaps(dst, 4 * n, c, cache))
+      return fail(KQ_ERR_ARG, op, "src or dst overlaps a cache");
+  return hip_status(op, kq::launch_kv_copy_pages(src, dst, n, (uint8_t*)k_cache, (uint8_t*)v_cache, pages, bytes,
+                                                 (hipStream_t)stream));
+}
+
+// ---- rotary positions ----
+
+int kq_rope_freqs(int64_t rot, double base, int scaling, double factor, int64_t original, double fast, double slow,
+                  const float* factors, float* inv_freq, float* mscale) {
+  const char* op = "kq_rope_freqs";
+  if (rot < 2 || rot > 4096 || rot % 2) return fail(KQ_ERR_SHAPE, op, "rot=%lld is not even in 2..4096", (long long)rot);
+  if (!(base > 1. && base <= 1e30)) return fail(KQ_ERR_ARG, op, "base=%g is not above 1 (at most 1e30)", base);
+  if (scaling < KQ_ROPE_NONE || scaling > KQ_ROPE_YARN) return fail(KQ_ERR_ARG, op, "scaling=%d is unknown", scaling);
+  if (scaling != KQ_ROPE_NONE && !(factor >= 1. && factor <= 1e6))
+    return fail(KQ_ERR_ARG, op, "factor=%g out of 1..1e6", factor);
+  if (scaling == KQ_ROPE_NTK && rot < 4) return fail(KQ_ERR_SHAPE, op, "rot=%lld is below 4", (long long)rot);
+  if (scaling == KQ_ROPE_YARN && (original < 1 || !(fast > slow && slow > 0. && fast <= 1e9)))
+    return fail(KQ_ERR_ARG, op, "original=%lld, fast=%g, slow=%g: wanted are original >= 1 and fast > slow > 0",
+                (long long)original, fast, slow);
+  if (!inv_freq || !mscale) return fail(KQ_ERR_ARG, op, "null output");
+  const int64_t pairs = rot / 2;
+  if (factors)
+    for (int64_t i = 0; i < pairs; ++i)
+      if (!(factors[i] > 0.f && factors[i] <= 1e30f)) return fail(KQ_ERR_ARG, op, "factors[%lld]=%g", (long long)i, factors[i]);
+  // NTK: the lowest frequency is divided by `factor`, the highest stays
+  if (scaling == KQ_ROPE_NTK) base *= std::pow(factor, (double)rot / (double)(rot - 2));
+  double lo = 0., hi = 1.;
+  if (scaling == KQ_ROPE_YARN) {
+    // the pair that makes `turns` turns over the original length
+    const auto at = [&](double turns) {
+      return (double)rot * std::log((double)original / (turns * 2. * M_PI)) / (2. * std::log(base));
+    };
+    lo = std::floor(at(fast));
+    hi = std::ceil(at(slow));
+    lo = lo < 0. ? 0. : lo;
+    hi = hi > (double)(rot - 1) ? (double)(rot - 1) : hi;
+  }
+  for (int64_t i = 0; i < pairs; ++i) {
+    double f = std::pow(base, -2. * (double)i / (double)rot);
+    if (factors) f /= (double)factors[i];
+    if (scaling == KQ_ROPE_LINEAR) f /= factor;
+    if (scaling == KQ_ROPE_YARN) {
+      const double span = hi - lo > 0.001 ? hi - lo : 0.001;
+      double r = ((double)i - lo) / span;
+      r = r < 0. ? 0. : r > 1. ? 1. : r;
+      f = f / factor * r + f * (1. - r);
+    }
+    inv_freq[i] = (float)f;
+  }
+  *mscale = scaling == KQ_ROPE_YARN ? (float)(0.1 * std::log(factor) + 1.) : 1.f;
+  return KQ_OK;
+}
+
+namespace {
+
+// Rows of heads * d elements, `stride` apart.
+struct Rows {
+  const void* p;
+  int64_t stride, width;
+};
+// Whether rows of a and b (bytes) share any: rows of the same stride may lie
+// side by side, as slices of one buffer do.
+bool rows_overlap(const Rows& a, const Rows& b, int64_t tokens, int64_t es) {
+  if (!a.p || !b.p || tokens == 0) return false;
+  if (!overlaps(a.p, ((tokens - 1) * a.stride + a.width) * es, b.p, ((tokens - 1) * b.stride + b.width) * es)) return false;
+  if (a.stride != b.stride) return true;
+  const int64_t s = a.stride * es, at = (((intptr_t)b.p - (intptr_t)a.p) % s + s) % s;
+  return at < a.width * es || at + b.width * es > s;
+}
+
+}  // namespace
+
+int kq_rope(const void* q, int64_t q_heads, int64_t q_stride, const void* k, int64_t kv_heads, int64_t k_stride,
+            int dtype, int64_t tokens, int64_t d, int64_t rot, int layout, const int32_t* cu_new,
+            const int32_t* seq_lens, int64_t n_seqs, const float* inv_freq, float mscale, void* q_out,
+            int64_t q_out_stride, void* k_out, int64_t k_out_stride, void* stream) {
+  const char* op = "kq_rope";
+  int st = check_any_dtype(op, "row", dtype);
+  if (st) return st;
+  if (d < 32 || d > 256 || d % 32) return fail(KQ_ERR_SHAPE, op, "d=%lld is not a multiple of 32 in 32..256", (long long)d);
+  if (rot < 8 || rot > d || rot % 8)
+    return fail(KQ_ERR_SHAPE, op, "rot=%lld is not a multiple of 8 in 8..d=%lld", (long long)rot, (long long)d);
+  if (layout != KQ_ROPE_HALF && layout != KQ_ROPE_PAIRS) return fail(KQ_ERR_ARG, op, "layout=%d is unknown", layout);
+  if ((st = check_count(op, "q_heads", q_heads, 0, 4096)) || (st = check_count(op, "kv_heads", kv_heads, 0, 4096)) ||
+      (st = check_count(op, "n_seqs", n_seqs, 0, kMaxSeqs)))
+    return st;
+  if (tokens < 0 || tokens >= kMaxDim || tokens * (q_heads + kv_heads) * d >= (int64_t)1 << 34)
+    return fail(KQ_ERR_ARG, op, "tokens=%lld out of range", (long long)tokens);
+  if (!(mscale >= -3.0e38f && mscale <= 3.0e38f)) return fail(KQ_ERR_ARG, op, "mscale=%g is not finite", (double)mscale);
+  const struct { const char* name; int64_t stride, heads; } strides[] = {
+      {"q", q_stride, q_heads}, {"k", k_stride, kv_heads}, {"q_out", q_out_stride, q_heads}, {"k_out", k_out_stride, kv_heads}};
+  for (const auto& r : strides) {
+    if (r.heads == 0) continue;
+    if (r.stride < r.heads * d || r.stride >= kMaxDim)
+      return fail(KQ_ERR_SHAPE, op, "%s's row stride %lld out of range (heads * d = %lld)", r.name, (long long)r.stride,
+                  (long long)(r.heads * d));
+    if (r.stride % 8) return fail(KQ_ERR_ALIGN, op, "%s's row stride %lld is not a multiple of 8", r.name, (long long)r.stride);
+  }
+  if (tokens == 0 || n_seqs == 0 || q_heads + kv_heads == 0) return KQ_OK;
+  if ((q_heads > 0 && (!q || !q_out)) || (kv_heads > 0 && (!k || !k_out)) || !cu_new || !seq_lens || !inv_freq)
+    return fail(KQ_ERR_ARG, op, "null pointer (q=%p k=%p cu_new=%p seq_lens=%p inv_freq=%p q_out=%p k_out=%p)", q, k,
+                (const void*)cu_new, (const void*)seq_lens, (const void*)inv_freq, q_out, k_out);
+  if (q_heads == 0) q = q_out = nullptr;
+  if (kv_heads == 0) k = k_out = nullptr;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(q_out, 16) || !aligned(k_out, 16))
+    return fail(KQ_ERR_ALIGN, op, "q=%p, k=%p, q_out=%p, k_out=%p are not 16-byte aligned", q, k, q_out, k_out);
+  if (!aligned(cu_new, 4) || !aligned(seq_lens, 4) || !aligned(inv_freq, 4))
+    return fail(KQ_ERR_ALIGN, op, "cu_new, seq_lens and inv_freq must be 4-byte aligned");
+  const int64_t es = elem_bytes(dtype);
+  const Rows in[] = {{q, q_stride, q_heads * d}, {k, k_stride, kv_heads * d}};
+  const Rows out[] = {{q_out, q_out_stride, q_heads * d}, {k_out, k_out_stride, kv_heads * d}};
+  const struct { const char* name; const void* p; int64_t bytes; } small[] = {
+      {"cu_new", cu_new, 4 * (n_seqs + 1)}, {"seq_lens", seq_lens, 4 * n_seqs}, {"inv_freq", inv_freq, 2 * rot}};
+  for (int i = 0; i < 2; ++i) {
+    const bool in_place = out[i].p == in[i].p && out[i].stride == in[i].stride;
+    for (int j = 0; j < 2; ++j)
+      if (!(i == j && in_place) && rows_overlap(out[i], in[j], tokens, es))
+        return fail(KQ_ERR_ARG, op, "%s overlaps %s", i ? "k_out" : "q_out", j ? "k" : "q");
+    if (out[i].p)
+      for (const auto& r : small)
+        if (overlaps(r.p, r.bytes, out[i].p, ((tokens - 1) * out[i].stride + out[i].width) * es))
+          return fail(KQ_ERR_ARG, op, "%s overlaps %s", i ? "k_out" : "q_out", r.name);
+  }
+  if (rows_overlap(out[0], out[1], tokens, es)) return fail(KQ_ERR_ARG, op, "q_out and k_out overlap");
+  kq::RopeArgs a;
   a.q = q;
+  a.k = k;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.q_out_stride = q_out_stride;
+  a.k_out_stride = k_out_stride;
   a.cu = cu_new;
   a.lens = seq_lens;
-  a.table = table;
-  a.kc = (const uint8_t*)k_cache;
-  a.vc = (const uint8_t*)v_cache;
-  a.out = out;
-  a.many = (float*)workspace;
-  a.few = (float*)((uint8_t*)workspace + plan.few_at);
-  a.where = plan.bytes > 0 ? (int32_t*)((uint8_t*)workspace + plan.where_at) : nullptr;
-  a.q_stride = q_stride;
-  a.width = width;
-  a.page_head_bytes = page * (d / 2 + d / 16);
+  a.inv_freq = inv_freq;
+  a.mscale = mscale;
   a.tokens = (int)tokens;
   a.n_seqs = (int)n_seqs;
   a.hq = (int)q_heads;
   a.hkv = (int)kv_heads;
-  a.group = (int)(q_heads / kv_heads);
-  a.group_shift = (a.group & (a.group - 1)) ? -1 : __builtin_ctz((unsigned)a.group);
   a.d = (int)d;
-  a.pages = (int)pages;
-  a.page_shift = shift;
-  a.window = (int)window;
-  a.scale = scale;
-  a.q_bf16 = q_dtype == KQ_BF16;
-  a.out_type = elem_id(out_dtype);
-  a.few_rows = plan.few_rows;
-  a.one_tile = plan.one_tile;
-  a.few_wgs = plan.few_wgs;
-  a.many_wgs = plan.many_wgs;
-  a.many_shift = __builtin_ctz((unsigned)kq::attn_prompt_rows(d));
-  return hip_status(op, kq::launch_kv_attention(a, plan, (hipStream_t)stream));
+  a.rot = (int)rot;
+  a.copy_q = q_out != q || q_out_stride != q_stride;
+  a.copy_k = k_out != k || k_out_stride != k_stride;
+  return hip_status(op, kq::launch_rope(a, elem_id(dtype), layout == KQ_ROPE_PAIRS, (hipStream_t)stream));
 }
 
 }  // extern "C"

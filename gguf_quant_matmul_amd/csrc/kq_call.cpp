@@ -45,12 +45,14 @@ bool rows(const at::Tensor* x, int64_t* stride) {
 }
 
 // two caches uint8 [pages, kv_heads, page_bytes]
+bool byte_caches(PyObject* ko, PyObject* vo, long device, const at::Tensor** k, const at::Tensor** v) {
+  return tensor(ko, device, k) && tensor(vo, device, v) && (*k)->scalar_type() == at::kByte &&
+         (*v)->scalar_type() == at::kByte && (*k)->dim() == 3 && (*k)->sizes() == (*v)->sizes() && (*k)->is_contiguous() &&
+         (*v)->is_contiguous();
+}
 bool caches(PyObject* ko, PyObject* vo, long device, int64_t page, int64_t d, const at::Tensor** k,
             const at::Tensor** v) {
-  if (!tensor(ko, device, k) || !tensor(vo, device, v)) return false;
-  if ((*k)->scalar_type() != at::kByte || (*v)->scalar_type() != at::kByte || (*k)->dim() != 3 ||
-      (*k)->sizes() != (*v)->sizes() || !(*k)->is_contiguous() || !(*v)->is_contiguous())
-    return false;
+  if (!byte_caches(ko, vo, device, k, v)) return false;
   int64_t bytes;
   return kq_kv_page_bytes(KQ_Q4_0, page, d, &bytes) == KQ_OK && (*k)->size(2) == bytes;
 }
@@ -58,6 +60,15 @@ bool caches(PyObject* ko, PyObject* vo, long device, int64_t page, int64_t d, co
 bool number(PyObject* o, int64_t* v) {
   *v = PyLong_AsLongLong(o);
   if (*v == -1 && PyErr_Occurred()) {
+    PyErr_Clear();
+    return false;
+  }
+  return true;
+}
+
+bool real(PyObject* o, double* v) {
+  *v = PyFloat_AsDouble(o);
+  if (*v == -1.0 && PyErr_Occurred()) {
     PyErr_Clear();
     return false;
   }
@@ -132,35 +143,166 @@ PyObject* block_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// (q, cu_new, seq_lens, table, k_cache, v_cache, page, out, scale, window, max_new, max_kv, workspace or None, stream,
-//  device); no workspace only where none is needed
-PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) {
+// An attention call: q, cu_new, seq_lens, table, [prefix,] k_cache, v_cache, page, out, scale, [window, [sinks,]]
+// max_new, max_kv, workspace or None, stream, device; no workspace only where none is needed.
+enum Kind { PLAIN, SINKS, PREFIX };
+template <Kind K>
+PyObject* attention(PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
-    const at::Tensor *q, *cu, *lens, *table, *kc, *vc, *out, *ws = nullptr;
-    int64_t page, window, max_new, max_kv, stream, device, qs;
-    if (n != 15 || !number(a[6], &page) || !number(a[9], &window) || !number(a[10], &max_new) ||
-        !number(a[11], &max_kv) || !number(a[13], &stream) || !number(a[14], &device))
+    const at::Tensor *q, *cu, *lens, *table, *prefix = nullptr, *kc, *vc, *out, *ws = nullptr;
+    int64_t page, window = 0, sinks = 0, max_new, max_kv, stream, device, qs;
+    // places behind the table, behind the scale, behind the windows
+    constexpr int at = K == PREFIX ? 5 : 4, win = at + 5, end = win + (K == PLAIN ? 1 : K == SINKS ? 2 : 0);
+    if (n != end + 5 || !number(a[at + 2], &page) || (K != PREFIX && !number(a[win], &window)) ||
+        (K == SINKS && !number(a[win + 1], &sinks)) || !number(a[end], &max_new) || !number(a[end + 1], &max_kv) ||
+        !number(a[end + 3], &stream) || !number(a[end + 4], &device))
       Py_RETURN_NONE;
-    const double scale = PyFloat_AsDouble(a[8]);
-    if (scale == -1.0 && PyErr_Occurred()) {
-      PyErr_Clear();
-      Py_RETURN_NONE;
-    }
-    if (!tensor(a[0], device, &q) || !tensor(a[7], device, &out) || !rows(q, &qs) || q->sizes() != out->sizes() ||
+    double scale;
+    if (!real(a[at + 4], &scale)) Py_RETURN_NONE;
+    if (!tensor(a[0], device, &q) || !tensor(a[at + 3], device, &out) || !rows(q, &qs) || q->sizes() != out->sizes() ||
         !out->is_contiguous() || dtype(q) < 0 || dtype(out) < 0)
       Py_RETURN_NONE;
     if (!ints(a[2], device, -1, &lens) || !ints(a[3], device, -1, &table)) Py_RETURN_NONE;
+    if (K == PREFIX && !ints(a[4], device, -1, &prefix)) Py_RETURN_NONE;
     const int64_t m = lens->numel(), tokens = q->size(0), heads = q->size(1), d = q->size(2);
     if (!ints(a[1], device, m + 1, &cu) || table->dim() != 2 || table->size(0) != m) Py_RETURN_NONE;
-    if (!caches(a[4], a[5], device, page, d, &kc, &vc)) Py_RETURN_NONE;
-    if (a[12] != Py_None && (!tensor(a[12], device, &ws) || !ws->is_contiguous())) Py_RETURN_NONE;
-    const int st = kq_kv_attention(KQ_Q4_0, q->data_ptr(), dtype(q), tokens, heads, kc->size(1), d, qs, ptr(cu),
-                                   ptr(lens), m, ptr(table), table->size(1), kc->data_ptr(), vc->data_ptr(),
-                                   kc->size(0), page, (float)scale, window, max_new, max_kv, out->data_ptr(),
-                                   dtype(out), ws ? ws->data_ptr() : nullptr,
-                                   ws ? (int64_t)ws->nbytes() : 0, (void*)stream);
+    if (!caches(a[at], a[at + 1], device, page, d, &kc, &vc)) Py_RETURN_NONE;
+    PyObject* wo = a[end + 2];
+    if (wo != Py_None && (!tensor(wo, device, &ws) || !ws->is_contiguous())) Py_RETURN_NONE;
+    void* wp = ws ? ws->data_ptr() : nullptr;
+    const int64_t wn = ws ? (int64_t)ws->nbytes() : 0;
+    int st;
+    if constexpr (K == PLAIN)
+      st = kq_kv_attention(KQ_Q4_0, q->data_ptr(), dtype(q), tokens, heads, kc->size(1), d, qs, ptr(cu), ptr(lens), m,
+                           ptr(table), table->size(1), kc->data_ptr(), vc->data_ptr(), kc->size(0), page, (float)scale,
+                           window, max_new, max_kv, out->data_ptr(), dtype(out), wp, wn, (void*)stream);
+    else if constexpr (K == SINKS)
+      st = kq_kv_attention_sinks(KQ_Q4_0, q->data_ptr(), dtype(q), tokens, heads, kc->size(1), d, qs, ptr(cu), ptr(lens), m,
+                                 ptr(table), table->size(1), kc->data_ptr(), vc->data_ptr(), kc->size(0), page,
+                                 (float)scale, window, sinks, max_new, max_kv, out->data_ptr(), dtype(out), wp, wn,
+                                 (void*)stream);
+    else
+      st = kq_kv_attention_prefix(KQ_Q4_0, q->data_ptr(), dtype(q), tokens, heads, kc->size(1), d, qs, ptr(cu), ptr(lens), m,
+                                  ptr(table), table->size(1), ptr(prefix), prefix->numel(), kc->data_ptr(), vc->data_ptr(),
+                                  kc->size(0), page, (float)scale, max_new, max_kv, out->data_ptr(), dtype(out), wp, wn,
+                                  (void*)stream);
     if (st == KQ_ERR_CAPACITY && !ws) Py_RETURN_NONE;  // the caller allocates one
     return status(st);
+  });
+}
+PyObject* kv_attention(PyObject*, PyObject* const* a, Py_ssize_t n) { return attention<PLAIN>(a, n); }
+PyObject* kv_attention_sinks(PyObject*, PyObject* const* a, Py_ssize_t n) { return attention<SINKS>(a, n); }
+PyObject* kv_attention_prefix(PyObject*, PyObject* const* a, Py_ssize_t n) { return attention<PREFIX>(a, n); }
+
+// one count or head, or None
+bool maybe_one(PyObject* o, long device, const at::Tensor** t) {
+  *t = nullptr;
+  return o == Py_None || ints(o, device, 1, t);
+}
+
+// (parents, children, lens, page, table, refs, free_pages, free_head, copy_src, copy_dst, free_head_out, status or None,
+//  stream, device)
+PyObject* kv_fork(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *parents, *children, *lens, *table, *refs, *fp, *fh, *src, *dst, *ho, *st;
+    int64_t page, stream, device;
+    if (n != 14 || !number(a[3], &page) || !number(a[12], &stream) || !number(a[13], &device)) Py_RETURN_NONE;
+    if (!ints(a[0], device, -1, &parents)) Py_RETURN_NONE;
+    const int64_t m = parents->numel();
+    if (!ints(a[1], device, m, &children) || !ints(a[2], device, m, &lens) || !ints(a[4], device, -1, &table) ||
+        table->dim() != 2 || !ints(a[5], device, -1, &refs) || !ints(a[6], device, -1, &fp) || !ints(a[7], device, 1, &fh) ||
+        !ints(a[8], device, m, &src) || !ints(a[9], device, m, &dst) || !ints(a[10], device, 1, &ho) ||
+        !maybe_one(a[11], device, &st))
+      Py_RETURN_NONE;
+    return status(kq_kv_fork(ptr(parents), ptr(children), ptr(lens), m, page, ptr(table), table->size(0), table->size(1),
+                             ptr(refs), refs->numel(), ptr(fp), fp->numel(), ptr(fh), ptr(src), ptr(dst), ptr(ho),
+                             st ? (uint32_t*)ptr(st) : nullptr, (void*)stream));
+  });
+}
+
+// (first, last, table, refs, free_pages, free_head, free_head_out, status or None, stream, device)
+PyObject* kv_free(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *first, *last, *table, *refs, *fp, *fh, *ho, *st;
+    int64_t stream, device;
+    if (n != 10 || !number(a[8], &stream) || !number(a[9], &device)) Py_RETURN_NONE;
+    if (!ints(a[0], device, -1, &first)) Py_RETURN_NONE;
+    const int64_t m = first->numel();
+    if (!ints(a[1], device, m, &last) || !ints(a[2], device, -1, &table) || table->dim() != 2 || table->size(0) != m ||
+        !ints(a[3], device, -1, &refs) || !ints(a[4], device, -1, &fp) || !ints(a[5], device, 1, &fh) ||
+        !ints(a[6], device, 1, &ho) || !maybe_one(a[7], device, &st))
+      Py_RETURN_NONE;
+    return status(kq_kv_free(ptr(first), ptr(last), m, ptr(table), table->size(1), ptr(refs), refs->numel(), ptr(fp),
+                             fp->numel(), ptr(fh), ptr(ho), st ? (uint32_t*)ptr(st) : nullptr, (void*)stream));
+  });
+}
+
+// (free_pages, free_head, table, refs, table_out, refs_out, free_out, remap, copy_src, copy_dst, free_head_out,
+//  status or None, stream, device)
+PyObject* kv_compact(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *fp, *fh, *table, *refs, *to, *ro, *fo, *remap, *src, *dst, *ho, *st;
+    int64_t stream, device;
+    if (n != 14 || !number(a[12], &stream) || !number(a[13], &device)) Py_RETURN_NONE;
+    if (!ints(a[0], device, -1, &fp) || !ints(a[1], device, 1, &fh) || !ints(a[2], device, -1, &table) ||
+        !ints(a[3], device, -1, &refs) || !ints(a[8], device, -1, &src))
+      Py_RETURN_NONE;
+    const int64_t pages = refs->numel(), entries = table->numel(), n_free = fp->numel(), n_copy = src->numel();
+    if (!ints(a[4], device, entries, &to) || !ints(a[5], device, pages, &ro) || !ints(a[6], device, n_free, &fo) ||
+        !ints(a[7], device, pages, &remap) || !ints(a[9], device, n_copy, &dst) || !ints(a[10], device, 1, &ho) ||
+        !maybe_one(a[11], device, &st))
+      Py_RETURN_NONE;
+    return status(kq_kv_compact(ptr(fp), n_free, ptr(fh), ptr(table), entries, ptr(refs), pages, ptr(to), ptr(ro), ptr(fo),
+                                ptr(remap), ptr(src), ptr(dst), n_copy, ptr(ho), st ? (uint32_t*)ptr(st) : nullptr,
+                                (void*)stream));
+  });
+}
+
+// (src, dst, k_cache, v_cache, stream, device)
+PyObject* kv_copy_pages(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *src, *dst, *k, *v;
+    int64_t stream, device;
+    if (n != 6 || !number(a[4], &stream) || !number(a[5], &device)) Py_RETURN_NONE;
+    if (!ints(a[0], device, -1, &src) || !ints(a[1], device, src->numel(), &dst) || !byte_caches(a[2], a[3], device, &k, &v))
+      Py_RETURN_NONE;
+    return status(kq_kv_copy_pages(ptr(src), ptr(dst), src->numel(), k->data_ptr(), v->data_ptr(), k->size(0),
+                                   k->size(1) * k->size(2), (void*)stream));
+  });
+}
+
+// (q or None, k or None, cu_new, seq_lens, inv_freq, q_out or None, k_out or None, layout, mscale, stream, device); no
+// output: in place
+PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    const at::Tensor *x[2] = {nullptr, nullptr}, *out[2], *cu, *lens, *freq, *one = nullptr;
+    int64_t layout, stream, device, stride[2] = {0, 0}, ostride[2] = {0, 0};
+    double mscale;
+    if (n != 11 || !number(a[7], &layout) || !real(a[8], &mscale) || !number(a[9], &stream) || !number(a[10], &device))
+      Py_RETURN_NONE;
+    if (!ints(a[3], device, -1, &lens) || !ints(a[2], device, lens->numel() + 1, &cu) || !tensor(a[4], device, &freq) ||
+        freq->scalar_type() != at::kFloat || !freq->is_contiguous())
+      Py_RETURN_NONE;
+    for (int i = 0; i < 2; ++i) {
+      if (a[i] == Py_None) {
+        if (a[5 + i] != Py_None) Py_RETURN_NONE;
+        continue;
+      }
+      if (!tensor(a[i], device, &x[i]) || !rows(x[i], &stride[i]) || dtype(x[i]) < 0) Py_RETURN_NONE;
+      out[i] = x[i];
+      if (a[5 + i] != Py_None && !tensor(a[5 + i], device, &out[i])) Py_RETURN_NONE;
+      if (out[i]->sizes() != x[i]->sizes() || out[i]->scalar_type() != x[i]->scalar_type() || !rows(out[i], &ostride[i]))
+        Py_RETURN_NONE;
+      if (one && (one->size(0) != x[i]->size(0) || one->size(2) != x[i]->size(2) || one->scalar_type() != x[i]->scalar_type()))
+        Py_RETURN_NONE;
+      one = x[i];
+    }
+    if (!one) Py_RETURN_NONE;
+    const auto at = [&](const at::Tensor* const* t, int i) { return x[i] ? t[i]->data_ptr() : nullptr; };
+    return status(kq_rope(at(x, 0), x[0] ? x[0]->size(1) : 0, stride[0], at(x, 1), x[1] ? x[1]->size(1) : 0, stride[1],
+                          dtype(one), one->size(0), one->size(2), 2 * freq->numel(), (int)layout, ptr(cu), ptr(lens),
+                          lens->numel(), (const float*)freq->data_ptr(), (float)mscale, at(out, 0), ostride[0], at(out, 1),
+                          ostride[1], (void*)stream));
   });
 }
 
@@ -168,6 +310,13 @@ PyMethodDef methods[] = {{"kv_store", (PyCFunction)(void*)kv_store, METH_FASTCAL
                          {"kv_load", (PyCFunction)(void*)kv_load, METH_FASTCALL, nullptr},
                          {"block_tables", (PyCFunction)(void*)block_tables, METH_FASTCALL, nullptr},
                          {"kv_attention", (PyCFunction)(void*)kv_attention, METH_FASTCALL, nullptr},
+                         {"kv_attention_sinks", (PyCFunction)(void*)kv_attention_sinks, METH_FASTCALL, nullptr},
+                         {"kv_attention_prefix", (PyCFunction)(void*)kv_attention_prefix, METH_FASTCALL, nullptr},
+                         {"kv_fork", (PyCFunction)(void*)kv_fork, METH_FASTCALL, nullptr},
+                         {"kv_free", (PyCFunction)(void*)kv_free, METH_FASTCALL, nullptr},
+                         {"kv_compact", (PyCFunction)(void*)kv_compact, METH_FASTCALL, nullptr},
+                         {"kv_copy_pages", (PyCFunction)(void*)kv_copy_pages, METH_FASTCALL, nullptr},
+                         {"rope", (PyCFunction)(void*)rope, METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_kqcall", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

@@ -425,6 +425,12 @@ struct AttnArgs {
   int few_wgs;     // workgroups a kv head that share all requests' 16-row tiles evenly (0: one to a tile)
   int many_wgs;    // prompt tiles: likewise
   int many_shift;  // log2 of a prompt tile's rows
+  int sinks;       // beside a window: so many first keys stay visible
+  // a prefix that requests share (kq_kv_attention_prefix)
+  const int32_t* prefix;  // its pages
+  int prefix_len;         // its keys
+  int splits;             // parts its steps are cut into
+  float* prefix_sums;     // [splits][kv_heads][tokens * group] rows of d floats, then (maximum, sum) pairs
 };
 // How a call's work is split, from its host-known sizes alone.
 struct AttnPlan {
@@ -436,8 +442,52 @@ struct AttnPlan {
 };
 AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
                    int64_t max_kv, int64_t window);
-hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
 int attn_prompt_rows(int64_t d);  // rows of a prompt tile
+// The prefix's part: one tile kernel over all rows of the batch, each tile's
+// steps cut into `splits`.
+struct PrefixPlan {
+  int prompt, splits;  // prompt tiles or 16-row tiles
+  int64_t tiles;       // a kv head, at most
+  int64_t bytes;       // of prefix_sums
+};
+PrefixPlan prefix_plan(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t prefix_len);
+hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
+hipError_t launch_kv_attention_sinks(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
+hipError_t launch_kv_attention_prefix(const AttnArgs& a, const AttnPlan& p, const PrefixPlan& f, hipStream_t s);
+// the tile kernels of each (kq_kv_split.h, kq_kv_prompt.h) and the join
 hipError_t launch_attn_prompt(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
+hipError_t launch_sinks_prompt(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
+hipError_t launch_tail_prompt(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
+hipError_t launch_flat_prompt(const AttnArgs& a, const PrefixPlan& f, hipStream_t s);
+hipError_t launch_attn_join(const AttnArgs& a, bool prefix, hipStream_t s);
+
+// Pages of the cache (kq_kv_pages.hip).
+constexpr int64_t COMPACT_PAGES = (int64_t)1 << 20;  // kq_kv_compact: a bit a page in LDS
+hipError_t launch_kv_fork(const int32_t* parents, const int32_t* children, const int32_t* lens, int64_t n, int page_shift,
+                          int32_t* table, int64_t n_seqs, int64_t width, int32_t* refs, int64_t pages,
+                          const int32_t* free_pages, int64_t n_free, const int32_t* free_head, int32_t* copy_src,
+                          int32_t* copy_dst, int32_t* head_out, uint32_t* status, hipStream_t s);
+hipError_t launch_kv_free(const int32_t* first, const int32_t* last, int64_t n_seqs, const int32_t* table, int64_t width,
+                          int32_t* refs, int64_t pages, int32_t* free_pages, int64_t n_free, const int32_t* free_head,
+                          int32_t* head_out, uint32_t* status, hipStream_t s);
+hipError_t launch_kv_compact(const int32_t* free_pages, int64_t n_free, const int32_t* free_head, const int32_t* table,
+                             int64_t n_entries, const int32_t* refs, int64_t pages, int32_t* table_out, int32_t* refs_out,
+                             int32_t* free_out, int32_t* remap, int32_t* copy_src, int32_t* copy_dst, int64_t n_copy,
+                             int32_t* head_out, uint32_t* status, hipStream_t s);
+hipError_t launch_kv_copy_pages(const int32_t* src, const int32_t* dst, int64_t n, uint8_t* kc, uint8_t* vc, int64_t pages,
+                                int64_t bytes, hipStream_t s);
+
+// One kq_rope call.
+struct RopeArgs {
+  const void *q, *k;
+  void *q_out, *k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  const int32_t *cu, *lens;
+  const float* inv_freq;
+  float mscale;
+  int tokens, n_seqs, hq, hkv, d, rot;
+  int copy_q, copy_k;  // written apart: the values behind `rot` are carried over
+};
+hipError_t launch_rope(const RopeArgs& a, int type, bool pairs, hipStream_t s);
 
 }  // namespace kq

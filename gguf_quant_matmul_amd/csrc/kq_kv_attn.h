@@ -43,19 +43,79 @@ __device__ __forceinline__ int token_of(const AttnArgs& a, int row) {
   return a.group_shift >= 0 ? row >> a.group_shift : (int)((uint32_t)row / (uint32_t)a.group);
 }
 
-// Keys that rows r0 .. r1 of a request see: lo (64-aligned) .. end - 1.
+constexpr int STEP = 64;  // keys of one step
+
+// What a kernel works on: a request's rows over all its keys; with a few first
+// keys that stay visible beside a window; all rows of a batch over the keys of
+// a prefix that its requests share; a request's rows over the keys behind the prefix.
+enum AttnMode { PLAIN, SINKS, FLAT, TAIL };
+
+// Position of a request's token; of every row behind all keys of a shared prefix.
+template <int M>
+__device__ __forceinline__ int pos_of(const Seq& q, int token) {
+  return M == FLAT ? q.len - 1 : q.len - q.n + token;
+}
+
+// Whether a request reads the shared prefix: all its new tokens stand behind it.
+__device__ __forceinline__ bool shares_prefix(const AttnArgs& a, const Seq& q) { return q.len - q.n >= a.prefix_len; }
+
+// Keys that rows r0 .. r1 of a request see: lo .. end - 1, and with sinks the
+// keys of `first` steps before.  lo is a multiple of 64; behind a prefix, of a
+// page's rows.
 struct Keys {
-  int lo, end;
+  int lo, end, first;
 };
+template <int M>
 __device__ __forceinline__ Keys key_range(const AttnArgs& a, const Seq& q, int r0, int r1) {
-  const int p0 = q.len - q.n + token_of(a, r0), p1 = q.len - q.n + token_of(a, r1);  // positions
+  const int p0 = pos_of<M>(q, token_of(a, r0)), p1 = pos_of<M>(q, token_of(a, r1));
   Keys k;
   k.end = p1 + 1 > 0 ? p1 + 1 : 0;
+  k.first = 0;
+  if constexpr (M == TAIL) {
+    k.lo = shares_prefix(a, q) ? a.prefix_len : 0;
+    return k;
+  }
+  if constexpr (M == FLAT) {
+    k.lo = 0;
+    return k;
+  }
   const int64_t lo = a.window > 0 ? (int64_t)p0 - a.window + 1 : 0;
   k.lo = (lo > 0 ? (int)lo : 0) & ~63;
+  if constexpr (M == SINKS) {
+    // (sinks that reach the window's first step make one run of keys of both)
+    k.first = (a.sinks + STEP - 1) / STEP;
+    if (k.lo <= k.first * STEP) k.lo = k.first = 0;
+  }
   return k;
 }
-constexpr int STEP = 64;  // keys of one step
+// First key of a step, and how many steps there are.
+template <int M>
+__device__ __forceinline__ int step_base(const Keys& k, int st) {
+  if constexpr (M == SINKS) return st * STEP + (st < k.first ? 0 : k.lo - k.first * STEP);
+  return k.lo + st * STEP;
+}
+template <int M>
+__device__ __forceinline__ int steps_of(const Keys& k) {
+  const int n = k.end > k.lo ? (k.end - k.lo + STEP - 1) / STEP : 0;
+  return M == SINKS ? n + k.first : n;
+}
+// Whether the row at position p sees key k.
+template <int M>
+__device__ __forceinline__ bool sees(const AttnArgs& a, int k, int p) {
+  if constexpr (M == SINKS) return k <= p && (k > p - a.window || k < a.sinks);
+  if constexpr (M == PLAIN) return k <= p && (a.window <= 0 || k > p - a.window);
+  return k <= p;
+}
+// Whether some row of positions p0 .. p1 does not see all of 64 keys (of the
+// request's), and whether any of them sees one.
+template <int M>
+__device__ __forceinline__ bool masked(const AttnArgs& a, int base, int p0, int p1) {
+  return base + STEP - 1 > p0 || (M <= SINKS && a.window > 0 && base <= p1 - a.window);
+}
+template <int M>
+__device__ __forceinline__ bool any_seen(const AttnArgs& a, int base, int p0, int p1) {
+  return base <= p1 && (M > SINKS || a.window <= 0 || base + STEP - 1 > p0 - a.window || (M == SINKS && base < a.sinks));
+}
 constexpr float HEADROOM = 7.f;  // log2 of the weight of a running maximum
 
 // What a tile costs beside its steps, in steps: its start and its end.  (Shares
@@ -66,22 +126,22 @@ constexpr int TILE_EXTRA = ROWS == 16 ? 6 : 5;
 
 // Cost of a tile of ROWS rows of a request; a tile without keys counts as
 // one step, so that someone writes its zeros.
-template <int ROWS>
+template <int ROWS, int M>
 __device__ __forceinline__ int tile_cost(const AttnArgs& a, const Seq& q, int sub) {
   const int rows = q.n * a.group, r0 = sub * ROWS, r1 = r0 + ROWS - 1 < rows ? r0 + ROWS - 1 : rows - 1;
-  const Keys k = key_range(a, q, r0, r1);
-  return (k.end > k.lo ? (k.end - k.lo + STEP - 1) / STEP : 1) + TILE_EXTRA<ROWS>;
+  const int n = steps_of<M>(key_range<M>(a, q, r0, r1));
+  return (n > 0 ? n : 1) + TILE_EXTRA<ROWS>;
 }
 // ... of all tiles of a request with more than `above` and at most `most` rows
 // (64-bit: 2^21 tiles of 2^24 steps are within the bounds on a call's sizes).
-template <int ROWS>
+template <int ROWS, int M>
 __device__ __forceinline__ uint64_t request_cost(const AttnArgs& a, int s, int above, int most) {
   if (s >= a.n_seqs) return 0;
   const Seq q = load_seq(a, s);
   const int rows = q.n * a.group;
   if (rows <= above || rows > most) return 0;
   uint64_t n = 0;
-  for (int sub = 0; sub * ROWS < rows; ++sub) n += (uint32_t)tile_cost<ROWS>(a, q, sub);
+  for (int sub = 0; sub * ROWS < rows; ++sub) n += (uint32_t)tile_cost<ROWS, M>(a, q, sub);
   return n;
 }
 
@@ -110,13 +170,13 @@ __device__ __forceinline__ uint64_t wave_prefix(uint64_t v) {
 struct Share {
   uint64_t x, x0, x1, size;
 };
-template <int ROWS>
+template <int ROWS, int M>
 __device__ __forceinline__ bool find_share(const AttnArgs& a, int wg, int wgs, int least, int above, int most, int& s,
                                            int& sub, Share& r) {
   const int lane = threadIdx.x & 63;
   uint64_t total = 0;
   for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
-    uint64_t n = request_cost<ROWS>(a, s0 + lane, above, most);
+    uint64_t n = request_cost<ROWS, M>(a, s0 + lane, above, most);
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) n += __shfl_xor(n, o, 64);
     total += n;
@@ -132,7 +192,7 @@ __device__ __forceinline__ bool find_share(const AttnArgs& a, int wg, int wgs, i
   uint64_t x = 0;
   s = -1;
   for (int s0 = 0; s0 < a.n_seqs; s0 += 64) {
-    const uint64_t n = request_cost<ROWS>(a, s0 + lane, above, most), incl = wave_prefix(n);
+    const uint64_t n = request_cost<ROWS, M>(a, s0 + lane, above, most), incl = wave_prefix(n);
     const uint64_t hit = __ballot(x + incl > r.x0);
     if (hit) {
       const int l = __builtin_ctzll(hit);
@@ -147,7 +207,7 @@ __device__ __forceinline__ bool find_share(const AttnArgs& a, int wg, int wgs, i
   const Seq q = load_seq(a, s);
   const int tiles = (q.n * a.group + ROWS - 1) / ROWS;
   for (int t0 = 0; t0 < tiles; t0 += 64) {
-    const uint64_t n = t0 + lane < tiles ? (uint64_t)tile_cost<ROWS>(a, q, t0 + lane) : 0, incl = wave_prefix(n);
+    const uint64_t n = t0 + lane < tiles ? (uint64_t)tile_cost<ROWS, M>(a, q, t0 + lane) : 0, incl = wave_prefix(n);
     const uint64_t hit = __ballot(x + incl > r.x0);
     if (hit) {
       const int l = __builtin_ctzll(hit);
@@ -172,6 +232,22 @@ __device__ __forceinline__ bool take_steps(Share& r, int steps, int& st0, int& s
   first = (int)(x / r.size);
   pieces = (int)((end - 1) / r.size) - first + 1;
   return true;
+}
+
+// The workgroup's tile of all rows of the batch as those of one request, and
+// its steps: cut `wg` of a.splits to a tile.
+__device__ __forceinline__ Seq flat_seq(const AttnArgs& a) {
+  int b = ((ConstInts)a.cu)[0], e = ((ConstInts)a.cu)[a.n_seqs];
+  b = b < 0 ? 0 : b > a.tokens ? a.tokens : b;
+  e = e < b ? b : e > a.tokens ? a.tokens : e;
+  return Seq{b, e - b, a.prefix_len};
+}
+// Place of a row's sums over the prefix: `row` counts the token buffer's rows of a kv head.
+__device__ __forceinline__ int64_t prefix_row(const AttnArgs& a, int split, int h, int64_t row) {
+  return ((int64_t)split * a.hkv + h) * ((int64_t)a.tokens * a.group) + row;
+}
+__device__ __forceinline__ float* prefix_ml(const AttnArgs& a) {
+  return a.prefix_sums + prefix_row(a, a.splits, 0, 0) * a.d;  // (maximum, sum) pairs behind the sums
 }
 
 // Request and tile index inside it of tile `tile`, the tiles of the requests
@@ -408,6 +484,25 @@ __device__ __forceinline__ float move_maximum(float mx, float factor, float4_t (
 // the very bias of its weights, negative.
 __device__ __forceinline__ float sums_at(float m, float factor) {
   return m == NEG_INF ? NEG_INF : fmaf(m, factor, -HEADROOM);
+}
+
+// A row's sums over the shared prefix, a.splits pieces of them, beside its own:
+// the maximum of both, then the pieces weighted at `ref`.
+constexpr int PREFIX_TOO = 1 << 30;  // in `where`: the join adds them
+__device__ __forceinline__ float prefix_max(const AttnArgs& a, int h, int64_t row, float m) {
+  const float* ml = prefix_ml(a);
+  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, ml[2 * prefix_row(a, i, h, row)]);
+  return m;
+}
+__device__ __forceinline__ void add_prefix(const AttnArgs& a, int h, int64_t row, int c, float ref, float& l, float4_t& v) {
+  const float* ml = prefix_ml(a);
+#pragma unroll 4
+  for (int i = 0; i < a.splits; ++i) {
+    const int64_t r = prefix_row(a, i, h, row);
+    const float w = __builtin_amdgcn_exp2f(ml[2 * r] - ref);
+    l += w * ml[2 * r + 1];
+    v += w * *(const float4_t*)(a.prefix_sums + r * a.d + c);
+  }
 }
 
 template <int OUT>

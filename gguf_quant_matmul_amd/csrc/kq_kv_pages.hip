@@ -1,0 +1,402 @@
+// Pages of the 4-bit cache shared and moved: kq_kv_fork, kq_kv_free,
+// kq_kv_compact, kq_kv_copy_pages.
+//
+// refs[p] counts the holders of page p beyond its first.  Counts change by
+// integer atomics, whose sums no order changes; what goes by order (which
+// fresh page a fork takes, where a freed page goes) goes by prefix sums.
+#include "kq_internal.h"
+
+namespace kq {
+namespace {
+
+// inclusive prefix sum over a wave's lanes
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xF, 0xF, false);  // row_shr:1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xF, 0xF, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xA, 0xF, false);  // row_bcast:15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xC, 0xF, false);  // row_bcast:31 into rows 2 and 3
+  return v;
+}
+
+// ---- fork -------------------------------------------------------------------
+//
+// Fork i takes a fresh page if its length ends inside one: the one behind
+// those of the forks before it.  Every workgroup sums over all forks itself
+// (a thread a strip, then one scan over the strips), so that one launch does;
+// then a wave copies a fork's row of page ids and counts their new holder.
+constexpr int FORK_THREADS = 256, FORK_WAVES = FORK_THREADS / 64;
+constexpr int FORK_MOST = 64;  // forks of a workgroup
+
+struct Fork {
+  int parent, child, whole, part, fit;
+  uint32_t before;  // fresh pages that earlier forks ask for
+};
+
+__global__ __launch_bounds__(FORK_THREADS) void kv_fork_kernel(
+    const int32_t* __restrict__ parents, const int32_t* __restrict__ children, const int32_t* __restrict__ lens, int n,
+    int page_shift, int32_t* table, int n_seqs, int64_t width, int32_t* __restrict__ refs, int64_t pages,
+    const int32_t* __restrict__ free_pages, int64_t n_free, const int32_t* __restrict__ free_head,
+    int32_t* __restrict__ copy_src, int32_t* __restrict__ copy_dst, int32_t* __restrict__ head_out,
+    uint32_t* __restrict__ status, int each) {
+  __shared__ uint32_t wave_need[FORK_WAVES], wave_flags[FORK_WAVES], wave_taken[FORK_WAVES];
+  __shared__ Fork fork[FORK_MOST];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int first = blockIdx.x * each;
+  const int strip = (n + FORK_THREADS - 1) / FORK_THREADS;
+  const int i0 = tid * strip, i1 = i0 + strip < n ? i0 + strip : n;
+  const auto ask = [&](int i, Fork& f, uint32_t& bad) -> uint32_t {
+    f.parent = parents[i];
+    f.child = children[i];
+    const int len = lens[i];
+    f.whole = len >> page_shift;
+    f.part = (len & ((1 << page_shift) - 1)) != 0;
+    bad = len < 0 ? 8u
+          : (uint32_t)f.parent >= (uint32_t)n_seqs || (uint32_t)f.child >= (uint32_t)n_seqs || f.parent == f.child ? 4u
+          : (int64_t)f.whole + f.part > width ? 2u : 0u;
+    return bad ? 0u : (uint32_t)f.part;
+  };
+  const int64_t head = free_head[0];
+  uint32_t need = 0;
+  for (int i = i0; i < i1; ++i) {
+    Fork f;
+    uint32_t bad;
+    need += ask(i, f, bad);
+  }
+  const uint32_t incl = wave_scan(need);
+  if (lane == 63) wave_need[wave] = incl;
+  __syncthreads();
+  uint32_t cum = incl - need;
+#pragma unroll
+  for (int w = 0; w < FORK_WAVES; ++w) cum += w < wave ? wave_need[w] : 0u;
+
+  const uint32_t avail = head >= 0 && head <= n_free ? (uint32_t)(n_free - head) : 0u;
+  uint32_t flags = 0, taken = 0;
+  for (int i = i0; i < i1; ++i) {
+    Fork f;
+    uint32_t bad;
+    const uint32_t m = ask(i, f, bad);
+    f.before = cum;
+    cum += m;
+    f.fit = !bad && (m == 0 || cum <= avail);
+    if (!bad && !f.fit) bad = 1u;
+    flags |= bad;
+    if (f.fit && m > 0) taken = cum;  // sums only grow: the last one that fits
+    if (i >= first && i < first + each) fork[i - first] = f;
+  }
+  if (blockIdx.x == 0 && blockIdx.y == 0) {
+    const uint64_t took = __ballot(taken > 0);
+    const uint32_t most = took ? __builtin_amdgcn_readlane(taken, 63 - __builtin_clzll(took)) : 0u;
+    uint32_t all = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) all |= __ballot(flags >> i & 1u) ? 1u << i : 0u;
+    if (lane == 0) {
+      wave_flags[wave] = all;
+      wave_taken[wave] = most;
+    }
+  }
+  __syncthreads();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0) {
+    flags = taken = 0;
+    for (int w = 0; w < FORK_WAVES; ++w) {
+      flags |= wave_flags[w];
+      taken = wave_taken[w] > taken ? wave_taken[w] : taken;
+    }
+    head_out[0] = (int32_t)(head + taken);
+    if (status) *status = flags;
+  }
+  for (int i = wave; i < each && first + i < n; i += FORK_WAVES) {
+    const Fork f = fork[i];
+    const int32_t* from = table + (int64_t)f.parent * width;
+    int32_t* to = table + (int64_t)f.child * width;
+    if (blockIdx.y == 0 && lane == 0) {
+      int32_t src = -1, dst = -1;
+      if (f.fit && f.part) {
+        src = from[f.whole];
+        dst = free_pages[head + f.before];
+        to[f.whole] = dst;
+      }
+      copy_src[first + i] = src;
+      copy_dst[first + i] = dst;
+    }
+    if (!f.fit) continue;
+    for (int64_t j = (int64_t)blockIdx.y * 64 + lane; j < f.whole; j += (int64_t)gridDim.y * 64) {
+      const int32_t id = from[j];
+      to[j] = id;
+      if (id >= 0 && id < pages) atomicAdd(refs + id, 1);
+    }
+  }
+}
+
+// ---- free -------------------------------------------------------------------
+//
+// One launch takes every given entry off its page's count; the second collects
+// the pages whose count fell below 0, in the order of their ids, by one
+// workgroup: the count of the list's new head wants all of them first.
+constexpr int COLLECT_THREADS = 1024, COLLECT_WAVES = COLLECT_THREADS / 64;
+
+__global__ __launch_bounds__(256) void kv_release_kernel(const int32_t* __restrict__ first, const int32_t* __restrict__ last,
+                                                         int n_seqs, const int32_t* __restrict__ table, int64_t width,
+                                                         int32_t* __restrict__ refs, int64_t pages) {
+  const int lane = threadIdx.x & 63, s = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  if (s >= n_seqs) return;
+  int64_t j0 = first[s], j1 = last[s];
+  j0 = j0 < 0 ? 0 : j0;
+  j1 = j1 > width ? width : j1;
+  const int32_t* row = table + (int64_t)s * width;
+  for (int64_t j = j0 + (int64_t)blockIdx.y * 64 + lane; j < j1; j += (int64_t)gridDim.y * 64) {
+    const int32_t id = row[j];
+    if (id >= 0 && id < pages) atomicSub(refs + id, 1);
+  }
+}
+
+__global__ __launch_bounds__(COLLECT_THREADS) void kv_collect_kernel(int32_t* __restrict__ refs, int64_t pages,
+                                                                     int32_t* __restrict__ free_pages, int64_t n_free,
+                                                                     const int32_t* __restrict__ free_head,
+                                                                     int32_t* __restrict__ head_out,
+                                                                     uint32_t* __restrict__ status) {
+  constexpr int AHEAD = 8;
+  __shared__ uint32_t counts[COLLECT_WAVES], overs[COLLECT_WAVES];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  // a wave takes a run of pages, 64 * AHEAD at a time
+  const int64_t run = (pages + COLLECT_WAVES * 64 * AHEAD - 1) / (COLLECT_WAVES * 64 * AHEAD) * (64 * AHEAD);
+  const int64_t p0 = wave * run, p1 = p0 + run < pages ? p0 + run : pages;
+  const int64_t head = free_head[0];
+  uint32_t mine = 0, over = 0;
+  for (int64_t p = p0; p < p1; p += 64 * AHEAD) {
+    int32_t v[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) v[i] = p + i * 64 + lane < p1 ? refs[p + i * 64 + lane] : 0;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      mine += v[i] < 0 ? 1u : 0u;
+      over |= v[i] < -1 ? 1u : 0u;
+    }
+  }
+  mine = __builtin_amdgcn_readlane(wave_scan(mine), 63);
+  over = __ballot(over) ? 1u : 0u;
+  if (lane == 0) {
+    counts[wave] = mine;
+    overs[wave] = over;
+  }
+  __syncthreads();
+  uint32_t before = 0, total = 0, any = 0;
+#pragma unroll
+  for (int w = 0; w < COLLECT_WAVES; ++w) {
+    before += w < wave ? counts[w] : 0u;
+    total += counts[w];
+    any |= overs[w];
+  }
+  if (threadIdx.x == 0) {
+    const int64_t left = head - total;
+    head_out[0] = (int32_t)(left < 0 ? 0 : left);
+    if (status) *status = any | (left < 0 ? 2u : 0u);
+  }
+  if (mine == 0) return;
+  int64_t at = head - total + before;  // place of the wave's next page
+  for (int64_t p = p0; p < p1; p += 64 * AHEAD) {
+    int32_t v[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) v[i] = p + i * 64 + lane < p1 ? refs[p + i * 64 + lane] : 0;
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const uint64_t dead = __ballot(v[i] < 0);
+      if (v[i] < 0) {
+        const int64_t page = p + i * 64 + lane, place = at + __popcll(dead & ((1ull << lane) - 1));
+        refs[page] = 0;
+        if (place >= 0 && place < n_free) free_pages[place] = (int32_t)page;
+      }
+      at += __popcll(dead);
+    }
+  }
+}
+
+// ---- compact ----------------------------------------------------------------
+//
+// A bit a page in LDS says which are free.  With c held pages in all, the free
+// pages below c (the first free ones) are the holes, the held ones from c on
+// the movers; as many of each.  A page's place among either is its rank among
+// the free pages, a prefix sum over the bits.  The second launch renumbers
+// tables and counts.
+constexpr int COMPACT_THREADS = 1024, COMPACT_WAVES = COMPACT_THREADS / 64;
+constexpr int GROUP = 8;  // words of bits to one entry of the prefix sums
+
+__global__ __launch_bounds__(COMPACT_THREADS) void kv_compact_kernel(
+    const int32_t* free_pages, int64_t n_free, const int32_t* free_head, int pages, int32_t* __restrict__ remap,
+    int32_t* copy_src, int32_t* copy_dst, int64_t n_copy, int32_t* head_out, uint32_t* __restrict__ status) {
+  extern __shared__ uint32_t bits[];
+  __shared__ uint32_t wave_sums[COMPACT_WAVES];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int groups = (pages + 32 * GROUP - 1) / (32 * GROUP), words = groups * GROUP;
+  uint32_t* before = bits + words;  // free pages before a group
+  for (int i = tid; i < words; i += COMPACT_THREADS) bits[i] = 0;
+  const int64_t head = free_head[0];
+  __syncthreads();
+  for (int64_t i = head >= 0 && head <= n_free ? head + tid : n_free; i < n_free; i += COMPACT_THREADS) {
+    const int32_t id = free_pages[i];
+    if (id >= 0 && id < pages) atomicOr(bits + (id >> 5), 1u << (id & 31));
+  }
+  __syncthreads();
+  const int each = (groups + COMPACT_THREADS - 1) / COMPACT_THREADS;
+  const int g0 = tid * each, g1 = g0 + each < groups ? g0 + each : groups;
+  uint32_t mine = 0;
+  for (int g = g0; g < g1; ++g)
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) mine += __popc(bits[g * GROUP + i]);
+  const uint32_t incl = wave_scan(mine);
+  if (lane == 63) wave_sums[wave] = incl;
+  __syncthreads();
+  uint32_t sum = incl - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < COMPACT_WAVES; ++w) {
+    sum += w < wave ? wave_sums[w] : 0u;
+    total += wave_sums[w];
+  }
+  for (int g = g0; g < g1; ++g) {
+    before[g] = sum;
+#pragma unroll
+    for (int i = 0; i < GROUP; ++i) sum += __popc(bits[g * GROUP + i]);
+  }
+  __syncthreads();
+  const int held = pages - (int)total;
+  const auto rank = [&](int id) {  // free pages before page id
+    const int w = id >> 5;
+    uint32_t r = before[w / GROUP] + __popc(bits[w] & ((1u << (id & 31)) - 1));
+    for (int i = w / GROUP * GROUP; i < w; ++i) r += __popc(bits[i]);
+    return (int)r;
+  };
+  const int moves = total ? rank(held) : 0;
+  for (int id = tid; id < pages; id += COMPACT_THREADS) {
+    const bool is_free = bits[id >> 5] >> (id & 31) & 1u;
+    if (is_free || id < held) remap[id] = is_free ? -1 : id;
+    if (is_free != (id < held)) continue;
+    // a hole, or a mover behind held - moves pages that stay
+    const int r = rank(id), at = is_free ? r : id - r - (held - moves);
+    if (at < n_copy) (is_free ? copy_dst : copy_src)[at] = id;
+  }
+  __threadfence_block();
+  __syncthreads();
+  for (int64_t i = tid; i < n_copy; i += COMPACT_THREADS) {
+    if (i < moves) remap[copy_src[i]] = copy_dst[i];
+    else copy_src[i] = copy_dst[i] = -1;
+  }
+  if (tid == 0) {
+    if (status) *status = head != n_free - total ? 1u : 0u;
+    head_out[0] = (int32_t)(n_free - total);
+  }
+}
+
+// Table entries, counts and the free list by the new ids, an element a thread.
+__global__ __launch_bounds__(256) void kv_renumber_kernel(const int32_t* table, int32_t* table_out, int64_t n_entries,
+                                                          const int32_t* refs, int32_t* refs_out, int pages,
+                                                          const int32_t* free_pages, int32_t* free_out, int64_t n_free,
+                                                          const int32_t* __restrict__ remap,
+                                                          const int32_t* __restrict__ free_head) {
+  const int64_t step = (int64_t)gridDim.x * 256, t0 = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t head = free_head[0], held = pages - (n_free - head);
+  for (int64_t i = t0; i < n_entries; i += step) {
+    const int32_t id = table[i];
+    table_out[i] = id >= 0 && id < pages ? remap[id] : -1;
+  }
+  for (int64_t p = t0; p < pages; p += step) {
+    // (a hole's count is written with that of the page that moves into it)
+    const int32_t to = remap[p], count = refs[p];
+    if (to >= 0) refs_out[to] = count;
+    if (p >= held) refs_out[p] = 0;
+  }
+  for (int64_t i = t0; i < n_free; i += step) free_out[i] = i < head ? free_pages[i] : (int32_t)(held + i - head);
+}
+
+// ---- copy -------------------------------------------------------------------
+//
+// A workgroup copies pieces of 16 KB of one cache, all of a thread's loads
+// before its stores.
+constexpr int COPY_THREADS = 256, COPY_AHEAD = 4;
+constexpr int COPY_PIECE = COPY_THREADS * COPY_AHEAD * 16;
+
+__global__ __launch_bounds__(COPY_THREADS) void kv_copy_pages_kernel(const int32_t* __restrict__ src,
+                                                                     const int32_t* __restrict__ dst, int64_t n,
+                                                                     uint8_t* kc, uint8_t* vc, int64_t pages,
+                                                                     int64_t bytes, int pieces) {
+  const int64_t work = n * 2 * pieces;
+  for (int64_t w = blockIdx.x; w < work; w += gridDim.x) {
+    const int64_t pair = w / (2 * pieces);
+    const int rest = (int)(w - pair * (2 * pieces)), piece = rest >> 1;
+    const int64_t from = src[pair], to = dst[pair];
+    if (from < 0 || from >= pages || to < 0 || to >= pages || from == to) continue;
+    uint8_t* cache = rest & 1 ? vc : kc;
+    const uint8_t* s = cache + from * bytes;
+    uint8_t* d = cache + to * bytes;
+    const int64_t at = (int64_t)piece * COPY_PIECE + threadIdx.x * 16;
+    u32x4 v[COPY_AHEAD];
+#pragma unroll
+    for (int i = 0; i < COPY_AHEAD; ++i)
+      if (at + i * COPY_THREADS * 16 < bytes) v[i] = *(const u32x4*)(s + at + i * COPY_THREADS * 16);
+#pragma unroll
+    for (int i = 0; i < COPY_AHEAD; ++i)
+      if (at + i * COPY_THREADS * 16 < bytes) *(u32x4*)(d + at + i * COPY_THREADS * 16) = v[i];
+  }
+}
+
+}  // namespace
+
+hipError_t launch_kv_fork(const int32_t* parents, const int32_t* children, const int32_t* lens, int64_t n, int page_shift,
+                          int32_t* table, int64_t n_seqs, int64_t width, int32_t* refs, int64_t pages,
+                          const int32_t* free_pages, int64_t n_free, const int32_t* free_head, int32_t* copy_src,
+                          int32_t* copy_dst, int32_t* head_out, uint32_t* status, hipStream_t s) {
+  // four forks to a workgroup (one a wave); above 4096 more of them, so that
+  // the repeated sums stay small beside the rows
+  int64_t each = (n + 1023) / 1024;
+  each = each < 4 ? 4 : each > FORK_MOST ? FORK_MOST : each;
+  const int64_t gx = n > 0 ? (n + each - 1) / each : 1;
+  int64_t gy = (width + 1023) / 1024;
+  gy = gy < 1 ? 1 : gy > 64 ? 64 : gy;
+  hipLaunchKernelGGL(kv_fork_kernel, dim3((unsigned)gx, (unsigned)gy), dim3(FORK_THREADS), 0, s, parents, children, lens,
+                     (int)n, page_shift, table, (int)n_seqs, width, refs, pages, free_pages, n_free, free_head, copy_src,
+                     copy_dst, head_out, status, (int)each);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_free(const int32_t* first, const int32_t* last, int64_t n_seqs, const int32_t* table, int64_t width,
+                          int32_t* refs, int64_t pages, int32_t* free_pages, int64_t n_free, const int32_t* free_head,
+                          int32_t* head_out, uint32_t* status, hipStream_t s) {
+  if (n_seqs > 0 && width > 0) {
+    int64_t gy = (width + 511) / 512;
+    gy = gy > 64 ? 64 : gy;
+    hipLaunchKernelGGL(kv_release_kernel, dim3((unsigned)((n_seqs + 3) / 4), (unsigned)gy), dim3(256), 0, s, first, last,
+                       (int)n_seqs, table, width, refs, pages);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(kv_collect_kernel, dim3(1), dim3(COLLECT_THREADS), 0, s, refs, pages, free_pages, n_free, free_head,
+                     head_out, status);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_compact(const int32_t* free_pages, int64_t n_free, const int32_t* free_head, const int32_t* table,
+                             int64_t n_entries, const int32_t* refs, int64_t pages, int32_t* table_out, int32_t* refs_out,
+                             int32_t* free_out, int32_t* remap, int32_t* copy_src, int32_t* copy_dst, int64_t n_copy,
+                             int32_t* head_out, uint32_t* status, hipStream_t s) {
+  const int64_t groups = (pages + 32 * GROUP - 1) / (32 * GROUP);
+  hipLaunchKernelGGL(kv_compact_kernel, dim3(1), dim3(COMPACT_THREADS), (size_t)(groups * (GROUP + 1) * 4), s, free_pages,
+                     n_free, free_head, (int)pages, remap, copy_src, copy_dst, n_copy, head_out, status);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  int64_t most = n_entries > pages ? n_entries : pages;
+  most = n_free > most ? n_free : most;
+  const int64_t wgs = (most + 255) / 256;
+  hipLaunchKernelGGL(kv_renumber_kernel, dim3((unsigned)(wgs < 2048 ? wgs : 2048)), dim3(256), 0, s, table, table_out,
+                     n_entries, refs, refs_out, (int)pages, free_pages, free_out, n_free, remap, head_out);
+  return hipGetLastError();
+}
+
+hipError_t launch_kv_copy_pages(const int32_t* src, const int32_t* dst, int64_t n, uint8_t* kc, uint8_t* vc, int64_t pages,
+                                int64_t bytes, hipStream_t s) {
+  const int64_t pieces = (bytes + COPY_PIECE - 1) / COPY_PIECE, work = n * 2 * pieces;
+  hipLaunchKernelGGL(kv_copy_pages_kernel, dim3((unsigned)(work < 65536 ? work : 65536)), dim3(COPY_THREADS), 0, s, src, dst,
+                     n, kc, vc, pages, bytes, (int)pieces);
+  return hipGetLastError();
+}
+
+}  // namespace kq

@@ -88,6 +88,23 @@ _SIGS = {
     "kq_kv_attention": (c_int, [c_int, c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64,
                                 c_vp, c_vp, c_i64, c_i64, ctypes.c_float, c_i64, c_i64, c_i64, c_vp, c_int, c_vp, c_i64,
                                 c_vp]),
+    "kq_kv_attention_sinks": (c_int, [c_int, c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp,
+                                      c_i64, c_vp, c_vp, c_i64, c_i64, ctypes.c_float, c_i64, c_i64, c_i64, c_i64, c_vp,
+                                      c_int, c_vp, c_i64, c_vp]),
+    "kq_kv_attention_prefix_workspace": (c_int, [c_i64, c_i64, c_i64, c_i64, c_i64, c_i64, c_i64, c_i64, _P(c_i64)]),
+    "kq_kv_attention_prefix": (c_int, [c_int, c_vp, c_int, c_i64, c_i64, c_i64, c_i64, c_i64, c_vp, c_vp, c_i64, c_vp,
+                                       c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, ctypes.c_float, c_i64, c_i64, c_vp,
+                                       c_int, c_vp, c_i64, c_vp]),
+    "kq_kv_fork": (c_int, [c_vp, c_vp, c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp,
+                           c_vp, c_vp, c_vp]),
+    "kq_kv_free": (c_int, [c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp]),
+    "kq_kv_compact": (c_int, [c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_i64, c_vp,
+                              c_vp, c_vp]),
+    "kq_kv_copy_pages": (c_int, [c_vp, c_vp, c_i64, c_vp, c_vp, c_i64, c_i64, c_vp]),
+    "kq_rope": (c_int, [c_vp, c_i64, c_i64, c_vp, c_i64, c_i64, c_int, c_i64, c_i64, c_i64, c_int, c_vp, c_vp, c_i64, c_vp,
+                        ctypes.c_float, c_vp, c_i64, c_vp, c_i64, c_vp]),
+    "kq_rope_freqs": (c_int, [c_i64, ctypes.c_double, c_int, ctypes.c_double, c_i64, ctypes.c_double, ctypes.c_double, c_vp,
+                              _P(ctypes.c_float), _P(ctypes.c_float)]),
 }
 
 #: every symbol the header declares
@@ -105,6 +122,10 @@ KQ_F32, KQ_F16, KQ_BF16 = 0, 1, 2
 KQ_GLU_SILU, KQ_GLU_GELU_TANH, KQ_GLU_SILU_LIMIT = 0, 1, 2
 _GLU_ACTS = {"silu": KQ_GLU_SILU, "gelu": KQ_GLU_GELU_TANH, "gelu_tanh": KQ_GLU_GELU_TANH,
              "silu_limit": KQ_GLU_SILU_LIMIT}
+KQ_ROPE_HALF, KQ_ROPE_PAIRS = 0, 1
+KQ_ROPE_NONE, KQ_ROPE_LINEAR, KQ_ROPE_NTK, KQ_ROPE_YARN = 0, 1, 2, 3
+_ROPE_LAYOUTS = {"half": KQ_ROPE_HALF, "pairs": KQ_ROPE_PAIRS}
+_ROPE_SCALINGS = {"none": KQ_ROPE_NONE, "linear": KQ_ROPE_LINEAR, "ntk": KQ_ROPE_NTK, "yarn": KQ_ROPE_YARN}
 KQ_OK, KQ_ERR_ARG, KQ_ERR_CODEC, KQ_ERR_SHAPE, KQ_ERR_ALIGN, KQ_ERR_CAPACITY, KQ_ERR_HIP = 0, -1, -2, -3, -4, -5, -6
 STATUS_NAMES = {0: "KQ_OK", -1: "KQ_ERR_ARG", -2: "KQ_ERR_CODEC", -3: "KQ_ERR_SHAPE", -4: "KQ_ERR_ALIGN",
                 -5: "KQ_ERR_CAPACITY", -6: "KQ_ERR_HIP"}
@@ -474,7 +495,58 @@ def kq_kv_attention(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page: i
                                   torch._C._cuda_getCurrentRawStream(dev), dev)
         if st is not None:
             return _check(st)
-    op, n, shape, dev = "kq_kv_attention", seq_lens.numel(), q.shape, q.get_device()
+    _attention("kq_kv_attention", _lib.kq_kv_attention, codec, q, cu_new, seq_lens, table, None, k_cache, v_cache, page, out,
+               scale, (window,), max_new, max_kv, workspace, stream)
+
+
+def kq_kv_attention_sinks(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page: int, out, window: int, sinks: int,
+                          scale: float | None = None, max_new: int | None = None, max_kv: int | None = None, workspace=None,
+                          stream=None) -> None:
+    """kq_kv_attention where each token sees the last `window` keys and its request's first `sinks` ones.  Workspace of
+    kq_kv_attention_workspace."""
+    if _kqcall is not None and stream is None and q.is_cuda and (codec == "q4_0" or codec == KQ_Q4_0) \
+            and max_new is not None and max_kv is not None:
+        dev = torch._C._cuda_getDevice()
+        st = _kqcall.kv_attention_sinks(q, cu_new, seq_lens, table, k_cache, v_cache, page, out,
+                                        q.size(-1) ** -0.5 if scale is None else scale, window, sinks, max_new, max_kv,
+                                        workspace, torch._C._cuda_getCurrentRawStream(dev), dev)
+        if st is not None:
+            return _check(st)
+    _attention("kq_kv_attention_sinks", _lib.kq_kv_attention_sinks, codec, q, cu_new, seq_lens, table, None, k_cache, v_cache,
+               page, out, scale, (window, sinks), max_new, max_kv, workspace, stream)
+
+
+def kq_kv_attention_prefix_workspace(tokens: int, n_seqs: int, q_heads: int, kv_heads: int, d: int, prefix_len: int,
+                                     max_new: int, max_kv: int) -> int:
+    """Bytes of workspace that kq_kv_attention_prefix needs for these sizes; prefix_len in keys."""
+    out = c_i64()
+    _check(_lib.kq_kv_attention_prefix_workspace(tokens, n_seqs, q_heads, kv_heads, d, prefix_len, max_new, max_kv,
+                                                 ctypes.byref(out)))
+    return out.value
+
+
+def kq_kv_attention_prefix(codec, q, cu_new, seq_lens, table, prefix, k_cache, v_cache, page: int, out,
+                           scale: float | None = None, max_new: int | None = None, max_kv: int | None = None, workspace=None,
+                           stream=None) -> None:
+    """kq_kv_attention for requests whose first keys are the pages prefix int32 [n_prefix], read once for all of them.
+    seq_lens and table count the prefix in; a request whose new tokens do not all stand behind it reads its own row of the
+    table alone.  workspace: uint8 of kq_kv_attention_prefix_workspace bytes; allocated if left out."""
+    if _kqcall is not None and stream is None and q.is_cuda and (codec == "q4_0" or codec == KQ_Q4_0) \
+            and max_new is not None and max_kv is not None:
+        dev = torch._C._cuda_getDevice()
+        st = _kqcall.kv_attention_prefix(q, cu_new, seq_lens, table, prefix, k_cache, v_cache, page, out,
+                                         q.size(-1) ** -0.5 if scale is None else scale, max_new, max_kv, workspace,
+                                         torch._C._cuda_getCurrentRawStream(dev), dev)
+        if st is not None:
+            return _check(st)
+    _attention("kq_kv_attention_prefix", _lib.kq_kv_attention_prefix, codec, q, cu_new, seq_lens, table, prefix, k_cache,
+               v_cache, page, out, scale, (), max_new, max_kv, workspace, stream)
+
+
+def _attention(op, fn, codec, q, cu_new, seq_lens, table, prefix, k_cache, v_cache, page, out, scale, windows, max_new,
+               max_kv, workspace, stream) -> None:
+    """An attention call through ctypes, its tensors checked."""
+    n, shape, dev = seq_lens.numel(), q.shape, q.get_device()
     qdt, odt = _DTYPES.get(q.dtype), _DTYPES.get(out.dtype)
     if len(shape) != 3 or qdt is None or odt is None:
         raise ValueError(f"{op}: q must be float16 or bfloat16 [tokens, q_heads, d], out a float tensor of its shape")
@@ -491,7 +563,10 @@ def kq_kv_attention(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page: i
     if max_kv is None:
         max_kv = max(width * page, 1)
     if workspace is None:
-        need = kq_kv_attention_workspace(tokens, n, heads, kv_heads, d, max_new, max_kv)
+        if prefix is None:
+            need = kq_kv_attention_workspace(tokens, n, heads, kv_heads, d, max_new, max_kv)
+        else:
+            need = kq_kv_attention_prefix_workspace(tokens, n, heads, kv_heads, d, prefix.numel() * page, max_new, max_kv)
         ws = None
         if need:
             _on_gpu(op, dev)
@@ -503,11 +578,150 @@ def kq_kv_attention(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page: i
         if not workspace.is_contiguous() or workspace.get_device() != dev:
             raise ValueError(f"{op}: workspace must be contiguous, on q's device")
         need, ws = workspace.numel() * workspace.element_size(), workspace.data_ptr()
-    _call_on(dev, stream, _lib.kq_kv_attention, cid, q.data_ptr(), qdt, tokens, heads, kv_heads, d,
+    more = () if prefix is None else (_index(op, "prefix", prefix, None, dev), prefix.numel())
+    _call_on(dev, stream, fn, cid, q.data_ptr(), qdt, tokens, heads, kv_heads, d,
              _row_stride(op, "q", q, shape), _index(op, "cu_new", cu_new, n + 1, dev),
              _index(op, "seq_lens", seq_lens, n, dev), n, _index(op, "table", table, None, dev), width,
-             k_cache.data_ptr(), v_cache.data_ptr(), pages, page, d ** -0.5 if scale is None else scale, window,
+             *more, k_cache.data_ptr(), v_cache.data_ptr(), pages, page, d ** -0.5 if scale is None else scale, *windows,
              max_new, max_kv, out.data_ptr(), odt, ws, need)
+
+
+# ---------------------------------------------------------------------------
+# pages of the cache shared, given back and moved; rotary positions
+# ---------------------------------------------------------------------------
+
+def kq_kv_fork(parents, children, lens, page: int, table, refs, free_pages, free_head, copy_src, copy_dst, free_head_out,
+               status=None, stream=None) -> None:
+    """Rows children int32 [n] of table int32 [n_seqs, width] start with the first lens int32 [n] tokens of rows parents
+    int32 [n].  refs int32 [pages]; copy_src, copy_dst int32 [n] are for kq_kv_copy_pages; free list as in kq_block_tables."""
+    if _kqcall is not None and stream is None and parents.is_cuda:
+        dev = torch._C._cuda_getDevice()
+        st = _kqcall.kv_fork(parents, children, lens, page, table, refs, free_pages, free_head, copy_src, copy_dst,
+                             free_head_out, status, torch._C._cuda_getCurrentRawStream(dev), dev)
+        if st is not None:
+            return _check(st)
+    op, n, dev = "kq_kv_fork", parents.numel(), parents.get_device()
+    if table.dim() != 2:
+        raise ValueError(f"{op}: table must be [n_seqs, width]")
+    _call_on(dev, stream, _lib.kq_kv_fork, _index(op, "parents", parents, n, dev), _index(op, "children", children, n, dev),
+             _index(op, "lens", lens, n, dev), n, page, _index(op, "table", table, None, dev), table.shape[0], table.shape[1],
+             _index(op, "refs", refs, None, dev), refs.numel(), _index(op, "free_pages", free_pages, None, dev),
+             free_pages.numel(), _index(op, "free_head", free_head, 1, dev), _index(op, "copy_src", copy_src, n, dev),
+             _index(op, "copy_dst", copy_dst, n, dev), _index(op, "free_head_out", free_head_out, 1, dev),
+             None if status is None else _index(op, "status", status, 1, dev))
+
+
+def kq_kv_free(first, last, table, refs, free_pages, free_head, free_head_out, status=None, stream=None) -> None:
+    """The entries first[s] <= j < last[s] (int32 [n_seqs]) of table int32 [n_seqs, width] are given back: refs int32
+    [pages] counts them off, pages without a holder go back to the free list."""
+    if _kqcall is not None and stream is None and first.is_cuda:
+        dev = torch._C._cuda_getDevice()
+        st = _kqcall.kv_free(first, last, table, refs, free_pages, free_head, free_head_out, status,
+                             torch._C._cuda_getCurrentRawStream(dev), dev)
+        if st is not None:
+            return _check(st)
+    op, n, dev = "kq_kv_free", first.numel(), first.get_device()
+    if table.dim() != 2 or table.shape[0] != n:
+        raise ValueError(f"{op}: table must be [{n}, width]")
+    _call_on(dev, stream, _lib.kq_kv_free, _index(op, "first", first, n, dev), _index(op, "last", last, n, dev), n,
+             _index(op, "table", table, None, dev), table.shape[1], _index(op, "refs", refs, None, dev), refs.numel(),
+             _index(op, "free_pages", free_pages, None, dev), free_pages.numel(), _index(op, "free_head", free_head, 1, dev),
+             _index(op, "free_head_out", free_head_out, 1, dev),
+             None if status is None else _index(op, "status", status, 1, dev))
+
+
+def kq_kv_compact(free_pages, free_head, table, refs, table_out, refs_out, free_out, remap, copy_src, copy_dst, free_head_out,
+                  status=None, stream=None) -> None:
+    """The held pages move to the front of the cache: copy_src, copy_dst int32 [n_copy] are for kq_kv_copy_pages, remap
+    int32 [pages] has the new ids; table, refs and free list by them in the outputs, which may be the inputs."""
+    if _kqcall is not None and stream is None and free_pages.is_cuda:
+        dev = torch._C._cuda_getDevice()
+        st = _kqcall.kv_compact(free_pages, free_head, table, refs, table_out, refs_out, free_out, remap, copy_src, copy_dst,
+                                free_head_out, status, torch._C._cuda_getCurrentRawStream(dev), dev)
+        if st is not None:
+            return _check(st)
+    op, dev, n_free, entries, pages, n = ("kq_kv_compact", free_pages.get_device(), free_pages.numel(), table.numel(),
+                                          refs.numel(), copy_src.numel())
+    _call_on(dev, stream, _lib.kq_kv_compact, _index(op, "free_pages", free_pages, None, dev), n_free,
+             _index(op, "free_head", free_head, 1, dev), _index(op, "table", table, None, dev), entries,
+             _index(op, "refs", refs, None, dev), pages, _index(op, "table_out", table_out, entries, dev),
+             _index(op, "refs_out", refs_out, pages, dev), _index(op, "free_out", free_out, n_free, dev),
+             _index(op, "remap", remap, pages, dev), _index(op, "copy_src", copy_src, None, dev),
+             _index(op, "copy_dst", copy_dst, n, dev), n, _index(op, "free_head_out", free_head_out, 1, dev),
+             None if status is None else _index(op, "status", status, 1, dev))
+
+
+def kq_kv_copy_pages(src, dst, k_cache, v_cache, stream=None) -> None:
+    """Page src[i] to page dst[i] (int32 [n]) of k_cache and v_cache uint8 [pages, kv_heads, page_bytes]; pairs with an id
+    that is no page are skipped."""
+    if _kqcall is not None and stream is None and src.is_cuda:
+        dev = torch._C._cuda_getDevice()
+        st = _kqcall.kv_copy_pages(src, dst, k_cache, v_cache, torch._C._cuda_getCurrentRawStream(dev), dev)
+        if st is not None:
+            return _check(st)
+    op, n, dev = "kq_kv_copy_pages", src.numel(), src.get_device()
+    if (k_cache.dtype is not torch.uint8 or v_cache.dtype is not torch.uint8 or k_cache.dim() != 3
+            or v_cache.shape != k_cache.shape or not k_cache.is_contiguous() or not v_cache.is_contiguous()):
+        raise ValueError(f"{op}: k_cache and v_cache must be contiguous uint8 [pages, kv_heads, page_bytes]")
+    if k_cache.get_device() != dev or v_cache.get_device() != dev:
+        raise ValueError(f"{op}: caches on devices {k_cache.get_device()} and {v_cache.get_device()}, lists on {dev}")
+    _call_on(dev, stream, _lib.kq_kv_copy_pages, _index(op, "src", src, n, dev), _index(op, "dst", dst, n, dev), n,
+             k_cache.data_ptr(), v_cache.data_ptr(), k_cache.shape[0], k_cache.shape[1] * k_cache.shape[2])
+
+
+def _rope_rows(op: str, name: str, x, out, dev: int):
+    """(pointer, heads, row stride, pointer, row stride) of rows and where they go; out None: in place."""
+    if out is None:
+        out = x
+    if x.dim() != 3 or x.dtype not in _DTYPES or out.shape != x.shape or out.dtype is not x.dtype:
+        raise ValueError(f"{op}: {name} and {name}_out must be [tokens, heads, d] of one float dtype")
+    if x.get_device() != dev or out.get_device() != dev:
+        raise ValueError(f"{op}: {name} and {name}_out must be on the device of cu_new")
+    return (x.data_ptr(), x.shape[1], _row_stride(op, name, x, x.shape), out.data_ptr(),
+            _row_stride(op, name + "_out", out, x.shape))
+
+
+def kq_rope(q, k, cu_new, seq_lens, inv_freq, q_out=None, k_out=None, layout="half", mscale: float = 1.0,
+            stream=None) -> None:
+    """q [tokens, q_heads, d] and k [tokens, kv_heads, d] (float32, float16 or bfloat16, dense rows, any row stride; one of
+    them may be None) turned to their positions, in place or to q_out and k_out.  cu_new int32 [n + 1], seq_lens int32 [n];
+    inv_freq float32 [rot / 2]: the first rot values of a head turn; layout 'half' or 'pairs' (or a KQ_ROPE_* id)."""
+    lay = _ROPE_LAYOUTS[layout] if isinstance(layout, str) else int(layout)
+    if _kqcall is not None and stream is None and cu_new.is_cuda:
+        dev = torch._C._cuda_getDevice()
+        st = _kqcall.rope(q, k, cu_new, seq_lens, inv_freq, q_out, k_out, lay, mscale,
+                          torch._C._cuda_getCurrentRawStream(dev), dev)
+        if st is not None:
+            return _check(st)
+    op, n, dev = "kq_rope", seq_lens.numel(), cu_new.get_device()
+    if (q is None and k is None) or (q is None and q_out is not None) or (k is None and k_out is not None):
+        raise ValueError(f"{op}: q or k is wanted, and no output without its input")
+    one = k if q is None else q
+    none = (None, 0, 0, None, 0)
+    qa = none if q is None else _rope_rows(op, "q", q, q_out, dev)
+    ka = none if k is None else _rope_rows(op, "k", k, k_out, dev)
+    if q is not None and k is not None and (q.shape[0] != k.shape[0] or q.shape[2] != k.shape[2] or q.dtype is not k.dtype):
+        raise ValueError(f"{op}: q and k must have the same tokens, head size and dtype")
+    if inv_freq.dtype is not torch.float32 or not inv_freq.is_contiguous() or inv_freq.get_device() != dev:
+        raise ValueError(f"{op}: inv_freq must be contiguous float32 on the device of cu_new")
+    _call_on(dev, stream, _lib.kq_rope, *qa[:3], *ka[:3], _DTYPES[one.dtype], one.shape[0], one.shape[2], 2 * inv_freq.numel(),
+             lay, _index(op, "cu_new", cu_new, n + 1, dev), _index(op, "seq_lens", seq_lens, n, dev), n, inv_freq.data_ptr(),
+             mscale, *qa[3:], *ka[3:])
+
+
+def kq_rope_freqs(rot: int, base: float = 10000.0, scaling="none", factor: float = 1.0, original: int = 0,
+                  fast: float = 32.0, slow: float = 1.0, factors=None, device="cuda"):
+    """(inv_freq float32 [rot / 2] on `device`, mscale) for kq_rope.  scaling 'none', 'linear', 'ntk' or 'yarn' by `factor`
+    over `original` positions; factors: a float tensor [rot / 2] of divisors (a GGUF file's rope_freqs)."""
+    sc = _ROPE_SCALINGS[scaling] if isinstance(scaling, str) else int(scaling)
+    div = None
+    if factors is not None:
+        div = factors.detach().to(device="cpu", dtype=torch.float32).contiguous()
+        if div.numel() != rot // 2:
+            raise ValueError(f"kq_rope_freqs: factors has {div.numel()} entries, expected {rot // 2}")
+    out, m = (ctypes.c_float * max(1, rot // 2))(), ctypes.c_float()
+    _check(_lib.kq_rope_freqs(rot, base, sc, factor, original, fast, slow, _ptr(div), out, ctypes.byref(m)))
+    return torch.tensor(list(out), dtype=torch.float32, device=device), m.value
 
 
 # ---------------------------------------------------------------------------
@@ -567,3 +781,41 @@ def kv_attention(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page: int,
     out = torch.zeros(q.shape, dtype=out_dtype or q.dtype, device=q.device)
     kq_kv_attention(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page, out, scale, window, max_new, max_kv)
     return out
+
+
+def kv_attention_sinks(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page: int, window: int, sinks: int, scale=None,
+                       max_new=None, max_kv=None, out_dtype=None):
+    out = torch.zeros(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    kq_kv_attention_sinks(codec, q, cu_new, seq_lens, table, k_cache, v_cache, page, out, window, sinks, scale, max_new, max_kv)
+    return out
+
+
+def kv_attention_prefix(codec, q, cu_new, seq_lens, table, prefix, k_cache, v_cache, page: int, scale=None, max_new=None,
+                        max_kv=None, out_dtype=None):
+    out = torch.zeros(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    kq_kv_attention_prefix(codec, q, cu_new, seq_lens, table, prefix, k_cache, v_cache, page, out, scale, max_new, max_kv)
+    return out
+
+
+def kv_fork(parents, children, lens, page: int, table, refs, free_pages, free_head):
+    """(copy_src [n], copy_dst [n], free_head_out [1], status [1]) of forks; table and refs are updated."""
+    n, dev = parents.numel(), parents.device
+    src, dst, head, status = (torch.empty((m,), dtype=torch.int32, device=dev) for m in (n, n, 1, 1))
+    kq_kv_fork(parents, children, lens, page, table, refs, free_pages, free_head, src, dst, head, status)
+    return src, dst, head, status
+
+
+def kv_free(first, last, table, refs, free_pages, free_head):
+    """(free_head_out [1], status [1]); refs and free_pages are updated."""
+    head, status = (torch.empty((1,), dtype=torch.int32, device=first.device) for _ in range(2))
+    kq_kv_free(first, last, table, refs, free_pages, free_head, head, status)
+    return head, status
+
+
+def kv_compact(free_pages, free_head, table, refs):
+    """(remap [pages], copy_src, copy_dst, status [1]); table, refs, free_pages and free_head are updated."""
+    pages, dev = refs.numel(), refs.device
+    most = min(free_pages.numel(), pages // 2)
+    remap, src, dst, status = (torch.empty((m,), dtype=torch.int32, device=dev) for m in (pages, most, most, 1))
+    kq_kv_compact(free_pages, free_head, table, refs, table, refs, free_pages, remap, src, dst, free_head, status)
+    return remap, src, dst, status

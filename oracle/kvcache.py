@@ -1,4 +1,5 @@
-"""Oracle of the 4-bit key/value cache: row encoding, cache layout, block tables, attention.
+"""Oracle of the 4-bit key/value cache: row encoding, cache layout, block tables, attention, pages shared and moved,
+rotary positions.
 
 Everything is plain NumPy from the definitions in ``include/kq.h``; encoding and
 attention are evaluated in float64.
@@ -6,7 +7,8 @@ attention are evaluated in float64.
 Pins (``tests/test_oracle_kv.py``): the encoding against exact rational
 arithmetic and the q4_0 wire encoder, the layout against a hand-packed page,
 block tables against a step-by-step allocator, attention against a scalar
-softmax loop and closed forms (uniform weights, one key).
+softmax loop and closed forms (uniform weights, one key), pages against hand-worked steps and
+what they mean for the rows a request reads, rotary positions against complex products.
 """
 
 from __future__ import annotations
@@ -106,8 +108,11 @@ def block_tables(ctx, new, page, free, head, table, tokens):
     return table, slots, cu, lens, head + taken, status
 
 
-def attention(q, cu, lens, table, k_cache, v_cache, page, scale, window=0, detail=False):
+def attention(q, cu, lens, table, k_cache, v_cache, page, scale, window=0, detail=False, sinks=0, prefix=None):
     """float64 [tokens, q_heads, d] from q [tokens, q_heads, d]; rows of no request are NaN.
+
+    ``sinks``: first keys that stay visible beside the window; ``prefix``: pages in the place of the table's first ones, for
+    requests whose new tokens all stand behind them.
 
     With ``detail`` also, per row: sum p |v| [tokens, q_heads, d], the largest
     scale * sum |q| |k| over its keys, and its number of keys.
@@ -122,7 +127,10 @@ def attention(q, cu, lens, table, k_cache, v_cache, page, scale, window=0, detai
         a, b = (min(max(int(cu[s + i]), 0), tokens) for i in (0, 1))
         length = min(max(int(lens[s]), 0), len(table[s]) * page)
         out[a:b] = 0
-        ids = np.repeat(np.asarray(table[s], np.int64), page)[:length]
+        row = np.array(table[s], np.int64)
+        if prefix is not None and length - (b - a) >= len(prefix) * page:
+            row[:len(prefix)] = prefix
+        ids = np.repeat(row, page)[:length]
         there = (ids >= 0) & (ids < pages)
         slots = np.where(there, ids, 0) * page + np.arange(length) % page
         k, v = (load(c, page, d, slots) for c in (k_cache, v_cache))
@@ -130,7 +138,7 @@ def attention(q, cu, lens, table, k_cache, v_cache, page, scale, window=0, detai
             p = length - (b - a) + (t - a)
             see = there & (np.arange(length) <= p)
             if window > 0:
-                see &= np.arange(length) > p - window
+                see &= (np.arange(length) > p - window) | (np.arange(length) < sinks)
             if not see.any():
                 continue
             for h in range(hq):
@@ -144,3 +152,112 @@ def attention(q, cu, lens, table, k_cache, v_cache, page, scale, window=0, detai
                     mag[t, h] = abs(scale) * (np.abs(ks) @ np.abs(q[t, h])).max()
                     count[t, h] = see.sum()
     return (out, absv, mag, count) if detail else out
+
+
+# ---------------------------------------------------------------------------
+# pages shared, given back and moved
+# ---------------------------------------------------------------------------
+
+def fork(parents, children, lens, page, table, refs, free, head):
+    """(table, refs, copy_src, copy_dst, head, status) of forks taken one after the other."""
+    table = [list(map(int, row)) for row in table]
+    refs, free = [int(r) for r in refs], [int(f) for f in free]
+    width = len(table[0]) if table else 0
+    avail = len(free) - head if 0 <= head <= len(free) else 0
+    src, dst, status, asked, taken = [], [], 0, 0, 0
+    for p, c, n in zip(map(int, parents), map(int, children), map(int, lens)):
+        whole, part = n // page, n % page > 0
+        bad = 0
+        if n < 0:
+            bad = 8
+        elif not 0 <= p < len(table) or not 0 <= c < len(table) or p == c:
+            bad = 4
+        elif whole + part > width:
+            bad = 2
+        elif part:
+            asked += 1
+            if asked > avail:
+                bad = 1
+        status |= bad
+        src.append(-1)
+        dst.append(-1)
+        if bad:
+            continue
+        for j in range(whole):
+            table[c][j] = table[p][j]
+            if 0 <= table[p][j] < len(refs):
+                refs[table[p][j]] += 1
+        if part:
+            taken = asked
+            src[-1], dst[-1] = table[p][whole], free[head + asked - 1]
+            table[c][whole] = dst[-1]
+    return table, refs, src, dst, head + taken, status
+
+
+def free(first, last, table, refs, free_pages, head):
+    """(refs, free_pages, head, status) after the entries first .. last - 1 of every row are given back."""
+    refs, out = [int(r) for r in refs], [int(f) for f in free_pages]
+    for a, b, row in zip(map(int, first), map(int, last), table):
+        for j in range(max(a, 0), min(b, len(row))):
+            if 0 <= int(row[j]) < len(refs):
+                refs[int(row[j])] -= 1
+    status = int(min(refs, default=0) < -1)
+    dead = [p for p, r in enumerate(refs) if r < 0]
+    for i, p in enumerate(dead):
+        refs[p] = 0
+        if 0 <= head - len(dead) + i < len(out):
+            out[head - len(dead) + i] = p
+    return refs, out, max(0, head - len(dead)), status | 2 * (head < len(dead))
+
+
+def compact(free_pages, head, table, refs, n_copy):
+    """(table, refs, free_pages, remap, copy_src, copy_dst, head, status); table is a flat list of entries."""
+    pages, n_free = len(refs), len(free_pages)
+    listed = [int(f) for f in free_pages[head:]] if 0 <= head <= n_free else []
+    gone = {f for f in listed if 0 <= f < pages}
+    held = pages - len(gone)
+    movers = [p for p in range(held, pages) if p not in gone]
+    holes = [p for p in range(held) if p in gone]
+    remap = [-1 if p in gone else p for p in range(pages)]
+    for a, b in zip(movers, holes):
+        remap[a] = b
+    out = [0] * pages
+    for p in range(pages):
+        if remap[p] >= 0:
+            out[remap[p]] = int(refs[p])
+    entries = [remap[int(e)] if 0 <= int(e) < pages else -1 for e in table]
+    new_head = n_free - len(gone)
+    lists = [x + [-1] * (n_copy - len(x)) for x in (movers, holes)]
+    return (entries, out, [int(f) for f in free_pages[:new_head]] + list(range(held, pages)), remap, *lists, new_head,
+            int(new_head != head))
+
+
+# ---------------------------------------------------------------------------
+# rotary positions
+# ---------------------------------------------------------------------------
+
+def positions(cu, lens, tokens):
+    """Position of every token row; None for rows of no request and below 0."""
+    pos = [None] * tokens
+    for s, n in enumerate(lens):
+        a, b = (min(max(int(cu[s + i]), 0), tokens) for i in (0, 1))
+        for t in range(a, b):
+            p = max(int(n), 0) - b + t
+            pos[t] = p if p >= 0 else None
+    return pos
+
+
+def rope(x, pos, inv_freq, layout, mscale):
+    """float64 rows [tokens, heads, d] turned to their positions; rows without one are NaN."""
+    x = np.asarray(x, np.float64)
+    out, half = np.full(x.shape, np.nan), len(inv_freq)
+    for t, p in enumerate(pos):
+        if p is None:
+            continue
+        out[t] = x[t]
+        for i in range(half):
+            a = p * float(inv_freq[i])
+            j, k = (2 * i, 2 * i + 1) if layout == "pairs" else (i, i + half)
+            out[t, :, j] = mscale * (x[t, :, j] * np.cos(a) - x[t, :, k] * np.sin(a))
+            out[t, :, k] = mscale * (x[t, :, k] * np.cos(a) + x[t, :, j] * np.sin(a))
+    return out

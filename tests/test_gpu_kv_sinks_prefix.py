@@ -1,0 +1,435 @@
+"""GPU parity of attention with sinks and over a shared prefix, and serving steps of all cache operators together.
+
+Bounds are those of ``test_gpu_kv``: the rows' sums over a prefix and over their
+own keys are joined in float32, as those of workgroups that share a row are.
+"""
+
+import numpy as np
+import pytest
+
+from _gpu import dev, host
+from oracle import kvcache
+from test_gpu_kv import HEADS, _bound, _case, _close, _f64, _i32, _tdt
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def kq():
+    from gguf_quant_matmul_amd import kq as mod
+
+    return mod
+
+
+def _hold(c, got, what, out, scale=None, window=0, sinks=0, prefix=None):
+    sc = c["d"] ** -0.5 if scale is None else float(np.float32(scale))
+    ref, absv, mag, count = kvcache.attention(_f64(c["q"]), c["cu"], c["lens"], c["table"], c["kc"], c["vc"], c["page"], sc,
+                                              window, detail=True, sinks=sinks, prefix=prefix)
+    got = _f64(got)
+    none = np.isnan(ref)
+    assert (got[none] == 77).all(), f"{what}: rows of no request were written"
+    ref[none] = got[none]
+    vmax = np.nanmax(np.abs(kvcache.load(c["vc"], c["page"], c["d"], np.arange(c["vc"].shape[0] * c["page"]))))
+    assert not got[(count == 0) & ~none.any(-1)].any(), f"{what}: a row without keys is not zero"
+    _close(got, ref, _bound(ref, absv, mag, count, vmax, c["d"], out), what)
+
+
+def _args(c, out):
+    import torch
+
+    o = torch.full(c["q"].shape, 77.0, dtype=_tdt(out), device="cuda")
+    return o, (c["q"], _i32(c["cu"]), _i32(c["lens"]), _i32(c["table"]))
+
+
+# ---------------------------------------------------------------------------
+# sinks
+# ---------------------------------------------------------------------------
+
+def _sinks(kq, c, window, sinks, out="f16", **kw):
+    o, a = _args(c, out)
+    kq.kq_kv_attention_sinks("q4_0", *a, dev(c["kc"]), dev(c["vc"]), c["page"], o, window, sinks, **kw)
+    return o
+
+
+@pytest.mark.parametrize("q_dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq, kv, d, page", HEADS)
+def test_sinks_single_tokens(kq, hq, kv, d, page, q_dtype):
+    lens = [1, 2, 15, 16, 64, 65, 0, 129, 300, 555]
+    c = _case(d, [1] * len(lens), lens, hq, kv, d, page, q_dtype)
+    for window, sinks in ((33, 4), (64, 70), (100, 1), (1, 1)):
+        got = _sinks(kq, c, window, sinks, q_dtype, max_new=1, max_kv=555)
+        _hold(c, got, f"window {window} sinks {sinks}", q_dtype, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("q_dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq, kv, d, page", HEADS)
+def test_sinks_prompts(kq, hq, kv, d, page, q_dtype):
+    new = [1, 37, 0, 64, 5, 3, 9, 150]
+    lens = [1, 37, 10, 330, 400, 0, 4, 500]
+    c = _case(d + 1, new, lens, hq, kv, d, page, q_dtype, extra_tokens=3)
+    for window, sinks, bounds in ((17, 4, True), (40, 130, True), (90, 5, False)):
+        kw = dict(max_new=150, max_kv=500) if bounds else {}
+        _hold(c, _sinks(kq, c, window, sinks, "bf16", **kw), f"window {window} sinks {sinks}", "bf16", window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("d, hq, kv, page", [(64, 4, 2, 16), (128, 8, 2, 128), (256, 4, 2, 64)])
+@pytest.mark.parametrize("new, lens", [([1, 1, 1], [5000, 30, 4000]), ([2, 90, 1, 40], [3000, 2500, 7, 1500]), ([300], [4000])])
+def test_sinks_split_keys(kq, new, lens, d, hq, kv, page):
+    # rows whose keys are shared by workgroups, 16-row and prompt tiles
+    c = _case(sum(lens) + d, new, lens, hq, kv, d, page)
+    _hold(c, _sinks(kq, c, 2000, 100, "f32", max_new=max(new), max_kv=5000), "split", "f32", window=2000, sinks=100)
+
+
+def test_no_sinks_no_window(kq):
+    # where sinks change nothing the call is kq_kv_attention, bit for bit
+    import torch
+
+    c = _case(5, [1, 40, 3], [400, 700, 90], 8, 2, 128, 32)
+    o, a = _args(c, "f16")
+    caches = dev(c["kc"]), dev(c["vc"])
+    for window, sinks in ((50, 0), (0, 9), (1 << 30, 4), (60, 1 << 30), (1 << 40, 1 << 40)):
+        kq.kq_kv_attention_sinks("q4_0", *a, *caches, c["page"], o.fill_(77), window, sinks, max_new=40, max_kv=700)
+        same = torch.full_like(o, 77.0)
+        kq.kq_kv_attention("q4_0", *a, *caches, c["page"], same, window=window if sinks == 0 else 0, max_new=40, max_kv=700)
+        assert torch.equal(o, same), (window, sinks)
+    # sinks as far as the window: every key, by another path
+    _hold(c, _sinks(kq, c, 300, 500, "f32", max_new=40, max_kv=700), "all keys", "f32", window=300, sinks=500)
+
+
+@pytest.mark.parametrize("new, lens", [([1, 1], [3000, 900]), ([70, 1], [2000, 500])])
+def test_pages_between_sinks_and_window_are_not_read(kq, new, lens):
+    # their table entries name no pages; and pages full of NaN, where one is named, give nothing
+    page, window, sinks = 16, 200, 20
+    c = _case(8, new, lens, 4, 2, 64, page)
+    want = _f64(_sinks(kq, c, window, sinks, max_new=max(new), max_kv=3000))
+    free = np.nonzero(~np.isin(np.arange(c["kc"].shape[0]), c["table"]))[0][0]  # (NaN scales)
+    for s, (m, n) in enumerate(zip(new, lens)):
+        a, b = 128 // page, (n - m - window + 1) // 64 * 64 // page
+        for fill in (-1, free, 1 << 30):
+            was = c["table"].copy()
+            c["table"][s, a:b] = fill
+            assert np.array_equal(_f64(_sinks(kq, c, window, sinks, max_new=max(new), max_kv=3000)), want)
+            c["table"] = was
+
+
+# ---------------------------------------------------------------------------
+# a shared prefix
+# ---------------------------------------------------------------------------
+
+def _shared(seed, new, own, n_prefix, hq, kv, d, page, q_dtype="f16", apart=(), q_scale=1.0, extra_tokens=0):
+    """A batch whose requests share n_prefix pages and hold own[s] keys behind them (those in `apart`: own[s] keys of
+    their own and no prefix)."""
+    lens = [m if s in apart else n_prefix * page + m for s, m in enumerate(own)]
+    c = _case(seed, new, lens, hq, kv, d, page, q_dtype, q_scale, extra_tokens)
+    first = next(s for s in range(len(own)) if s not in apart)
+    prefix = c["table"][first, :n_prefix].copy()
+    for s in range(len(own)):
+        if s not in apart:
+            c["table"][s, :n_prefix] = -5  # (not read)
+    c["prefix"] = prefix
+    return c
+
+
+def _prefix(kq, c, out="f16", **kw):
+    o, a = _args(c, out)
+    kq.kq_kv_attention_prefix("q4_0", *a, _i32(c["prefix"]), dev(c["kc"]), dev(c["vc"]), c["page"], o, **kw)
+    return o
+
+
+def _check_prefix(kq, c, what, out="f16", scale=None, **kw):
+    _hold(c, _prefix(kq, c, out, scale=scale, **kw), what, out, scale, prefix=c["prefix"])
+
+
+@pytest.mark.parametrize("q_dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq, kv, d, page", HEADS)
+def test_prefix_single_tokens(kq, hq, kv, d, page, q_dtype):
+    own = [1, 2, 15, 16, 17, 64, 0, 65, 130, 9]
+    c = _shared(d, [1] * len(own), own, 5 if page < 128 else 1, hq, kv, d, page, q_dtype, apart=(6, 9))
+    bounds = dict(max_new=1, max_kv=int(c["lens"].max()))
+    _check_prefix(kq, c, "host bounds", q_dtype, **bounds)
+    _check_prefix(kq, c, "no bounds", "f32")
+
+
+@pytest.mark.parametrize("q_dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("hq, kv, d, page", HEADS)
+def test_prefix_prompts(kq, hq, kv, d, page, q_dtype):
+    new = [1, 37, 0, 64, 5, 3, 9, 100]
+    own = [1, 37, 10, 130, 200, 0, 4, 100]
+    c = _shared(d + 1, new, own, 9 if page < 128 else 2, hq, kv, d, page, q_dtype, apart=(2, 4, 5, 6), extra_tokens=3)
+    bounds = dict(max_new=100, max_kv=int(c["lens"].max()))
+    _check_prefix(kq, c, "host bounds", q_dtype, **bounds)
+    _check_prefix(kq, c, "no bounds", "bf16")
+
+
+@pytest.mark.parametrize("d, hq, kv, page", [(64, 4, 2, 16), (128, 8, 2, 128), (96, 3, 3, 64), (256, 4, 2, 32)])
+@pytest.mark.parametrize("new, own, keys", [([1] * 3, [5, 1, 1], 4000), ([1] * 70, [3] * 70, 1000), ([2, 90, 1], [2100, 90, 1500], 256),
+                                            ([1, 1], [3000, 1700], 128), ([300], [300], 640), ([6] * 9, [6] * 9, 144)])
+def test_prefix_split_keys(kq, new, own, keys, d, hq, kv, page):
+    # prefixes cut into parts, own keys shared by workgroups, and both
+    c = _shared(sum(own) + d, new, own, max(1, keys // page), hq, kv, d, page)
+    _check_prefix(kq, c, "split", "f32", max_new=max(new), max_kv=int(c["lens"].max()))
+
+
+def test_prefix_uniform_weights_count_every_key_once(kq):
+    c = _shared(50, [1, 1, 3, 70, 1], [30, 1, 66, 200, 5], 21, 8, 2, 128, 16)
+    _check_prefix(kq, c, "mean", "f32", scale=0.0, max_new=70, max_kv=540)
+    _check_prefix(kq, c, "mean, no bounds", "f32", scale=0.0)
+
+
+@pytest.mark.parametrize("new, own", [([1, 1, 1], [9, 200, 1]), ([90, 1], [90, 30])])
+def test_prefix_pages_that_are_none(kq, new, own):
+    # keys of entries that name no page are left out; a prefix of such alone is like none
+    c = _shared(7, new, own, 12, 4, 2, 64, 16)
+    bounds = dict(max_new=max(new), max_kv=int(c["lens"].max()))
+    c["prefix"][[0, 3, 11]] = [-1, 1 << 30, c["kc"].shape[0]]
+    _check_prefix(kq, c, "some", "f16", **bounds)
+    c["prefix"][:] = -1
+    _check_prefix(kq, c, "all", "f16", **bounds)
+
+
+@pytest.mark.parametrize("scale, q_scale", [(20.0, 200.0), (-20.0, 200.0), (3e38, 1.0)])
+def test_prefix_large_logits(kq, scale, q_scale):
+    # logits far apart: the row is the value of its largest key, in the prefix or behind it
+    c = _shared(70, [1, 1, 40], [40, 3, 90], 8, 8, 2, 64, 16, q_scale=q_scale)
+    got, ref = _f64(_prefix(kq, c, "f32", scale=scale, max_new=40, max_kv=250)), kvcache.attention(
+        _f64(c["q"]), c["cu"], c["lens"], c["table"], c["kc"], c["vc"], 16, float(np.float32(scale)), prefix=c["prefix"])
+    assert np.isfinite(got).all()
+    # products are off by 2^-11 of the largest at most; rows whose two largest are nearer than that say nothing
+    sure = 0
+    for t in range(got.shape[0]):
+        for h in range(got.shape[1]):
+            sure += np.abs(got[t, h] - ref[t, h]).max() <= 2.0 ** -10 * np.abs(ref[t, h]).max()
+    assert sure >= 0.97 * got.shape[0] * got.shape[1]
+
+
+def test_prefix_of_a_part_of_the_batch(kq):
+    # requests 2 and 3 of four share a prefix: a call of their own, on slices, writes only their rows
+    import torch
+
+    c = _shared(90, [1, 3, 2, 5, 1], [30, 90, 7, 60, 4], 6, 4, 2, 128, 16, apart=(0, 1, 4))
+    o, (q, cu, lens, table) = _args(c, "f16")
+    kq.kq_kv_attention_prefix("q4_0", q, cu[2:5], lens[2:4], table[2:4], _i32(c["prefix"]), dev(c["kc"]), dev(c["vc"]), 16, o,
+                              max_new=5, max_kv=160)
+    torch.cuda.synchronize()
+    assert (o[:4] == 77).all() and (o[11:] == 77).all()
+    whole = _prefix(kq, c, "f16", max_new=5, max_kv=160)
+    ref = _f64(whole)[4:11]
+    assert np.abs(_f64(o)[4:11] - ref).max() <= 2.0 ** -9 * np.abs(ref).max()
+
+
+# ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+
+HQ, KV, D, PAGE, PAGES, ROWS, WIDTH = 8, 2, 64, 16, 80, 5, 12
+
+
+def test_serving_steps_together(kq):
+    """A prompt, four samples of it, steps on the shared pages, a window that moves on, a compaction."""
+    import torch
+
+    rng = np.random.default_rng(4)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    kc, vc = kq.kv_cache("q4_0", PAGES, KV, PAGE, D)
+    table = torch.full((ROWS, WIDTH), -1, dtype=torch.int32, device="cuda")
+    refs = torch.zeros(PAGES, dtype=torch.int32, device="cuda")
+    free = torch.from_numpy(rng.permutation(PAGES).astype(np.int32)).cuda()
+    head = i32(0)
+    freq, m = kq.kq_rope_freqs(D, 1e4, "yarn", 4.0, 512)
+    ctx = torch.zeros(ROWS, dtype=torch.int32, device="cuda")
+
+    def step(new):
+        """One step of the batch: tables, rotation in place, store; its queries, offsets and lengths."""
+        nonlocal head, ctx
+        tokens = sum(new)
+        slots, cu, lens, head, st = kq.block_tables(ctx, i32(*new), free, head, PAGE, table, tokens)
+        assert st.item() == 0
+        qkv = torch.from_numpy(rng.standard_normal((tokens, HQ + 2 * KV, D)).astype(np.float16)).cuda()
+        q, k, v = qkv[:, :HQ], qkv[:, HQ:HQ + KV], qkv[:, HQ + KV:]
+        was = qkv.clone()
+        kq.kq_rope(q, k, cu, lens, freq, mscale=m)
+        pos = kvcache.positions(host(cu), host(lens), tokens)
+        ref = kvcache.rope(_f64(was[:, :HQ + KV]), pos, host(freq), "half", m)
+        assert np.abs(_f64(qkv[:, :HQ + KV]) - ref).max() <= 2.0 ** -10 * np.abs(ref).max()
+        kq.kq_kv_store("q4_0", k, v, slots, kc, vc, PAGE)
+        ctx = lens
+        return q, cu, lens
+
+    def case(q, cu, lens):
+        return dict(q=q, cu=host(cu), lens=host(lens), table=host(table), kc=host(kc), vc=host(vc), page=PAGE, d=D)
+
+    def attend(fn, *a, **kw):
+        o = torch.full((a[0].shape[0], HQ, D), 77.0, dtype=torch.float16, device="cuda")
+        fn("q4_0", *a, kc, vc, PAGE, o, **kw)
+        return o
+
+    # the prompt of request 0
+    q, cu, lens = step([70, 0, 0, 0, 0])
+    _hold(case(q, cu, lens), attend(kq.kq_kv_attention, q, cu, lens, table), "prompt", "f16")
+    # requests 1 to 4 continue from it, the last from its 64th token; the ends are copied
+    src, dst, head, st = kq.kv_fork(i32(0, 0, 0, 0), i32(1, 2, 3, 4), i32(70, 70, 70, 64), PAGE, table, refs, free, head)
+    kq.kq_kv_copy_pages(src, dst, kc, vc)
+    assert st.item() == 0 and host(refs).sum() == 4 * 4 and (host(dst) >= 0).tolist() == [True, True, True, False]
+    ctx = i32(70, 70, 70, 70, 64)
+    prefix = table[0, :4].clone()
+    for new in ([1, 1, 1, 1, 1], [0, 3, 1, 1, 40], [1] * 5):
+        q, cu, lens = step(new)
+        c = case(q, cu, lens)
+        c["prefix"] = host(prefix)
+        plain = attend(kq.kq_kv_attention, q, cu, lens, table)
+        shared = attend(kq.kq_kv_attention_prefix, q, cu, lens, table, prefix)
+        _hold(c, plain, "every request by itself", "f16")
+        _hold(c, shared, "over the prefix", "f16", prefix=c["prefix"])
+    # request 2 ends; the others keep 4 tokens and a window of 20: pages between go back
+    n = host(lens)
+    first = [1, 1, 0, 1, 1]
+    last = [int((x - 20) // PAGE) for x in n]
+    last[2] = -(-int(n[2]) // PAGE)
+    before = host(head).item()
+    head, st = kq.kv_free(i32(*first), i32(*last), table, refs, free, head)
+    assert st.item() == 0 and host(head).item() < before
+    for s in range(ROWS):
+        table[s, first[s]:last[s]] = -1
+    lens = lens.clone()
+    lens[2] = 0
+    c = case(q, cu, lens)
+    got = attend(kq.kq_kv_attention_sinks, q, cu, lens, table, window=20, sinks=4)
+    _hold(c, got, "sinks and window", "f16", window=20, sinks=4)
+    # held pages to the front: rows read the same, bit for bit
+    count = PAGES - (PAGES - host(head).item())
+    remap, src, dst, st = kq.kv_compact(free, head, table, refs)
+    kq.kq_kv_copy_pages(src, dst, kc, vc)
+    assert st.item() == 0 and host(table).max() < count and host(head).item() == count
+    assert sorted(host(free)[count:].tolist()) == list(range(count, PAGES))
+    kc[count:], vc[count:] = 255, 255  # (nothing there is read)
+    again = attend(kq.kq_kv_attention_sinks, q, cu, lens, table, window=20, sinks=4)
+    assert torch.equal(got, again)
+    holders = np.bincount(host(table)[host(table) >= 0], minlength=PAGES)
+    assert (np.maximum(holders - 1, 0) == host(refs)).all()
+
+
+def _all_calls(kq):
+    """Calls of every operator on one set of buffers, and the buffers they write."""
+    import torch
+
+    rng = np.random.default_rng(6)
+    c = _shared(30, [1, 3, 1], [700, 1300, 40], 6, HQ, KV, D, PAGE)
+    i32 = lambda *a: torch.tensor(a, dtype=torch.int32, device="cuda")
+    fill = lambda *s: torch.full(s, -99, dtype=torch.int32, device="cuda")
+    q, cu, lens, table, pre = c["q"], _i32(c["cu"]), _i32(c["lens"]), _i32(c["table"]), _i32(c["prefix"])
+    kc, vc = dev(c["kc"]), dev(c["vc"])
+    pages = kc.shape[0]
+    freq = torch.from_numpy(_freq()).cuda()
+    b = dict(qo=torch.zeros_like(q), sinks=torch.zeros_like(q), prefix=torch.zeros_like(q), src=fill(2), dst=fill(2),
+             head=fill(1), status=fill(1), table2=torch.full((4, 6), -1, dtype=torch.int32, device="cuda"),
+             refs=torch.zeros(pages, dtype=torch.int32, device="cuda"), free=torch.arange(pages, dtype=torch.int32, device="cuda"),
+             head2=fill(1), status2=fill(1), to=fill(4, 6), ro=fill(pages), fo=fill(pages), remap=fill(pages),
+             csrc=fill(pages // 2), cdst=fill(pages // 2), ho=fill(1), kc=torch.randint_like(kc, 256), vc=torch.randint_like(vc, 256))
+    b["table2"][0, :3] = i32(5, 1, 9)
+    table0, refs0, free0 = b["table2"].clone(), b["refs"].clone(), b["free"].clone()
+    parents, children, take, head0, first, last = i32(0, 0), i32(1, 3), i32(40, 32), i32(20), i32(0, 0, 0, 0), i32(0, 3, 0, 1)
+    heads = i32(20)
+    ws = [torch.empty(kq.kq_kv_attention_workspace(5, 3, HQ, KV, D, 3, 1400), dtype=torch.uint8, device="cuda"),
+          torch.empty(kq.kq_kv_attention_prefix_workspace(5, 3, HQ, KV, D, 6 * PAGE, 3, 1400), dtype=torch.uint8, device="cuda")]
+
+    def run(**kw):
+        b["table2"].copy_(table0)
+        b["refs"].copy_(refs0)
+        b["free"].copy_(free0)
+        kq.kq_rope(q, None, cu, lens, freq, b["qo"], **kw)
+        kq.kq_kv_fork(parents, children, take, PAGE, b["table2"], b["refs"], b["free"], head0, b["src"], b["dst"], b["head"],
+                      b["status"], **kw)
+        kq.kq_kv_copy_pages(b["src"], b["dst"], b["kc"], b["vc"], **kw)
+        kq.kq_kv_free(first, last, b["table2"], b["refs"], b["free"], b["head"], b["head2"], b["status2"], **kw)
+        kq.kq_kv_compact(b["free"], heads, b["table2"], b["refs"], b["to"], b["ro"], b["fo"], b["remap"], b["csrc"], b["cdst"],
+                         b["ho"], **kw)
+        kq.kq_kv_attention_sinks("q4_0", b["qo"], cu, lens, table, kc, vc, PAGE, b["sinks"], 600, 30, max_new=3, max_kv=1400,
+                                 workspace=ws[0], **kw)
+        kq.kq_kv_attention_prefix("q4_0", b["qo"], cu, lens, table, pre, kc, vc, PAGE, b["prefix"], max_new=3, max_kv=1400,
+                                  workspace=ws[1], **kw)
+
+    return run, b, q
+
+
+def _freq():
+    return (1e4 ** (-np.arange(0, D, 2) / D)).astype(np.float32)
+
+
+def test_both_python_paths_and_streams_give_the_same(kq, monkeypatch):
+    import torch
+
+    assert kq._kqcall is not None
+    run, b, _ = _all_calls(kq)
+    run()
+    torch.cuda.synchronize()
+    want = {n: x.clone() for n, x in b.items()}
+    assert want["sinks"].abs().sum() > 0 and want["prefix"].abs().sum() > 0
+    other = torch.cuda.Stream()
+
+    def on_current():
+        other.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(other):
+            run()
+
+    for what in ("ctypes", "another stream is current", "ctypes, another stream is current"):
+        for n, x in b.items():
+            if n not in ("kc", "vc"):
+                x.zero_()
+        torch.cuda.synchronize()
+        with monkeypatch.context() as mp:
+            if "ctypes" in what:
+                mp.setattr(kq, "_kqcall", None)
+            run() if what == "ctypes" else on_current()
+        torch.cuda.synchronize()
+        for n in want:
+            assert torch.equal(b[n], want[n]), (what, n)
+
+
+def test_a_given_stream(kq):
+    # a call on a stream that is not the current one: after that stream's own work
+    import torch
+
+    run, b, q = _all_calls(kq)
+    run()
+    torch.cuda.synchronize()
+    want = b["qo"].clone()
+    other, src = torch.cuda.Stream(), q.clone()
+    q.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(other):
+        torch.cuda._sleep(10_000_000)
+        q.copy_(src)
+    cu, lens = _i32([0, 1, 4, 5]), _i32([796, 1396, 136])
+    freq = torch.from_numpy(_freq()).cuda()
+    out = torch.zeros_like(q)
+    torch.cuda.current_stream().synchronize()
+    kq.kq_rope(q, None, cu, lens, freq, out, stream=other)
+    other.synchronize()
+    assert torch.equal(out, want)
+
+
+def test_graph_replays_match_eager(kq):
+    import torch
+
+    run, b, q = _all_calls(kq)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        run()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        run()
+    for i in range(4):
+        q.copy_(torch.randn_like(q))
+        caches = b["kc"].clone(), b["vc"].clone()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = {n: x.clone() for n, x in b.items()}
+        b["kc"].copy_(caches[0])
+        b["vc"].copy_(caches[1])
+        run()
+        torch.cuda.synchronize()
+        for n in b:
+            assert torch.equal(b[n], got[n]), (i, n)
+        torch.zeros(1000, device="cuda").sum().item()
