@@ -677,7 +677,9 @@ struct AttnCall {
 kq::AttnPlan tail_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
                        int64_t max_kv, int64_t prefix_len) {
   const int64_t own = max_kv > prefix_len ? max_kv - prefix_len : 1;
-  return kq::attn_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, own, 0);
+  kq::AttnPlan p = kq::attn_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, own, 0);
+  kq::plan_tiles(p, tokens, q_heads, kv_heads, d, own);
+  return p;
 }
 
 int check_prefix(const char* op, int64_t prefix_len) {
@@ -732,10 +734,11 @@ int attention(const char* op, const AttnCall& c) {
       {"v_cache", c.v_cache, cache}, {"prefix", c.prefix, 4 * c.n_prefix}};
   for (const auto& r : in)
     if (r.bytes > 0 && overlaps(r.p, r.bytes, c.out, out_bytes)) return fail(KQ_ERR_ARG, op, "out overlaps %s", r.name);
-  // (the sinks widen what a row sees as so many keys more of its window do)
   const kq::AttnPlan plan =
       c.prefix ? tail_plan(c.tokens, c.n_seqs, c.q_heads, c.kv_heads, c.d, c.max_new, c.max_kv, prefix_len)
-               : kq::attn_plan(c.tokens, c.n_seqs, c.q_heads, c.kv_heads, c.d, c.max_new, c.max_kv, window + sinks);
+      : sinks > 0
+          ? kq::sinks_plan(c.tokens, c.n_seqs, c.q_heads, c.kv_heads, c.d, c.max_new, c.max_kv, window, sinks)
+          : kq::attn_plan(c.tokens, c.n_seqs, c.q_heads, c.kv_heads, c.d, c.max_new, c.max_kv, window);
   kq::PrefixPlan flat = {0, 0, 0, 0};
   if (c.prefix) flat = kq::prefix_plan(c.tokens, c.q_heads, c.kv_heads, c.d, prefix_len);
   const int64_t need = flat.bytes + plan.bytes;

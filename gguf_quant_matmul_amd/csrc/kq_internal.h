@@ -442,6 +442,9 @@ struct AttnPlan {
 };
 AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
                    int64_t max_kv, int64_t window);
+AttnPlan sinks_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
+                    int64_t max_kv, int64_t window, int64_t sinks);
+void plan_tiles(AttnPlan& p, int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t seen);
 int attn_prompt_rows(int64_t d);  // rows of a prompt tile
 // The prefix's part: one tile kernel over all rows of the batch, each tile's
 // steps cut into `splits`.

@@ -488,9 +488,11 @@ __device__ __forceinline__ float sums_at(float m, float factor) {
 
 // A row's sums over the shared prefix, a.splits pieces of them, beside its own:
 // the maximum of both, then the pieces weighted at `ref`.
+constexpr int MAX_SPLITS = 128;      // pieces at most
 constexpr int PREFIX_TOO = 1 << 30;  // in `where`: the join adds them
 __device__ __forceinline__ float prefix_max(const AttnArgs& a, int h, int64_t row, float m) {
   const float* ml = prefix_ml(a);
+#pragma unroll 8
   for (int i = 0; i < a.splits; ++i) m = fmaxf(m, ml[2 * prefix_row(a, i, h, row)]);
   return m;
 }
@@ -503,6 +505,15 @@ __device__ __forceinline__ void add_prefix(const AttnArgs& a, int h, int64_t row
     l += w * ml[2 * r + 1];
     v += w * *(const float4_t*)(a.prefix_sums + r * a.d + c);
   }
+}
+
+// Four values of a row's pieces `first`, first + step, .. by their weights.
+__device__ __forceinline__ float4_t prefix_values(const AttnArgs& a, int h, int64_t row, int c, const float* w, int first,
+                                                  int step) {
+  float4_t v = {0, 0, 0, 0};
+#pragma unroll 8
+  for (int i = first; i < a.splits; i += step) v += w[i] * *(const float4_t*)(a.prefix_sums + prefix_row(a, i, h, row) * a.d + c);
+  return v;
 }
 
 template <int OUT>

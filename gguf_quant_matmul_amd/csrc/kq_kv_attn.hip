@@ -84,6 +84,13 @@ __global__ __launch_bounds__(256) void attn_join_kernel(AttnArgs a) {
 // tile, when a batch holds both
 constexpr int FEW_ROWS = 32;
 
+static void plan_workspace(AttnPlan& p, int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d) {
+  const int64_t many = (int64_t)p.many_wgs * kv_heads * 2 * attn_prompt_rows(d), few = (int64_t)p.few_wgs * kv_heads * 32;
+  p.few_at = many * (d + 2) * 4;
+  p.where_at = p.few_at + few * (d + 2) * 4;
+  p.bytes = many + few > 0 ? p.where_at + tokens * q_heads * 8 : 0;
+}
+
 AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
                    int64_t max_kv, int64_t window) {
   AttnPlan p;
@@ -132,11 +139,28 @@ AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_h
                                   : (rounds - each) * (full - fresh) + (n_seqs > 1 ? 0.3 * full : 0.);
     if (saved > (each < 1 ? 12 : 24)) p.many_wgs = (int)(256 / kv_heads);
   }
-  const int64_t many = (int64_t)p.many_wgs * kv_heads * 2 * tile, few = (int64_t)p.few_wgs * kv_heads * 32;
-  p.few_at = many * (d + 2) * 4;
-  p.where_at = p.few_at + few * (d + 2) * 4;
-  p.bytes = many + few > 0 ? p.where_at + tokens * q_heads * 8 : 0;
+  plan_workspace(p, tokens, q_heads, kv_heads, d);
   return p;
+}
+
+// A plan's 16-row tiles where their rows see at most `seen` keys, far fewer
+// than the requests may hold (a window, the keys behind a prefix): the tiles are
+// then of about one size, and a workgroup to each beats even shares, whose
+// workgroups hold pieces of two tiles and whose sums are joined, but where few
+// tiles of many steps leave CUs idle: up to half as many steps as tiles,
+// 16 at least, 128 at most.  (8 kv heads of 128, groups of 4, a window of 2000:
+// 32 requests 22 us against 32, 64 39 against 51; 8 requests, 1000: 13.4
+// against 16.2; 4000: 31 against 21.5.)  Eight waves to each where every one
+// has a CU, four where they share (64 requests, a window of 2000: 39 us
+// against 44).
+void plan_tiles(AttnPlan& p, int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t seen) {
+  const int64_t steps = (seen + STEP - 1) / STEP, tiles = p.few_tiles * kv_heads;
+  const int64_t most = tiles / 2 < 16 ? 16 : tiles / 2 > 128 ? 128 : tiles / 2;
+  if (p.few_wgs > 0 && steps <= most) {
+    p.few_wgs = 0;
+    plan_workspace(p, tokens, q_heads, kv_heads, d);
+  }
+  if (p.few_wgs == 0) p.more_waves = tiles <= (d > 128 ? 128 : 256) && seen > STEP * WAVES;
 }
 
 template <bool PREFIX>

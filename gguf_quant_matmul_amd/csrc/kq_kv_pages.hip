@@ -132,8 +132,12 @@ __global__ __launch_bounds__(FORK_THREADS) void kv_fork_kernel(
 // ---- free -------------------------------------------------------------------
 //
 // One launch takes every given entry off its page's count; the second collects
-// the pages whose count fell below 0, in the order of their ids, by one
-// workgroup: the count of the list's new head wants all of them first.
+// the pages whose count fell below 0 in the order of their ids, by one
+// workgroup: where the first of them goes wants all of them counted.  Its
+// threads read 32 counts each at once, and again for the second pass only
+// where there are more.  Both are bound by latency.  (One launch for both,
+// its one workgroup taking the entries off first: 14.2 us against 9.9 for 5
+// of 64 requests.)
 constexpr int COLLECT_THREADS = 1024, COLLECT_WAVES = COLLECT_THREADS / 64;
 
 __global__ __launch_bounds__(256) void kv_release_kernel(const int32_t* __restrict__ first, const int32_t* __restrict__ last,
@@ -145,6 +149,7 @@ __global__ __launch_bounds__(256) void kv_release_kernel(const int32_t* __restri
   j0 = j0 < 0 ? 0 : j0;
   j1 = j1 > width ? width : j1;
   const int32_t* row = table + (int64_t)s * width;
+#pragma unroll 4
   for (int64_t j = j0 + (int64_t)blockIdx.y * 64 + lane; j < j1; j += (int64_t)gridDim.y * 64) {
     const int32_t id = row[j];
     if (id >= 0 && id < pages) atomicSub(refs + id, 1);
@@ -156,18 +161,24 @@ __global__ __launch_bounds__(COLLECT_THREADS) void kv_collect_kernel(int32_t* __
                                                                      const int32_t* __restrict__ free_head,
                                                                      int32_t* __restrict__ head_out,
                                                                      uint32_t* __restrict__ status) {
-  constexpr int AHEAD = 8;
+  constexpr int AHEAD = 32;
   __shared__ uint32_t counts[COLLECT_WAVES], overs[COLLECT_WAVES];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  // a wave takes a run of pages, 64 * AHEAD at a time
-  const int64_t run = (pages + COLLECT_WAVES * 64 * AHEAD - 1) / (COLLECT_WAVES * 64 * AHEAD) * (64 * AHEAD);
-  const int64_t p0 = wave * run, p1 = p0 + run < pages ? p0 + run : pages;
   const int64_t head = free_head[0];
+  // a wave takes a run of pages
+  const int64_t run = ((pages + COLLECT_WAVES - 1) / COLLECT_WAVES + 63) & ~(int64_t)63;
+  const int64_t p0 = wave * run, p1 = p0 + run < pages ? p0 + run : pages;
+  int32_t v[AHEAD];
+  const auto load = [&](int64_t p) {
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int64_t q = p + i * 64 + lane;
+      v[i] = q < p1 ? refs[q] : 0;
+    }
+  };
   uint32_t mine = 0, over = 0;
   for (int64_t p = p0; p < p1; p += 64 * AHEAD) {
-    int32_t v[AHEAD];
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) v[i] = p + i * 64 + lane < p1 ? refs[p + i * 64 + lane] : 0;
+    load(p);
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       mine += v[i] < 0 ? 1u : 0u;
@@ -196,9 +207,7 @@ __global__ __launch_bounds__(COLLECT_THREADS) void kv_collect_kernel(int32_t* __
   if (mine == 0) return;
   int64_t at = head - total + before;  // place of the wave's next page
   for (int64_t p = p0; p < p1; p += 64 * AHEAD) {
-    int32_t v[AHEAD];
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) v[i] = p + i * 64 + lane < p1 ? refs[p + i * 64 + lane] : 0;
+    if (run > 64 * AHEAD) load(p);
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       const uint64_t dead = __ballot(v[i] < 0);

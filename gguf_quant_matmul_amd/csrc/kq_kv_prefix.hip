@@ -12,6 +12,7 @@ PrefixPlan prefix_plan(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_
   const int64_t at_once = f.prompt ? 256 : d <= 64 ? 1024 : 512, least = 4;
   int64_t n = at_once / (f.tiles * kv_heads);
   n = n > steps / least ? steps / least : n;
+  n = n > MAX_SPLITS ? MAX_SPLITS : n;
   f.splits = n < 1 ? 1 : (int)n;
   f.bytes = (f.splits * tokens * q_heads * (d + 2) * 4 + 15) & ~(int64_t)15;
   return f;

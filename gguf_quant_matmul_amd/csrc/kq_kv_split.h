@@ -72,6 +72,10 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
   constexpr int REGION = region_bytes<NB>();
   __shared__ __attribute__((aligned(16))) uint8_t lds[WAVES * REGION];
   __shared__ float merge_m[WAVES][16], merge_l[WAVES][16];
+  // of a shared prefix: its pieces' weights, each row's maximum and sum; parts of the sums
+  constexpr int PRE = M == TAIL ? 16 : 1;
+  __shared__ float pre_w[PRE][M == TAIL ? MAX_SPLITS : 1], pre_m[PRE], pre_l[PRE];
+  __shared__ float4_t pre_part[M == TAIL ? 64 * WAVES : 1];
   const int lane = threadIdx.x & 63, col = lane & 15, g = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = blockIdx.x, wg = blockIdx.y + gridDim.y * blockIdx.z;
@@ -324,6 +328,47 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
         merge_m[wave][mcol] = sums_at(m, factor);
         merge_l[wave][mcol] = l4[0];
       }
+      const bool with_prefix = M == TAIL && keys.lo > 0 && pieces == 1;
+      const int64_t prow = (int64_t)sq.row0 * a.group + r0;  // the tile's rows among the prefix's sums
+      int parts = 1;  // threads to a value's pieces
+      if constexpr (M == TAIL) {
+        const int live_rows = rows - r0 < 16 ? rows - r0 : 16, slots = live_rows * (D / 4);
+        if (with_prefix) {
+          // weights of the prefix's pieces at their own maximum, a lane to a piece
+          for (int r = wave; r < live_rows; r += WAVES) {
+            const float* ml = prefix_ml(a);
+            float pm[MAX_SPLITS / 64], pl[MAX_SPLITS / 64], mx = NEG_INF, l = 0.f;
+#pragma unroll
+            for (int i = 0; i < MAX_SPLITS / 64; ++i) {
+              const int piece = i * 64 + (tid & 63);
+              const bool some = piece < a.splits;
+              const int64_t at = 2 * prefix_row(a, some ? piece : 0, h, prow + r);
+              pm[i] = some ? ml[at] : NEG_INF;
+              pl[i] = some ? ml[at + 1] : 0.f;
+              mx = fmaxf(mx, pm[i]);
+            }
+#pragma unroll
+            for (int o2 = 32; o2 > 0; o2 >>= 1) mx = fmaxf(mx, __shfl_xor(mx, o2, 64));
+            const float ref = mx == NEG_INF ? 0.f : mx;
+#pragma unroll
+            for (int i = 0; i < MAX_SPLITS / 64; ++i) {
+              const float w = __builtin_amdgcn_exp2f(pm[i] - ref);
+              pre_w[r][i * 64 + (tid & 63)] = w;
+              l += w * pl[i];
+            }
+#pragma unroll
+            for (int o2 = 32; o2 > 0; o2 >>= 1) l += __shfl_xor(l, o2, 64);
+            pre_m[r] = mx;
+            pre_l[r] = l;
+          }
+          parts = slots >= 64 * WAVES ? 1 : 64 * WAVES / slots;
+          if (parts > 1) {
+            __syncthreads();
+            const int part = tid / slots, slot = tid - part * slots, r = slot / (D / 4), c = slot % (D / 4) * 4;
+            if (part < parts) pre_part[tid] = prefix_values(a, h, prow + r, c, pre_w[r], part, parts);
+          }
+        }
+      }
       __syncthreads();
 #pragma unroll
       for (int k = 0; k < (16 * D / 4 + 64 * WAVES - 1) / (64 * WAVES); ++k) {
@@ -332,9 +377,9 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
         float mx = merge_m[0][r];
 #pragma unroll
         for (int w = 1; w < WAVES; ++w) mx = fmaxf(mx, merge_m[w][r]);
-        const bool with_prefix = M == TAIL && keys.lo > 0 && pieces == 1;
-        const int64_t prow = (int64_t)sq.row0 * a.group + r0 + r;  // among the prefix's sums
-        if (with_prefix) mx = prefix_max(a, h, prow, mx);
+        if constexpr (M == TAIL) {
+          if (with_prefix) mx = fmaxf(mx, pre_m[r]);
+        }
         const float ref = mx == NEG_INF ? 0.f : mx;
         float l = 0.f;
         float4_t v = {0, 0, 0, 0};
@@ -344,9 +389,20 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
           l += f * merge_l[w][r];
           v += f * *(const float4_t*)((const float*)(lds + w * REGION) + r * (D + 4) + c);
         }
-        if (with_prefix) add_prefix(a, h, prow, c, ref, l, v);
+        if constexpr (M == TAIL) {
+          if (with_prefix) {
+            const float f = __builtin_amdgcn_exp2f(pre_m[r] - ref);
+            l += f * pre_l[r];
+            if (parts > 1) {
+              const int slots = (rows - r0 < 16 ? rows - r0 : 16) * (D / 4);
+              for (int p = 0; p < parts; ++p) v += f * pre_part[p * slots + i];
+            } else {
+              v += f * prefix_values(a, h, prow + r, c, pre_w[r], 0, 1);
+            }
+          }
+        }
         if constexpr (M == FLAT) {
-          const int64_t pr = prefix_row(a, split, h, prow);
+          const int64_t pr = prefix_row(a, split, h, prow + r);
           store4<0>(a.prefix_sums, pr * D + c, v);
           if (c == 0) {
             float* ml = prefix_ml(a) + 2 * pr;

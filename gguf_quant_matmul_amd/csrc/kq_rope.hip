@@ -73,39 +73,41 @@ __device__ __forceinline__ void sin_cos(double angle, float& s, float& c) {
 }
 
 // V values a lane and load: 8, or 4 where rot / 2 is no multiple of 8.  A unit
-// is V pairs of one head, or (rows written apart) V of the values behind rot.
+// is V values of one head that make V / 2 pairs of neighbours, V of the lower half with V of the upper one, or
+// (rows written apart) V of the values behind rot.  The units that turn come
+// first, so that few waves hold both kinds.
 template <int T, bool PAIRS, int V>
-__global__ __launch_bounds__(64 * ROPE_WAVES) void rope_kernel(RopeArgs a, int slices, uint32_t per, uint32_t inv_per) {
+__global__ __launch_bounds__(64 * ROPE_WAVES) void rope_kernel(RopeArgs a, int slices, uint32_t turn, uint32_t inv_turn,
+                                                               uint32_t keep, uint32_t inv_keep) {
   typedef typename Elem<T>::type E;
   typedef E EV __attribute__((ext_vector_type(V)));
+  constexpr int F = PAIRS ? V / 2 : V;  // frequencies of a unit
   __shared__ __attribute__((aligned(16))) float cosines[ROPE_WAVES][128], sines[ROPE_WAVES][128];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t item = blockIdx.x * ROPE_WAVES + wave;
   const int tok = (int)(item / (uint32_t)slices), slice = (int)(item - (uint32_t)tok * (uint32_t)slices);
   const bool some = tok < a.tokens;
-  const uint32_t units = (uint32_t)(a.hq + a.hkv) * per, turn = a.rot / (2 * V);
+  const uint32_t heads = a.hq + a.hkv, turning = heads * turn, units = turning + heads * keep;
   const int half = a.rot / 2;
 
   struct Unit {
     EV lo, hi;
-    const E* in;
     E* out;
-    int c, on;  // (on: 1 a pair, 2 values behind rot)
+    int c, on;  // (on: 1 turned, 2 carried over)
   };
   const auto load = [&](uint32_t u, Unit& x) {
-    const uint32_t head = per == 1 ? u : __umulhi(u, inv_per);
-    x.c = (int)(u - head * per);
+    const bool turns = u < turning;
+    const uint32_t n = turns ? u : u - turning, per = turns ? turn : keep;
+    const uint32_t head = per == 1 ? n : __umulhi(n, turns ? inv_turn : inv_keep);
     const bool is_q = head < (uint32_t)a.hq;
     const int64_t h = is_q ? head : head - a.hq;
-    x.in = (const E*)(is_q ? a.q : a.k) + tok * (is_q ? a.q_stride : a.k_stride) + h * a.d;
-    x.out = (E*)(is_q ? a.q_out : a.k_out) + tok * (is_q ? a.q_out_stride : a.k_out_stride) + h * a.d;
-    x.on = !some || u >= units ? 0 : x.c < (int)turn ? 1 : (is_q ? a.copy_q : a.copy_k) ? 2 : 0;
-    if (x.on == 1) {
-      x.lo = *(const EV*)(x.in + (PAIRS ? 2 * x.c * V : x.c * V));
-      x.hi = *(const EV*)(x.in + (PAIRS ? 2 * x.c * V + V : half + x.c * V));
-    } else if (x.on == 2) {
-      x.lo = *(const EV*)(x.in + a.rot + (x.c - (int)turn) * V);
-    }
+    x.c = (int)(n - head * per);
+    x.on = !some || u >= units ? 0 : turns ? 1 : (is_q ? a.copy_q : a.copy_k) ? 2 : 0;
+    const int at = turns ? x.c * V : a.rot + x.c * V;
+    const E* in = (const E*)(is_q ? a.q : a.k) + tok * (is_q ? a.q_stride : a.k_stride) + h * a.d + at;
+    x.out = (E*)(is_q ? a.q_out : a.k_out) + tok * (is_q ? a.q_out_stride : a.k_out_stride) + h * a.d + at;
+    if (x.on) x.lo = *(const EV*)in;
+    if (!PAIRS && x.on == 1) x.hi = *(const EV*)(in + half);
   };
   Unit x[ROPE_AHEAD];
   uint32_t u = (uint32_t)slice * 64 + lane;
@@ -132,30 +134,29 @@ __global__ __launch_bounds__(64 * ROPE_WAVES) void rope_kernel(RopeArgs a, int s
 
   const auto store = [&](Unit& x) {
     if (x.on == 1) {
-      const float* cs = &cosines[wave][x.c * V];
-      const float* sn = &sines[wave][x.c * V];
+      const float* cs = &cosines[wave][x.c * F];
+      const float* sn = &sines[wave][x.c * F];
       EV lo, hi;
       if constexpr (PAIRS) {
 #pragma unroll
-        for (int j = 0; j < V / 2; ++j) {
-          const float r = (float)x.lo[2 * j], i = (float)x.lo[2 * j + 1], R = (float)x.hi[2 * j], I = (float)x.hi[2 * j + 1];
+        for (int j = 0; j < F; ++j) {
+          const float r = (float)x.lo[2 * j], i = (float)x.lo[2 * j + 1];
           lo[2 * j] = (E)(r * cs[j] - i * sn[j]);
           lo[2 * j + 1] = (E)(i * cs[j] + r * sn[j]);
-          hi[2 * j] = (E)(R * cs[V / 2 + j] - I * sn[V / 2 + j]);
-          hi[2 * j + 1] = (E)(I * cs[V / 2 + j] + R * sn[V / 2 + j]);
         }
+        *(EV*)x.out = lo;
       } else {
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
+        for (int j = 0; j < F; ++j) {
           const float r = (float)x.lo[j], i = (float)x.hi[j];
           lo[j] = (E)(r * cs[j] - i * sn[j]);
           hi[j] = (E)(i * cs[j] + r * sn[j]);
         }
+        *(EV*)x.out = lo;
+        *(EV*)(x.out + half) = hi;
       }
-      *(EV*)(x.out + (PAIRS ? 2 * x.c * V : x.c * V)) = lo;
-      *(EV*)(x.out + (PAIRS ? 2 * x.c * V + V : half + x.c * V)) = hi;
     } else if (x.on == 2) {
-      *(EV*)(x.out + a.rot + (x.c - (int)turn) * V) = x.lo;
+      *(EV*)x.out = x.lo;
     }
   };
   for (;;) {
@@ -170,14 +171,16 @@ __global__ __launch_bounds__(64 * ROPE_WAVES) void rope_kernel(RopeArgs a, int s
 
 template <int T, bool PAIRS, int V>
 hipError_t launch(const RopeArgs& a, hipStream_t s) {
-  const uint32_t per = (uint32_t)(a.rot / (2 * V) + (a.copy_q || a.copy_k ? (a.d - a.rot) / V : 0));
-  const int64_t rounds = ((int64_t)(a.hq + a.hkv) * per + 63) / 64;  // of a token's wave
+  const uint32_t turn = (uint32_t)(a.rot / (PAIRS ? V : 2 * V));
+  const uint32_t keep = a.copy_q || a.copy_k ? (uint32_t)((a.d - a.rot) / V) : 0u;
+  const int64_t rounds = ((int64_t)(a.hq + a.hkv) * (turn + keep) + 63) / 64;  // of a token's wave
   int64_t slices = 4096 / a.tokens;
   slices = slices > rounds ? rounds : slices < 1 ? 1 : slices;
   const int64_t wgs = (a.tokens * slices + ROPE_WAVES - 1) / ROPE_WAVES;
-  // x / per by the high half of x * ceil(2^32 / per): exact for x below 2^19 and per in 2..64
-  const uint32_t inv = (uint32_t)((((uint64_t)1 << 32) + per - 1) / per);
-  hipLaunchKernelGGL((rope_kernel<T, PAIRS, V>), dim3((unsigned)wgs), dim3(64 * ROPE_WAVES), 0, s, a, (int)slices, per, inv);
+  // x / n by the high half of x * ceil(2^32 / n): exact for x below 2^19 and n in 2..64
+  const auto inv = [](uint32_t n) { return n > 1 ? (uint32_t)((((uint64_t)1 << 32) + n - 1) / n) : 0u; };
+  hipLaunchKernelGGL((rope_kernel<T, PAIRS, V>), dim3((unsigned)wgs), dim3(64 * ROPE_WAVES), 0, s, a, (int)slices, turn,
+                     inv(turn), keep, inv(keep));
   return hipGetLastError();
 }
 
