@@ -511,8 +511,10 @@ __device__ __forceinline__ void add_prefix(const AttnArgs& a, int h, int64_t row
 __device__ __forceinline__ float4_t prefix_values(const AttnArgs& a, int h, int64_t row, int c, const float* w, int first,
                                                   int step) {
   float4_t v = {0, 0, 0, 0};
+  const float* from = a.prefix_sums + prefix_row(a, first, h, row) * a.d + c;
+  const int64_t stride = prefix_row(a, step, 0, 0) * a.d;
 #pragma unroll 8
-  for (int i = first; i < a.splits; i += step) v += w[i] * *(const float4_t*)(a.prefix_sums + prefix_row(a, i, h, row) * a.d + c);
+  for (int i = first; i < a.splits; i += step, from += stride) v += w[i] * *(const float4_t*)from;
   return v;
 }
 

@@ -170,23 +170,22 @@ __global__ __launch_bounds__(COLLECT_THREADS) void kv_collect_kernel(int32_t* __
   const int64_t p0 = wave * run, p1 = p0 + run < pages ? p0 + run : pages;
   int32_t v[AHEAD];
   const auto load = [&](int64_t p) {
+    const int left = p1 - p < 64 * AHEAD ? (int)(p1 - p) : 64 * AHEAD;  // pages from p on
+    const int32_t* at = refs + p;
 #pragma unroll
-    for (int i = 0; i < AHEAD; ++i) {
-      const int64_t q = p + i * 64 + lane;
-      v[i] = q < p1 ? refs[q] : 0;
-    }
+    for (int i = 0; i < AHEAD; ++i) v[i] = i * 64 + lane < left ? at[i * 64 + lane] : 0;
   };
-  uint32_t mine = 0, over = 0;
+  uint32_t mine = 0;  // (the same in all lanes)
+  int32_t least = 0;
   for (int64_t p = p0; p < p1; p += 64 * AHEAD) {
     load(p);
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      mine += v[i] < 0 ? 1u : 0u;
-      over |= v[i] < -1 ? 1u : 0u;
+      mine += __popcll(__ballot(v[i] < 0));
+      least = v[i] < least ? v[i] : least;
     }
   }
-  mine = __builtin_amdgcn_readlane(wave_scan(mine), 63);
-  over = __ballot(over) ? 1u : 0u;
+  const uint32_t over = __ballot(least < -1) ? 1u : 0u;
   if (lane == 0) {
     counts[wave] = mine;
     overs[wave] = over;
@@ -211,8 +210,9 @@ __global__ __launch_bounds__(COLLECT_THREADS) void kv_collect_kernel(int32_t* __
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       const uint64_t dead = __ballot(v[i] < 0);
+      if (!dead) continue;
       if (v[i] < 0) {
-        const int64_t page = p + i * 64 + lane, place = at + __popcll(dead & ((1ull << lane) - 1));
+        const int64_t page = p + i * 64 + lane, place = at + __popcll(dead & (((uint64_t)1 << lane) - 1));
         refs[page] = 0;
         if (place >= 0 && place < n_free) free_pages[place] = (int32_t)page;
       }

@@ -59,8 +59,10 @@ constexpr int region_bytes() {
   return Stage<NB>::BYTES > m ? Stage<NB>::BYTES : m;
 }
 
-template <int NB, int WAVES, int M>
-__global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel(AttnArgs a) {
+// SHARE: the workgroup takes an even share of all requests' steps, or (a.few_wgs =
+// 0) one tile; else one tile, with the registers that the shares need free.
+template <int NB, int WAVES, int M, bool SHARE>
+__global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : NB <= 4 && !SHARE && WAVES == 4 ? 3 : 2) void attn_split_kernel(AttnArgs a) {
   constexpr int D = 32 * NB;
   constexpr int DT = D / 16;  // 16-value tiles of O^T
   // 16-key groups are whole numbers of 16-byte pieces to a load of the wave:
@@ -83,14 +85,15 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
   // the workgroup's part of all steps, or (few_wgs = 0) all of tile wg
   int s = wg, sub = 0;
   Share share;
+  const int few_wgs = SHARE ? a.few_wgs : 0;
   int split = 0;
   if constexpr (M == FLAT) {
     s = 0;
     sub = wg / a.splits;
     split = wg - sub * a.splits;
-  } else if (a.few_wgs == 0) {
+  } else if (few_wgs == 0) {
     if (a.one_tile ? s >= a.n_seqs : !find_tile(a, wg, 16, 0, a.few_rows, s, sub)) return;
-  } else if (!find_share<16, M>(a, wg, a.few_wgs, WAVES, 0, a.few_rows, s, sub, share)) {
+  } else if (!find_share<16, M>(a, wg, few_wgs, WAVES, 0, a.few_rows, s, sub, share)) {
     return;
   }
 
@@ -98,7 +101,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
     const Seq sq = M == FLAT ? flat_seq(a) : load_seq(a, s);
     const int rows = sq.n * a.group;
     if (sub * 16 >= rows || (M != FLAT && rows > a.few_rows)) {  // (a request with one tile may have none, or more)
-      if (M == FLAT || a.few_wgs == 0 || ++s >= a.n_seqs) return;
+      if (M == FLAT || few_wgs == 0 || ++s >= a.n_seqs) return;
       sub = -1;
       continue;
     }
@@ -109,7 +112,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
     if constexpr (M == FLAT) {
       st0 = (int)((int64_t)steps * split / a.splits);
       st1 = (int)((int64_t)steps * (split + 1) / a.splits);
-    } else if (a.few_wgs > 0) {
+    } else if (few_wgs > 0) {
       if (share.x >= share.x1) return;
       if (!take_steps<16>(share, steps, st0, st1, first, pieces)) continue;
     }
@@ -334,7 +337,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
       if constexpr (M == TAIL) {
         const int live_rows = rows - r0 < 16 ? rows - r0 : 16, slots = live_rows * (D / 4);
         if (with_prefix) {
-          // weights of the prefix's pieces at their own maximum, a lane to a piece
+          // weights of the prefix's pieces at their own maximum, a (tid & 63) to a piece
           for (int r = wave; r < live_rows; r += WAVES) {
             const float* ml = prefix_ml(a);
             float pm[MAX_SPLITS / 64], pl[MAX_SPLITS / 64], mx = NEG_INF, l = 0.f;
@@ -417,7 +420,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
           const int64_t pr = (((int64_t)wg * a.hkv + h) * 2 + (st0 == 0 ? 1 : 0)) * 16 + r;
           store4<0>(a.few, pr * D + c, v);
           if (c == 0) {
-            float* ml = a.few + (int64_t)a.few_wgs * a.hkv * 32 * D + 2 * pr;
+            float* ml = a.few + (int64_t)few_wgs * a.hkv * 32 * D + 2 * pr;
             ml[0] = mx;
             ml[1] = l;
           }
@@ -425,13 +428,13 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : 2) void attn_split_kernel
       }
       __syncthreads();  // the next tile reuses the LDS
     }
-    if (M == FLAT || (a.few_wgs == 0 && !a.one_tile)) return;
+    if (M == FLAT || (few_wgs == 0 && !a.one_tile)) return;
   }
 }
 
-template <int M>
-hipError_t launch_split(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
-  const int64_t n = M == FLAT ? p.few_tiles * a.splits : a.few_wgs > 0 ? a.few_wgs : p.few_tiles;
+template <int M, bool SHARE>
+hipError_t launch_tiles(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+  const int64_t n = M == FLAT ? p.few_tiles * a.splits : SHARE && a.few_wgs > 0 ? a.few_wgs : p.few_tiles;
   const int64_t gy = n < 32768 ? n : 32768;
   const dim3 grid((unsigned)a.hkv, (unsigned)gy, (unsigned)((n + gy - 1) / gy));
   const auto go = [&](auto four, auto eight) {
@@ -439,16 +442,23 @@ hipError_t launch_split(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
     else hipLaunchKernelGGL(four, grid, dim3(64 * WAVES), 0, s, a);
   };
   switch (a.d / 32) {
-    case 1: go(attn_split_kernel<1, WAVES, M>, attn_split_kernel<1, MORE_WAVES, M>); break;
-    case 2: go(attn_split_kernel<2, WAVES, M>, attn_split_kernel<2, MORE_WAVES, M>); break;
-    case 3: go(attn_split_kernel<3, WAVES, M>, attn_split_kernel<3, MORE_WAVES, M>); break;
-    case 4: go(attn_split_kernel<4, WAVES, M>, attn_split_kernel<4, MORE_WAVES, M>); break;
-    case 5: go(attn_split_kernel<5, WAVES, M>, attn_split_kernel<5, MORE_WAVES, M>); break;
-    case 6: go(attn_split_kernel<6, WAVES, M>, attn_split_kernel<6, MORE_WAVES, M>); break;
-    case 7: go(attn_split_kernel<7, WAVES, M>, attn_split_kernel<7, MORE_WAVES, M>); break;
-    default: go(attn_split_kernel<8, WAVES, M>, attn_split_kernel<8, MORE_WAVES, M>); break;
+    case 1: go(attn_split_kernel<1, WAVES, M, SHARE>, attn_split_kernel<1, MORE_WAVES, M, SHARE>); break;
+    case 2: go(attn_split_kernel<2, WAVES, M, SHARE>, attn_split_kernel<2, MORE_WAVES, M, SHARE>); break;
+    case 3: go(attn_split_kernel<3, WAVES, M, SHARE>, attn_split_kernel<3, MORE_WAVES, M, SHARE>); break;
+    case 4: go(attn_split_kernel<4, WAVES, M, SHARE>, attn_split_kernel<4, MORE_WAVES, M, SHARE>); break;
+    case 5: go(attn_split_kernel<5, WAVES, M, SHARE>, attn_split_kernel<5, MORE_WAVES, M, SHARE>); break;
+    case 6: go(attn_split_kernel<6, WAVES, M, SHARE>, attn_split_kernel<6, MORE_WAVES, M, SHARE>); break;
+    case 7: go(attn_split_kernel<7, WAVES, M, SHARE>, attn_split_kernel<7, MORE_WAVES, M, SHARE>); break;
+    default: go(attn_split_kernel<8, WAVES, M, SHARE>, attn_split_kernel<8, MORE_WAVES, M, SHARE>); break;
   }
   return hipGetLastError();
+}
+
+template <int M>
+hipError_t launch_split(const AttnArgs& a, const AttnPlan& p, hipStream_t s) {
+  if constexpr (M == PLAIN) return launch_tiles<M, true>(a, p, s);
+  else if constexpr (M == FLAT) return launch_tiles<M, false>(a, p, s);
+  else return a.few_wgs > 0 ? launch_tiles<M, true>(a, p, s) : launch_tiles<M, false>(a, p, s);
 }
 
 }  // namespace
