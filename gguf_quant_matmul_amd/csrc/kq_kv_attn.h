@@ -106,6 +106,14 @@ __device__ __forceinline__ bool sees(const AttnArgs& a, int k, int p) {
   if constexpr (M == PLAIN) return k <= p && (a.window <= 0 || k > p - a.window);
   return k <= p;
 }
+// Whether no row from position p0 on sees key k, one between sinks and window:
+// its page may be another request's or hold anything, NaN included.
+template <int M>
+__device__ __forceinline__ bool hidden(const AttnArgs& a, int k, int p0) {
+  if constexpr (M != SINKS) return false;
+  const int n = p0 - a.window - a.sinks + 1;  // of them
+  return (uint32_t)(k - a.sinks) < (uint32_t)(n > 0 ? n : 0);
+}
 // Whether some row of positions p0 .. p1 does not see all of 64 keys (of the
 // request's), and whether any of them sees one.
 template <int M>

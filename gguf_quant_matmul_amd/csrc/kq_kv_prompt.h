@@ -161,7 +161,9 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
         x.scale[k] = (uint16_t)ld_u16(a.vc + scales + 2 * (u - NB));
       }
     };
-    const auto stage_v = [&](const Pieces& x, int id) {
+    const int tile_p0 = pos_of<M>(sq, token_of(a, r0));
+    const auto stage_v = [&](const Pieces& x, int id, int st) {
+      const bool good = id >= 0 && !hidden<M>(a, step_base<M>(keys, st) + lane, tile_p0);
 #pragma unroll
       for (int k = 0; k < T::UNITS; ++k) {
         const int u = wave + PW * k;
@@ -170,7 +172,7 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
         uint16_t* scales = (uint16_t*)(rows16 + STEP * 16);
         *(u32x4*)(rows16 + (((lane >> 2) & 3) * 16 + g * 4 + (lane & 3)) * 16) = x.raw[k];
         // bytes behind the last key are anything, NaN included: their values enter as 0 * code
-        scales[((lane >> 2) & 3) * 16 + (g >> 1) * 8 + (lane & 3) * 2 + (g & 1)] = (uint16_t)(id >= 0 ? x.scale[k] : 0);
+        scales[((lane >> 2) & 3) * 16 + (g >> 1) * 8 + (lane & 3) * 2 + (g & 1)] = (uint16_t)(good ? x.scale[k] : 0);
       }
     };
     const auto unpack = [&](int kb, int vb, const Pieces& y) {
@@ -272,12 +274,12 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
       fetch_k(st0 + 1, id[1], x1);
       fetch_v(st0 + 1, id[1], x1);
       fetch_v(st0 + 2, id[2], x);
-      stage_v(x0, id[0]);
+      stage_v(x0, id[0], st0);
       unpack(0, 0, x0);
-      stage_v(x1, id[1]);
+      stage_v(x1, id[1], st0 + 1);
       if (late) {
         unpack(1, 1, x1);
-        stage_v(x, id[2]);
+        stage_v(x, id[2], st0 + 2);
         fetch_k(st0 + 2, id[2], x);
         fetch_v(st0 + 3, id[3], x);
         oks |= group_bits(id[3]) << 12;
@@ -384,7 +386,7 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
       int vn = vb + 1 + late;
       vn = vn >= T::VB ? vn - T::VB : vn;
       unpack((round + 1) & 1, vn, x);
-      stage_v(x, id_v);
+      stage_v(x, id_v, st0 + round + 2);
       id_k = id_v;
       id_v = checked(st0 + round + 3, id_next);
       id_next = page_id(st0 + round + 4);

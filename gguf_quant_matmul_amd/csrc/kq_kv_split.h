@@ -186,7 +186,7 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : NB <= 4 && !SHARE && WAVE
           *(u32x4*)(vcodes + lr * Stage<NB>::ROW + 16 * b) = f.vw[i];
         }
         // bytes behind the last key are anything, NaN included: their values enter as 0 * code
-        const bool good = ((ok >> g) & 1u) && base + lane < keys.end;
+        const bool good = ((ok >> g) & 1u) && base + lane < keys.end && !hidden<M>(a, base + lane, p0);
         const int pos = ((lane >> 2) & 3) * 16 + (g >> 1) * 8 + (lane & 3) * 2 + (g & 1);
 #pragma unroll
         for (int b = 0; b < NB; ++b) vscales[b * 64 + pos] = (uint16_t)((good ? f.vs[b / 2] : 0u) >> (16 * (b & 1)));

@@ -96,20 +96,40 @@ def test_no_sinks_no_window(kq):
     _hold(c, _sinks(kq, c, 300, 500, "f32", max_new=40, max_kv=700), "all keys", "f32", window=300, sinks=500)
 
 
-@pytest.mark.parametrize("new, lens", [([1, 1], [3000, 900]), ([70, 1], [2000, 500])])
-def test_pages_between_sinks_and_window_are_not_read(kq, new, lens):
-    # their table entries name no pages; and pages full of NaN, where one is named, give nothing
-    page, window, sinks = 16, 200, 20
+@pytest.mark.parametrize("new, lens, max_kv", [([1, 1], [3000, 900], 3000), ([1, 1], [3000, 900], 500), ([70, 1], [2000, 500], 2000),
+                                               ([70, 40], [2000, 1500], 1 << 20)])
+@pytest.mark.parametrize("sinks", [4, 20, 64, 100])
+def test_pages_between_sinks_and_window_are_not_read(kq, new, lens, max_kv, sinks):
+    # their table entries name no pages, or one full of NaN
+    page, window = 16, 203
     c = _case(8, new, lens, 4, 2, 64, page)
-    want = _f64(_sinks(kq, c, window, sinks, max_new=max(new), max_kv=3000))
-    free = np.nonzero(~np.isin(np.arange(c["kc"].shape[0]), c["table"]))[0][0]  # (NaN scales)
-    for s, (m, n) in enumerate(zip(new, lens)):
-        a, b = 128 // page, (n - m - window + 1) // 64 * 64 // page
-        for fill in (-1, free, 1 << 30):
-            was = c["table"].copy()
-            c["table"][s, a:b] = fill
-            assert np.array_equal(_f64(_sinks(kq, c, window, sinks, max_new=max(new), max_kv=3000)), want)
-            c["table"] = was
+    want = _f64(_sinks(kq, c, window, sinks, max_new=max(new), max_kv=max_kv))
+    _hold(c, _sinks(kq, c, window, sinks, "f32", max_new=max(new), max_kv=max_kv), "whole table", "f32", window=window, sinks=sinks)
+    spare = np.nonzero(~np.isin(np.arange(c["kc"].shape[0]), c["table"]))[0][0]
+    assert np.isnan(kvcache.load(c["vc"], page, 64, [spare * page])).all()
+    was = c["table"].copy()
+    for fill in (-1, spare, 1 << 30):
+        for s, (m, n) in enumerate(zip(new, lens)):
+            c["table"][s, -(-sinks // page):(n - m - window + 1) // page] = fill
+        assert np.array_equal(_f64(_sinks(kq, c, window, sinks, max_new=max(new), max_kv=max_kv)), want)
+        c["table"] = was.copy()
+
+
+def test_sinks_need_no_more_workspace_than_attention(kq):
+    # the bytes that kq_kv_attention_workspace names are enough whatever window and sinks are
+    import torch
+
+    rng = np.random.default_rng(12)
+    for i in range(40):
+        n, kv, group, d = int(rng.integers(1, 20)), int(rng.choice([1, 2, 8])), int(rng.choice([1, 4, 7])), int(rng.choice([32, 128, 256]))
+        new = rng.integers(1, int(rng.choice([2, 30, 300])), n)
+        c = _case(i, new, new + 5, kv * group, kv, d, 16)
+        max_kv, window, sinks = (int(2 ** rng.uniform(0, 20)) for _ in range(3))
+        need = kq.kq_kv_attention_workspace(int(new.sum()), n, kv * group, kv, d, int(new.max()), max_kv)
+        ws = torch.empty(max(1, need), dtype=torch.uint8, device="cuda")
+        got = _sinks(kq, c, window, sinks, "f32", max_new=int(new.max()), max_kv=max_kv, workspace=ws)
+        if i % 8 == 0:
+            _hold(c, got, "in that workspace", "f32", window=window, sinks=sinks)
 
 
 # ---------------------------------------------------------------------------
@@ -215,6 +235,43 @@ def test_prefix_of_a_part_of_the_batch(kq):
     whole = _prefix(kq, c, "f16", max_new=5, max_kv=160)
     ref = _f64(whole)[4:11]
     assert np.abs(_f64(o)[4:11] - ref).max() <= 2.0 ** -9 * np.abs(ref).max()
+
+
+def test_prefix_pages_behind_32_bits(kq):
+    # the same rows in pages whose byte offsets pass 2^32
+    import torch
+
+    c = _shared(33, [1, 20, 1], [3, 40, 200], 4, 64, 64, 128, 64)
+    near = _prefix(kq, c, "f16", max_new=20, max_kv=460)
+    few, page_bytes = c["kc"].shape[0], c["kc"].shape[1] * c["kc"].shape[2]
+    pages = (1 << 32) // page_bytes + few + 3
+    kc, vc = (torch.zeros((pages, *x.shape[1:]), dtype=torch.uint8, device="cuda") for x in (c["kc"], c["vc"]))
+    kc[-few:], vc[-few:] = dev(c["kc"]), dev(c["vc"])
+    up = lambda t: _i32(np.where(np.asarray(t) >= 0, np.asarray(t) + pages - few, -1))
+    o, (q, cu, lens, _) = _args(c, "f16")
+    kq.kq_kv_attention_prefix("q4_0", q, cu, lens, up(c["table"]), up(c["prefix"]), kc, vc, 64, o, max_new=20, max_kv=460)
+    assert torch.equal(o, near)
+
+
+def test_two_calls_at_once(kq):
+    # prefix calls on two streams, a workspace each
+    import torch
+
+    cs = [_shared(40 + i, [1] * 9, list(range(1, 10)), 30, 8, 2, 64, 16) for i in range(2)]
+    sizes = 9, 9, 8, 2, 64, 480, 1, 489
+    want = [_prefix(kq, c, "f32", max_new=1, max_kv=489) for c in cs]
+    args = [_args(c, "f32") for c in cs]
+    more = [(_i32(c["prefix"]), dev(c["kc"]), dev(c["vc"])) for c in cs]
+    ws = [torch.empty(kq.kq_kv_attention_prefix_workspace(*sizes), dtype=torch.uint8, device="cuda") for _ in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for (o, a), m, w, st in zip(args, more, ws, streams):
+            with torch.cuda.stream(st):
+                kq.kq_kv_attention_prefix("q4_0", *a, *m, 16, o, max_new=1, max_kv=489, workspace=w)
+    torch.cuda.synchronize()
+    for (o, _), w in zip(args, want):
+        assert torch.equal(o, w)
 
 
 # ---------------------------------------------------------------------------
