@@ -26,6 +26,8 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
 // those of the forks before it.  Every workgroup sums over all forks itself
 // (a thread a strip, then one scan over the strips), so that one launch does;
 // then a wave copies a fork's row of page ids and counts their new holder.
+// Bound by latency (a launch, two dependent loads, the scan): 8 forks of 330
+// tokens 3.0 us, 256 of up to 8000 4.8.
 constexpr int FORK_THREADS = 256, FORK_WAVES = FORK_THREADS / 64;
 constexpr int FORK_MOST = 64;  // forks of a workgroup
 
@@ -136,8 +138,8 @@ __global__ __launch_bounds__(FORK_THREADS) void kv_fork_kernel(
 // workgroup: where the first of them goes wants all of them counted.  Its
 // threads read 32 counts each at once, and again for the second pass only
 // where there are more.  Both are bound by latency.  (One launch for both,
-// its one workgroup taking the entries off first: 14.2 us against 9.9 for 5
-// of 64 requests.)
+// its one workgroup taking the entries off first: 14.2 us against 10.6 for 5
+// of 64 requests.)  500 of 500 with 34000 pages take 13.0 us.
 constexpr int COLLECT_THREADS = 1024, COLLECT_WAVES = COLLECT_THREADS / 64;
 
 __global__ __launch_bounds__(256) void kv_release_kernel(const int32_t* __restrict__ first, const int32_t* __restrict__ last,
@@ -336,7 +338,8 @@ __global__ __launch_bounds__(256) void kv_renumber_kernel(Renumber r, const int3
 // ---- copy -------------------------------------------------------------------
 //
 // A workgroup copies pieces of 16 KB of one cache, all of a thread's loads
-// before its stores.
+// before its stores.  Bound by HBM: 2660 pages of 36 KB a cache, 393 MB, 81 us,
+// 4.8 TB/s, what a large copy reaches.
 constexpr int COPY_THREADS = 256, COPY_AHEAD = 4;
 constexpr int COPY_PIECE = COPY_THREADS * COPY_AHEAD * 16;
 
@@ -370,12 +373,16 @@ hipError_t launch_kv_fork(const int32_t* parents, const int32_t* children, const
                           int32_t* table, int64_t n_seqs, int64_t width, int32_t* refs, int64_t pages,
                           const int32_t* free_pages, int64_t n_free, const int32_t* free_head, int32_t* copy_src,
                           int32_t* copy_dst, int32_t* head_out, uint32_t* status, hipStream_t s) {
-  // four forks to a workgroup (one a wave); above 4096 more of them, so that
-  // the repeated sums stay small beside the rows
-  int64_t each = (n + 1023) / 1024;
+  // four forks to a workgroup (one a wave); above 1024 more of them, so that
+  // the repeated sums stay small beside the rows (256 forks 3.4 us with 4 to a
+  // workgroup, 5.8 with 16; 4096 46 with 4, 19 with 16, 28 with 64; 16384 340
+  // with 16, 107 with 64)
+  int64_t each = n / 256;
   each = each < 4 ? 4 : each > FORK_MOST ? FORK_MOST : each;
   const int64_t gx = n > 0 ? (n + each - 1) / each : 1;
-  int64_t gy = (width + 1023) / 1024;
+  // long rows are shared out: 512 entries to a wave (8 forks of 6250 entries
+  // 7.5 us in eight parts, 8.8 in seven, 39 in one)
+  int64_t gy = (width + 511) / 512;
   gy = gy < 1 ? 1 : gy > 64 ? 64 : gy;
   hipLaunchKernelGGL(kv_fork_kernel, dim3((unsigned)gx, (unsigned)gy), dim3(FORK_THREADS), 0, s, parents, children, lens,
                      (int)n, page_shift, table, (int)n_seqs, width, refs, pages, free_pages, n_free, free_head, copy_src,
@@ -387,7 +394,9 @@ hipError_t launch_kv_free(const int32_t* first, const int32_t* last, int64_t n_s
                           int32_t* refs, int64_t pages, int32_t* free_pages, int64_t n_free, const int32_t* free_head,
                           int32_t* head_out, uint32_t* status, hipStream_t s) {
   if (n_seqs > 0 && width > 0) {
-    int64_t gy = (width + 511) / 512;
+    // 256 entries of a row to a wave (8 requests of 6250 entries 11.2 us in
+    // thirteen parts, 12.7 in eight, 44 in one)
+    int64_t gy = (width + 255) / 256;
     gy = gy > 64 ? 64 : gy;
     hipLaunchKernelGGL(kv_release_kernel, dim3((unsigned)((n_seqs + 3) / 4), (unsigned)gy), dim3(256), 0, s, first, last,
                        (int)n_seqs, table, width, refs, pages);

@@ -17,7 +17,9 @@
 // Measured: a prompt of 4096 tokens (8 kv heads, groups of 4, d = 128) 162 us
 // among others, 850 TFLOP/s of its causal products (a large library product
 // reaches 1190), 200 us by itself; 2048 tokens after 30000 1.04 ms, 1000
-// TFLOP/s.  A step of a workgroup takes 2 us.  Bound by the vector units, busy
+// TFLOP/s.  Over a prefix of 16384 keys that 64 requests share (one token each)
+// 32 us: eight steps of 1.8 us in each of 256 workgroups, 12 us of start and
+// end, 4 us for the sums of 32 parts.  A step of a workgroup takes 2 us.  Bound by the vector units, busy
 // 52% of the time with softmax and unpacking, and the matrix cores, busy 38%,
 // which run beside each other only in part.
 #pragma once
@@ -300,7 +302,8 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
     for (int n = 0; n < steps_here; ++n) {
       const int base = step_base<M>(keys, st0 + n);
       const uint32_t ok = (uint32_t)oks & 15u;
-      const bool active = any_seen<M>(a, base, p0, p1);
+      const bool active = base <= p1 && (M > SINKS || a.window <= 0 || base + STEP - 1 > p0 - a.window ||
+                                         (M == SINKS && base < a.sinks));
       // S^T; each group's operands are read while the group before is multiplied
       // (the scheduling barriers keep that order)
       float4_t sc[C][4];
@@ -327,7 +330,7 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
         const uint8_t* vbuf = lds + (2 + vb) * T::HALF;
         half8_t vf[2][4];
         read_v(vbuf, 0, vf[0]);
-        if (masked<M>(a, base, p0, p1) || ok != 15u) {
+        if (base + STEP - 1 > p0 || (M <= SINKS && a.window > 0 && base <= p1 - a.window) || ok != 15u) {
 #pragma unroll
           for (int c = 0; c < C; ++c)
 #pragma unroll
@@ -335,7 +338,8 @@ __global__ __launch_bounds__(64 * PW, 2) void attn_prompt_kernel(AttnArgs a) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 const int k = base + 16 * i + 4 * g + j;
-                const bool see = ((ok >> i) & 1u) && sees<M>(a, k, p[c]);
+                const bool see = ((ok >> i) & 1u) && k <= p[c] &&
+                                 (M > SINKS || a.window <= 0 || k > p[c] - a.window || (M == SINKS && k < a.sinks));
                 sc[c][i][j] = see ? sc[c][i][j] : NEG_INF;
               }
         }

@@ -400,9 +400,9 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
 /* ---- attention over the cache: a window and a few first tokens ----
  * kq_kv_attention where a row at position p sees, beside the window's keys
  * (p - window < j <= p), the first `sinks` keys of its request: j <= p and
- * (j > p - window or j < sinks).  Nothing between the two is read, so that its
- * pages may have been given back (kq_kv_free) and their table entries hold
- * anything.  window 0, or window or sinks from 2^30 on: all keys.
+ * (j > p - window or j < sinks).  Nothing between the two enters, whatever its
+ * pages hold, so that they may have been given back (kq_kv_free) and their
+ * table entries name anything.  window 0, or window or sinks from 2^30 on: all keys.
  * Arguments, workspace (kq_kv_attention_workspace), bounds and precision as
  * there. */
 int kq_kv_attention_sinks(int codec, const void* q, int q_dtype, int64_t tokens, int64_t q_heads, int64_t kv_heads,

@@ -183,11 +183,84 @@ def test_prefix_prompts(kq, hq, kv, d, page, q_dtype):
 
 @pytest.mark.parametrize("d, hq, kv, page", [(64, 4, 2, 16), (128, 8, 2, 128), (96, 3, 3, 64), (256, 4, 2, 32)])
 @pytest.mark.parametrize("new, own, keys", [([1] * 3, [5, 1, 1], 4000), ([1] * 70, [3] * 70, 1000), ([2, 90, 1], [2100, 90, 1500], 256),
-                                            ([1, 1], [3000, 1700], 128), ([300], [300], 640), ([6] * 9, [6] * 9, 144)])
+                                            ([1, 1], [3000, 1700], 128), ([300], [300], 640), ([6] * 9, [6] * 9, 144),
+                                            ([200, 3], [2500, 1800], 256)])
 def test_prefix_split_keys(kq, new, own, keys, d, hq, kv, page):
     # prefixes cut into parts, own keys shared by workgroups, and both
     c = _shared(sum(own) + d, new, own, max(1, keys // page), hq, kv, d, page)
     _check_prefix(kq, c, "split", "f32", max_new=max(new), max_kv=int(c["lens"].max()))
+
+
+def _check_prefix_on_gpu(kq, c, what, out, scale=None, **kw):
+    """_check_prefix with the reference as float64 products of a request at a time on the GPU, for prefixes so long that
+    prompt tiles take them."""
+    import torch
+
+    page, d, pages = c["page"], c["d"], c["kc"].shape[0]
+    q, prefix = c["q"].double(), c["prefix"]
+    tokens, hq, _ = q.shape
+    kv = c["kc"].shape[1]
+    sc = d ** -0.5 if scale is None else float(np.float32(scale))
+    ref, absv = torch.full_like(q, np.nan), torch.zeros_like(q)
+    mag, count = (torch.zeros((tokens, hq), dtype=torch.float64, device="cuda") for _ in range(2))
+
+    def rows(ids):
+        there = np.repeat((ids >= 0) & (ids < pages), page)
+        slots = np.repeat(np.where((ids >= 0) & (ids < pages), ids, 0), page) * page + np.tile(np.arange(page), len(ids))
+        k, v = (torch.from_numpy(kvcache.load(x, page, d, slots)).cuda() for x in (c["kc"], c["vc"]))
+        there = torch.from_numpy(there).cuda()
+        return [torch.where(there[:, None, None], x, 0.0).transpose(0, 1).contiguous() for x in (k, v)] + [there]
+
+    shared = rows(prefix)
+    for s, length in enumerate(c["lens"]):
+        a, b = int(c["cu"][s]), int(c["cu"][s + 1])
+        at = len(prefix) if length - (b - a) >= len(prefix) * page else 0
+        k, v, there = rows(c["table"][s, at:])
+        if at:
+            k, v, there = (torch.cat((x, y), -1 if x.dim() == 1 else 1) for x, y in zip(shared, (k, v, there)))
+        x = q[a:b].unflatten(1, (kv, hq // kv)).permute(1, 2, 0, 3).flatten(1, 2)  # [kv, group * n, d]
+        p = torch.arange(length - (b - a), length, device="cuda").repeat(hq // kv)
+        see = (torch.arange(k.shape[1], device="cuda") <= p[:, None]) & there
+        w = torch.where(see, x @ k.transpose(1, 2).contiguous() * sc, -torch.inf)
+        top = w.amax(-1, keepdim=True)
+        w = torch.exp(w - torch.where(top == -torch.inf, 0.0, top))
+        w = w / w.sum(-1, keepdim=True).clamp(min=1e-300)
+        back = lambda y: y.unflatten(1, (hq // kv, b - a)).permute(2, 0, 1, *range(3, y.dim() + 1)).flatten(1, 2)
+        ref[a:b], absv[a:b] = back(w @ v), back(w @ v.abs())
+        mag[a:b] = back(torch.where(see, x.abs() @ k.abs().transpose(1, 2).contiguous() * abs(sc), 0.0).amax(-1))
+        count[a:b] = back(see.sum(-1).expand(kv, -1).double())
+    got = _f64(_prefix(kq, c, out, scale=scale, **kw))
+    ref, absv, mag, count = (x.cpu().numpy() for x in (ref, absv, mag, count))
+    none = np.isnan(ref)
+    assert (got[none] == 77).all()
+    ref[none] = got[none]
+    vmax = np.nanmax(np.abs(kvcache.load(c["vc"], page, d, np.arange(pages * page))))
+    assert not got[(count == 0) & ~none.any(-1)].any()
+    _close(got, ref, _bound(ref, absv, mag, count, vmax, d, out), what)
+
+
+@pytest.mark.parametrize("d, hq, kv, page, keys, new, q_dtype", [
+    (128, 32, 8, 64, 16384, [1] * 40, "f16"), (256, 16, 4, 128, 8192, [2] * 30, "bf16"), (64, 7, 1, 16, 4816, [700, 1, 3], "bf16"),
+    (96, 6, 3, 32, 10016, [1, 250, 49], "f16"), (32, 8, 4, 64, 23040, [1] * 256, "f16"), (160, 8, 4, 64, 4800, [1] * 256, "bf16"),
+    (192, 8, 4, 16, 4016, [1] * 256, "f16"), (224, 8, 4, 64, 4160, [3] * 90, "f16"), (128, 8, 8, 256, 16384, [1] * 90, "bf16")])
+def test_prefix_of_many_rows(kq, d, hq, kv, page, keys, new, q_dtype):
+    # as much work over the prefix as prompt tiles take: rows that fill tiles in part, in full and several
+    rng = np.random.default_rng(d + len(new))
+    own = np.maximum(rng.integers(1, 60, len(new)), new)
+    own[-1] += 400
+    apart = (1,) if len(new) > 2 else ()
+    c = _shared(d, new, list(own), keys // page, hq, kv, d, page, q_dtype, apart=apart, extra_tokens=2)
+    bounds = dict(max_new=max(new), max_kv=int(c["lens"].max()))
+    _check_prefix_on_gpu(kq, c, "float32", "f32", **bounds)
+    _check_prefix_on_gpu(kq, c, "mean", q_dtype, scale=0.0, **bounds)
+    c["prefix"][[0, 7, -1]] = [-1, 1 << 30, c["kc"].shape[0]]
+    _check_prefix_on_gpu(kq, c, "pages that are none", q_dtype, **bounds)
+
+
+def test_both_references_agree(kq):
+    c = _shared(3, [1, 5, 2, 9], [4, 5, 80, 3], 5, 4, 2, 64, 16, apart=(3,), extra_tokens=1)
+    _check_prefix(kq, c, "oracle", "f32", max_new=9, max_kv=160)
+    _check_prefix_on_gpu(kq, c, "on the GPU", "f32", max_new=9, max_kv=160)
 
 
 def test_prefix_uniform_weights_count_every_key_once(kq):
@@ -490,3 +563,61 @@ def test_graph_replays_match_eager(kq):
         for n in b:
             assert torch.equal(b[n], got[n]), (i, n)
         torch.zeros(1000, device="cuda").sum().item()
+
+
+def test_both_python_paths_refuse_the_same(kq, monkeypatch):
+    import torch
+
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    kc, vc = (torch.zeros((6, 2, kq.kq_kv_page_bytes("q4_0", 16, 64)), dtype=torch.uint8, device="cuda") for _ in range(2))
+    q, k = (torch.zeros((3, h, 64), dtype=torch.float16, device="cuda") for h in (4, 2))
+    a = dict(q=q, k=k, cu=i32(3), lens=i32(2), freq=torch.zeros(32, device="cuda"), qo=torch.zeros_like(q), ko=torch.zeros_like(k),
+             layout="half", m=1.0, parents=i32(2), children=i32(2), take=i32(2), page=16, table=i32(4, 2), refs=i32(9), free=i32(4),
+             head=i32(1), src=i32(2), dst=i32(2), ho=i32(1), first=i32(4), last=i32(4), to=i32(4, 2), ro=i32(9), fo=i32(4),
+             remap=i32(9), csrc=i32(4), cdst=i32(4), kc=kc, vc=vc, t2=i32(2, 3), prefix=i32(1), out=torch.zeros_like(q), window=8,
+             sinks=2, max_new=2, max_kv=48, ws=torch.empty(1 << 20, dtype=torch.uint8, device="cuda"), codec="q4_0")
+    ops = {"rope": lambda x: kq.kq_rope(x["q"], x["k"], x["cu"], x["lens"], x["freq"], x["qo"], x["ko"], x["layout"], x["m"]),
+           "fork": lambda x: kq.kq_kv_fork(x["parents"], x["children"], x["take"], x["page"], x["table"], x["refs"], x["free"],
+                                           x["head"], x["src"], x["dst"], x["ho"]),
+           "free": lambda x: kq.kq_kv_free(x["first"], x["last"], x["table"], x["refs"], x["free"], x["head"], x["ho"]),
+           "compact": lambda x: kq.kq_kv_compact(x["free"], x["head"], x["table"], x["refs"], x["to"], x["ro"], x["fo"], x["remap"],
+                                                 x["csrc"], x["cdst"], x["ho"]),
+           "copy": lambda x: kq.kq_kv_copy_pages(x["src"], x["dst"], x["kc"], x["vc"]),
+           "sinks": lambda x: kq.kq_kv_attention_sinks(x["codec"], x["q"], x["cu"], x["lens"], x["t2"], x["kc"], x["vc"], x["page"],
+                                                       x["out"], x["window"], x["sinks"], max_new=x["max_new"],
+                                                       max_kv=x["max_kv"], workspace=x["ws"]),
+           "prefix": lambda x: kq.kq_kv_attention_prefix(x["codec"], x["q"], x["cu"], x["lens"], x["t2"], x["prefix"], x["kc"],
+                                                         x["vc"], x["page"], x["out"], max_new=x["max_new"],
+                                                         max_kv=x["max_kv"], workspace=x["ws"])}
+    bad = [("rope", dict(q=q.float())), ("rope", dict(q=q[:2])), ("rope", dict(qo=q[:, :2])), ("rope", dict(ko=k.float())),
+           ("rope", dict(q=None)), ("rope", dict(q=None, k=None, qo=None, ko=None)), ("rope", dict(freq=a["freq"].double())),
+           ("rope", dict(freq=a["freq"][:31])), ("rope", dict(freq=a["freq"][::2])), ("rope", dict(cu=i32(2))),
+           ("rope", dict(lens=a["lens"].long())), ("rope", dict(layout=7)), ("rope", dict(m=float("nan"))), ("rope", dict(qo=q[1:])),
+           ("rope", dict(q=q.transpose(0, 1))), ("rope", dict(cu=a["cu"].cpu())), ("rope", dict(q=q.cpu())), ("rope", dict(ko=a["qo"])),
+           ("fork", dict(children=i32(3))), ("fork", dict(take=a["take"].float())), ("fork", dict(table=i32(8))),
+           ("fork", dict(page=24)), ("fork", dict(ho=a["head"])), ("fork", dict(dst=i32(1))), ("fork", dict(refs=a["refs"][::2])),
+           ("fork", dict(src=a["dst"])), ("fork", dict(free=a["free"].cpu())),
+           ("free", dict(last=i32(3))), ("free", dict(table=i32(3, 2))), ("free", dict(refs=a["refs"].long())),
+           ("free", dict(ho=i32(2))), ("free", dict(free=a["refs"])), ("free", dict(table=i32(2, 4).T)),
+           ("compact", dict(to=i32(4, 3))), ("compact", dict(remap=i32(8))), ("compact", dict(csrc=i32(3), cdst=i32(3))),
+           ("compact", dict(cdst=i32(3))), ("compact", dict(fo=a["remap"][:4])), ("compact", dict(head=i32(2))),
+           ("copy", dict(dst=i32(3))), ("copy", dict(kc=kc.int())), ("copy", dict(vc=vc[1:])), ("copy", dict(vc=kc)),
+           ("copy", dict(kc=kc.cpu())), ("copy", dict(src=a["src"].long())), ("copy", dict(kc=kc.transpose(0, 1))),
+           ("sinks", dict(sinks=-1)), ("sinks", dict(window=-1)), ("sinks", dict(codec="q8_0")), ("sinks", dict(t2=i32(3, 2))),
+           ("sinks", dict(out=q)), ("sinks", dict(max_kv=0)), ("sinks", dict(kc=kc.cpu())),
+           ("prefix", dict(prefix=a["prefix"].long())), ("prefix", dict(prefix=i32(0))), ("prefix", dict(prefix=i32(4)[::2])),
+           ("prefix", dict(prefix=a["prefix"].cpu())), ("prefix", dict(ws=a["ws"][:64])), ("prefix", dict(ws=a["ws"].cpu())),
+           ("prefix", dict(max_new=0)), ("prefix", dict(page=32)), ("prefix", dict(out=a["out"].int()))]
+    want = {n: x.clone() for n, x in a.items() if torch.is_tensor(x)}
+    for i, (name, kw) in enumerate(bad):
+        errors = []
+        for module in (kq._kqcall, None):
+            with monkeypatch.context() as mp:
+                mp.setattr(kq, "_kqcall", module)
+                with pytest.raises((ValueError, TypeError, kq.KQError)) as e:
+                    ops[name](dict(a, **kw))
+                errors.append((e.type, str(e.value)))
+        assert errors[0] == errors[1], (i, name, list(kw), errors)
+    torch.cuda.synchronize()
+    for n, x in want.items():
+        assert torch.equal(a[n], x), n
