@@ -191,6 +191,35 @@ def test_prefix_split_keys(kq, new, own, keys, d, hq, kv, page):
     _check_prefix(kq, c, "split", "f32", max_new=max(new), max_kv=int(c["lens"].max()))
 
 
+def _long(seed, new, own, n_prefix, hq, kv, d, page, q_dtype, apart):
+    """_shared with rows of any codes, written page by page."""
+    import torch
+
+    rng = np.random.default_rng(seed)
+    held = -(-own // page)
+    pages = n_prefix + int(held.sum()) + 2
+    caches = []
+    for _ in range(2):
+        codes = rng.integers(0, 256, (pages, kv, page * d // 2), dtype=np.uint8)
+        scales = rng.uniform(0.1, 0.3, (pages, kv, page * d // 32)).astype(np.float16)
+        caches.append(np.concatenate((codes, scales.view(np.uint8)), -1))
+    ids = rng.permutation(pages)
+    table, at = np.full((len(new), n_prefix + int(held.max())), -5), n_prefix
+    for s, m in enumerate(held):
+        b = 0 if s in apart else n_prefix
+        table[s, b:b + m] = ids[at:at + m]
+        at += m
+        if own[s] % page:  # behind the last key: NaN
+            for c in caches:
+                tail = c[ids[at - 1], :, page * d // 2:].reshape(kv, page, -1)
+                tail[:, own[s] % page:] = 255
+                c[ids[at - 1], :, page * d // 2:] = tail.reshape(kv, -1)
+    lens = own + np.where(np.isin(np.arange(len(new)), apart), 0, n_prefix * page)
+    q = torch.from_numpy(rng.standard_normal((sum(new) + 2, hq, d)).astype(np.float32)).to(device="cuda", dtype=_tdt(q_dtype))
+    return dict(q=q, cu=np.concatenate(([0], np.cumsum(new))), lens=lens, table=table, kc=caches[0], vc=caches[1], page=page, d=d,
+                prefix=ids[:n_prefix].copy())
+
+
 def _check_prefix_on_gpu(kq, c, what, out, scale=None, **kw):
     """_check_prefix with the reference as float64 products of a request at a time on the GPU, for prefixes so long that
     prompt tiles take them."""
@@ -218,6 +247,7 @@ def _check_prefix_on_gpu(kq, c, what, out, scale=None, **kw):
         k, v, there = rows(c["table"][s, at:])
         if at:
             k, v, there = (torch.cat((x, y), -1 if x.dim() == 1 else 1) for x, y in zip(shared, (k, v, there)))
+        k, v, there = k[:, :length], v[:, :length], there[:length]
         x = q[a:b].unflatten(1, (kv, hq // kv)).permute(1, 2, 0, 3).flatten(1, 2)  # [kv, group * n, d]
         p = torch.arange(length - (b - a), length, device="cuda").repeat(hq // kv)
         see = (torch.arange(k.shape[1], device="cuda") <= p[:, None]) & there
@@ -249,7 +279,7 @@ def test_prefix_of_many_rows(kq, d, hq, kv, page, keys, new, q_dtype):
     own = np.maximum(rng.integers(1, 60, len(new)), new)
     own[-1] += 400
     apart = (1,) if len(new) > 2 else ()
-    c = _shared(d, new, list(own), keys // page, hq, kv, d, page, q_dtype, apart=apart, extra_tokens=2)
+    c = _long(d, new, own, keys // page, hq, kv, d, page, q_dtype, apart)
     bounds = dict(max_new=max(new), max_kv=int(c["lens"].max()))
     _check_prefix_on_gpu(kq, c, "float32", "f32", **bounds)
     _check_prefix_on_gpu(kq, c, "mean", q_dtype, scale=0.0, **bounds)
