@@ -5,11 +5,12 @@ namespace kq {
 
 // Prompt tiles unpack a step once for 256 rows, 16-row tiles start and end
 // sooner and split finer: 16-row tiles up to as much work as they do in some
-// 35 us.  (8 kv heads of 128, groups of 4, one own key: 16 requests behind 16384 keys 27.6 us
-// against 32.0 with prompt tiles, 24 36.2 against 34.1; 32 behind 4096 21.3
-// against 24.0; 128 heads of 64 in all behind 16384 52.7 against 48.7, 96 43.7 against 44.2.)  As many
-// parts as there are CUs (prompt tiles) or workgroups at once, of 2 or 4 steps
-// at least (128 rows behind 1024 keys: prompt tiles 19.6 us with 2, 22.4 with 4).
+// 35 us.  (8 kv heads of 128, groups of 4, one own key: 16 requests behind
+// 16384 keys 27.6 us against 32.0 with prompt tiles, 24 36.2 against 34.1; 32
+// behind 4096 21.3 against 24.0; 16 heads of 64, no groups: 128 requests behind
+// 16384 52.7 against 48.7, 96 43.7 against 44.2.)  As many parts as there are
+// CUs (prompt tiles) or workgroups at once, of 2 or 4 steps at least (128 rows
+// behind 1024 keys: prompt tiles 19.6 us with 2, 22.4 with 4).
 PrefixPlan prefix_plan(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t prefix_len) {
   PrefixPlan f;
   const int64_t rows = tokens * (q_heads / kv_heads), steps = (prefix_len + STEP - 1) / STEP;

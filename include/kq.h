@@ -398,11 +398,11 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
                     int out_dtype, void* workspace, int64_t workspace_bytes, void* stream);
 
 /* ---- attention over the cache: a window and a few first tokens ----
- * kq_kv_attention where a row at position p sees, beside the window's keys
- * (p - window < j <= p), the first `sinks` keys of its request: j <= p and
- * (j > p - window or j < sinks).  Nothing between the two enters, whatever its
- * pages hold, so that they may have been given back (kq_kv_free) and their
- * table entries name anything.  window 0, or window or sinks from 2^30 on: all keys.
+ * kq_kv_attention where a row at position p sees, beside the window's keys (p
+ * - window < j <= p), the first `sinks` keys of its request: j <= p and (j > p
+ * - window or j < sinks).  Nothing between the two enters, whatever its pages
+ * hold, so that they may have been given back (kq_kv_free) and their table
+ * entries name anything.  window 0, or window or sinks from 2^30 on: all keys.
  * Arguments, workspace (kq_kv_attention_workspace), bounds and precision as
  * there. */
 int kq_kv_attention_sinks(int codec, const void* q, int q_dtype, int64_t tokens, int64_t q_heads, int64_t kv_heads,
@@ -415,16 +415,16 @@ int kq_kv_attention_sinks(int codec, const void* q, int q_dtype, int64_t tokens,
  * kq_kv_attention for requests whose first prefix_len = n_prefix * page keys
  * are the same pages, prefix[0 .. n_prefix) (int32, device): these are read
  * and unpacked once for the rows of all requests.  seq_lens and the columns of
- * the table count the prefix in; key j of a request is read from
- * prefix[j / page] below prefix_len, from table[s][j / page] from there on (the
- * table's columns of the prefix are not read).  A request whose new tokens do not all stand
- * behind the prefix (seq_lens[s] - n < prefix_len; an idle one among them) has no
- * part in it: all its keys come from its row of the table.  prefix_len is at
- * least 1 page and below 2^30 keys; keys whose prefix entry is not a page of
- * the cache are left out.
- * max_kv bounds a request's length, prefix included.  The workspace always
- * holds the rows' sums over the prefix: kq_kv_attention_prefix_workspace gives
- * its bytes.  Other arguments, bounds and precision as in kq_kv_attention. */
+ * the table count the prefix in; key j of a request is read from prefix[j /
+ * page] below prefix_len, from table[s][j / page] from there on (the table's
+ * columns of the prefix are not read).  A request whose new tokens do not all
+ * stand behind the prefix (seq_lens[s] - n < prefix_len; an idle one among
+ * them) has no part in it: all its keys come from its row of the table.
+ * prefix_len is at least 1 page and below 2^30 keys; keys whose prefix entry
+ * is not a page of the cache are left out. max_kv bounds a request's length,
+ * prefix included.  The workspace always holds the rows' sums over the prefix:
+ * kq_kv_attention_prefix_workspace gives its bytes.  Other arguments, bounds
+ * and precision as in kq_kv_attention. */
 int kq_kv_attention_prefix_workspace(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d,
                                      int64_t prefix_len, int64_t max_new, int64_t max_kv, int64_t* bytes);
 int kq_kv_attention_prefix(int codec, const void* q, int q_dtype, int64_t tokens, int64_t q_heads, int64_t kv_heads,
@@ -436,58 +436,65 @@ int kq_kv_attention_prefix(int codec, const void* q, int q_dtype, int64_t tokens
 
 /* ---- pages of the cache shared, given back and moved ----
  * Bookkeeping on the GPU beside kq_block_tables, with its table (int32
- * [n_seqs][width]) and free list (int32 [n_free], the free pages from free_head
- * on), and refs, int32 [pages]: the holders of a page (table entries, or
- * what else the caller counts) beyond the first.  Pages that kq_block_tables
- * hands out have refs 0, so it needs no counts.  The table and the pages are
- * the same for all layers, the caches are not: kq_kv_copy_pages is called for
- * each layer's.  At most 65536 requests or forks.  Arrays are 4-byte aligned;
- * outputs must not overlap inputs or each other but where that is said
- * (KQ_ERR_ARG).
+ * [n_seqs][width]) and free list (int32 [n_free], the free pages from
+ * free_head on), and refs, int32 [pages]: the holders of a page (table
+ * entries, or what else the caller counts) beyond the first.  Pages that
+ * kq_block_tables hands out have refs 0, so it needs no counts.  The table and
+ * the pages are the same for all layers, the caches are not: kq_kv_copy_pages
+ * is called for each layer's.  At most 65536 requests or forks.  Arrays are
+ * 4-byte aligned; outputs must not overlap inputs or each other but where that
+ * is said (KQ_ERR_ARG).
  *
  * kq_kv_fork: request children[i] (a row of the table) starts with the first
- * lens[i] tokens of request parents[i], for i < n.  Whole pages are shared: the
- * parent's entries go to the child's row and refs counts them.  Where the length ends inside a page, that
- * page is to be copied: the child gets the next free page in its place, and
- * copy_src[i], copy_dst[i] are the two ids, for kq_kv_copy_pages; both are -1 where there
- * is nothing to copy.  Other entries of the child's row stay as they were.
- * Parent's entries that are no pages are taken over and not counted.
+ * lens[i] tokens of request parents[i], for i < n.  Whole pages are shared:
+ * the parent's entries go to the child's row and refs counts them.  Where the
+ * length ends inside a page, that page is to be copied: the child gets the
+ * next free page in its place, and copy_src[i], copy_dst[i] are the two ids,
+ * for kq_kv_copy_pages; both are -1 where there is nothing to copy.  Other
+ * entries of the child's row stay as they were. Parent's entries that are no
+ * pages are taken over and not counted.
  *   free_head_out  int32 [1]: free_head plus the pages taken
  *   status  nullable uint32 [1]: bit0 = a fork refused because the free pages
  *           ran out (later ones that need any are refused too), bit1 = one of more than
  *           `width` pages, bit2 = a parent or child that is no row of the table, or
  *           the same, bit3 = a negative length.
- * Refused forks change nothing.  Children must differ from each other and
- * from all parents of the call, and their rows hold no pages (they are not given back).
+ * Tokens are stored into pages of one holder only: the copied page is the
+ * child's, the parent goes on in its own, and kq_block_tables grows both by
+ * fresh ones; a request cut back into a shared page is first forked to another
+ * row at that length.
+ * Refused forks change nothing.  Children must differ from each other and from
+ * all parents of the call, and their rows hold no pages (they are not given
+ * back).
  *
- * kq_kv_free: the entries first[s] <= j < last[s] (int32, cut to 0 .. width) of
- * every row are given back: all of a request that ends, the columns that a
+ * kq_kv_free: the entries first[s] <= j < last[s] (int32, cut to 0 .. width)
+ * of every row are given back: all of a request that ends, the columns that a
  * window has passed, or those behind a length cut short.  Each takes one
  * holder off its page; pages left without one go back to the free list,
  * free_pages[free_head - count .. free_head) in the order of their ids, and
- * free_head_out is free_head - count.  Entries that are no pages are skipped.  The table
- * stays as it is: its caller says which entries count.  A list with less room
- * than that takes the last of them, and free_head_out is 0.
+ * free_head_out is free_head - count.  Entries that are no pages are skipped.
+ * The table stays as it is: its caller says which entries count.  A list with
+ * less room than that takes the last of them, and free_head_out is 0.
  *   status  nullable uint32 [1]: bit0 = a page given back more often than it
  *           was held (freed once), bit1 = no room in the list.
  *
  * kq_kv_compact: with `held` pages of the cache not in the free list, the held
  * pages with ids >= held move to the free ids below, both in ascending order,
- * so that the pages from `held` on are free.  Written: copy_src, copy_dst int32
- * [n_copy], the moves for kq_kv_copy_pages, -1 behind the last (n_copy at least
- * min(n_free, pages / 2), else KQ_ERR_CAPACITY); remap int32 [pages], every
- * page's new id, -1 for free ones; table_out (int32 [n_entries]) and refs_out
- * by the new ids, table entries that are free or no pages as -1;
- * free_out [n_free], ids held .. pages - 1 from free_head_out on and what stood in front before it; free_head_out =
- * n_free - (pages - held), which is free_head unless status bit0 = the list
- * named an id twice or one that is no page.  table_out, refs_out, free_out
- * and free_head_out may be table, refs, free_pages and free_head themselves.
- * At most 2^20 pages (KQ_ERR_ARG); a free_head outside 0 .. n_free means no free pages.
+ * so that the pages from `held` on are free.  Written: copy_src, copy_dst
+ * int32 [n_copy], the moves for kq_kv_copy_pages, -1 behind the last (n_copy
+ * at least min(n_free, pages / 2), else KQ_ERR_CAPACITY); remap int32 [pages],
+ * every page's new id, -1 for free ones; table_out (int32 [n_entries]) and
+ * refs_out by the new ids, table entries that are free or no pages as -1;
+ * free_out [n_free], ids held .. pages - 1 from free_head_out on and what
+ * stood in front before it; free_head_out = n_free - (pages - held), which is
+ * free_head unless status bit0 = the list named an id twice or one that is no
+ * page.  table_out, refs_out, free_out and free_head_out may be table, refs,
+ * free_pages and free_head themselves. At most 2^20 pages (KQ_ERR_ARG); a
+ * free_head outside 0 .. n_free means no free pages.
  *
  * kq_kv_copy_pages: page src[i] to page dst[i] of both caches, for i < n;
  * `bytes` is that of a page with all its heads (kv_heads * page_bytes, a
- * multiple of 16).  Pairs with an id outside 0 .. pages - 1 are skipped.  Pages
- * written must differ from each other and from all pages read. */
+ * multiple of 16).  Pairs with an id outside 0 .. pages - 1 are skipped.
+ * Pages written must differ from each other and from all pages read. */
 int kq_kv_fork(const int32_t* parents, const int32_t* children, const int32_t* lens, int64_t n, int64_t page,
                int32_t* table, int64_t n_seqs, int64_t width, int32_t* refs, int64_t pages, const int32_t* free_pages,
                int64_t n_free, const int32_t* free_head, int32_t* copy_src, int32_t* copy_dst, int32_t* free_head_out,
@@ -513,21 +520,20 @@ int kq_kv_copy_pages(const int32_t* src, const int32_t* dst, int64_t n, void* k_
  * other values are carried over.  Angles are float64 until they are within an
  * eighth of a turn, sines, cosines and products float32; a result is rounded
  * once.  Rows of no request, or with p < 0 (of refused requests), are left
- * unwritten.
- * q_out, k_out: rows q_out_stride and k_out_stride apart, either the input
- * itself with its stride or overlapping no input (rows of one stride may lie
- * side by side).  q_heads or kv_heads 0: no such rows.
- * rot is a multiple of 8 in 8..d, d a multiple of 32 in 32..256
- * (KQ_ERR_SHAPE); rows 16-byte aligned, strides multiples of 8; inv_freq float32
- * [rot / 2].  tokens * (q_heads + kv_heads) * d is below 2^34.
+ * unwritten. q_out, k_out: rows q_out_stride and k_out_stride apart, either
+ * the input itself with its stride or overlapping no input (rows of one stride
+ * may lie side by side).  q_heads or kv_heads 0: no such rows. rot is a
+ * multiple of 8 in 8..d, d a multiple of 32 in 32..256 (KQ_ERR_SHAPE); rows
+ * 16-byte aligned, strides multiples of 8; inv_freq float32 [rot / 2].  tokens
+ * * (q_heads + kv_heads) * d is below 2^34.
  *
  * kq_rope_freqs fills inv_freq [rot / 2] and mscale, on the host (HOST
  * pointers, no stream): base^(-2 i / rot), divided by factors[i] (float32,
- * positive, nullable: the rope_freqs tensor of a GGUF file) and
- * stretched by `factor` >= 1 as `scaling` says.  KQ_ROPE_YARN keeps the
- * frequencies that make more than `fast` turns over `original` positions,
- * divides those below `slow` turns, ramps between them, and sets mscale to
- * 0.1 ln(factor) + 1 (1 for the others). */
+ * positive, nullable: the rope_freqs tensor of a GGUF file) and stretched by
+ * `factor` >= 1 as `scaling` says.  KQ_ROPE_YARN keeps the frequencies that
+ * make more than `fast` turns over `original` positions, divides those below
+ * `slow` turns, ramps between them, and sets mscale to 0.1 ln(factor) + 1 (1
+ * for the others). */
 int kq_rope(const void* q, int64_t q_heads, int64_t q_stride, const void* k, int64_t kv_heads, int64_t k_stride,
             int dtype, int64_t tokens, int64_t d, int64_t rot, int layout, const int32_t* cu_new,
             const int32_t* seq_lens, int64_t n_seqs, const float* inv_freq, float mscale, void* q_out,
