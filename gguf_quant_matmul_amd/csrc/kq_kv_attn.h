@@ -113,10 +113,12 @@ template <int M>
 __device__ __forceinline__ bool masked(const AttnArgs& a, int base, int p0, int p1) {
   return base + STEP - 1 > p0 || (M <= SINKS && a.window > 0 && base <= p1 - a.window);
 }
-// Whether no row from position p0 on sees key k, one between sinks and window:
-// its page may be another request's or hold anything, NaN included.
+// Whether no row from position p0 on sees key k, one before the window, or
+// between sinks and window: a step of 64 keys holds such, and their pages may be
+// another request's or hold anything, NaN included.
 template <int M>
 __device__ __forceinline__ bool hidden(const AttnArgs& a, int k, int p0) {
+  if constexpr (M == PLAIN) return a.window > 0 && k <= p0 - a.window;
   if constexpr (M != SINKS) return false;
   const int n = p0 - a.window - a.sinks + 1;  // of them
   return (uint32_t)(k - a.sinks) < (uint32_t)(n > 0 ? n : 0);

@@ -373,8 +373,10 @@ int kq_kv_load(int codec, const void* k_cache, const void* v_cache, int64_t page
  * 2^-32 of the row's largest where that is more.  So it is for every out_dtype.
  * Device data is bounded, not trusted: cu_new entries are clamped to 0 ..
  * tokens, a length to 0 .. width * page, and keys whose table entry is not a
- * page of the cache are left out.  The cache is expected to hold finite
- * values, as kq_kv_store writes.
+ * page of the cache are left out.  Rows that are seen are expected to hold
+ * finite values, as kq_kv_store writes; rows before a request's windows enter
+ * nowhere, whatever their pages hold, so that these may have been given back
+ * (kq_kv_free) and their table entries name anything.
  * max_new and max_kv are the host's bounds on new tokens and length of a
  * request (at least 1): they choose the split of the work and the size of
  * the workspace; a request beyond them is still computed whole.
