@@ -440,8 +440,8 @@ int kq_kv_attention_prefix(int codec, const void* q, int q_dtype, int64_t tokens
  * Bookkeeping on the GPU beside kq_block_tables, with its table (int32
  * [n_seqs][width]) and free list (int32 [n_free], the free pages from
  * free_head on), and refs, int32 [pages]: the holders of a page (table
- * entries, or what else the caller counts) beyond the first.  Pages that
- * kq_block_tables hands out have refs 0, so it needs no counts.  The table and
+ * entries, or what else the caller counts) beyond the first, below 2^27.  Pages
+ * that kq_block_tables hands out have refs 0, so it needs no counts.  The table and
  * the pages are the same for all layers, the caches are not: kq_kv_copy_pages
  * is called for each layer's.  At most 65536 requests or forks.  Arrays are
  * 4-byte aligned; outputs must not overlap inputs or each other but where that
@@ -477,7 +477,11 @@ int kq_kv_attention_prefix(int codec, const void* q, int q_dtype, int64_t tokens
  * The table stays as it is: its caller says which entries count.  A list with
  * less room than that takes the last of them, and free_head_out is 0.
  *   status  nullable uint32 [1]: bit0 = a page given back more often than it
- *           was held (freed once), bit1 = no room in the list.
+ *           was held (freed once), or one that the list holds already (it stays
+ *           there once), bit1 = no room in the list.
+ * Counts do not tell whose a page is: entries that were given back must not be
+ * given back again (nor forked, nor stored into) once their pages may have been
+ * handed out anew.  A window's columns are left out by first[s], or set to -1.
  *
  * kq_kv_compact: with `held` pages of the cache not in the free list, the held
  * pages with ids >= held move to the free ids below, both in ascending order,

@@ -201,7 +201,11 @@ def free(first, last, table, refs, free_pages, head):
         for j in range(max(a, 0), min(b, len(row))):
             if 0 <= int(row[j]) < len(refs):
                 refs[int(row[j])] -= 1
-    status = int(min(refs, default=0) < -1)
+    listed = {int(f) for f in free_pages[head:]} if 0 <= head <= len(free_pages) else set()
+    twice = [p for p, r in enumerate(refs) if r < 0 and p in listed]  # stays listed once
+    status = int(bool(twice) or min(refs, default=0) < -1)
+    for p in twice:
+        refs[p] = 0
     dead = [p for p, r in enumerate(refs) if r < 0]
     for i, p in enumerate(dead):
         refs[p] = 0

@@ -30,6 +30,15 @@ def test_free_by_hand():
     assert (refs, free, head, status) == ([0] * 4, [7, 7], 0, 3)
 
 
+def test_free_of_listed_pages_by_hand():
+    # page 2 stands in the list: given back once more it stays there once, and that is told
+    refs, free, head, status = kvcache.free([0], [2], [[2, 3]], [0] * 5, [0, 4, 2], 1)
+    assert (refs, free, head, status) == ([0] * 5, [3, 4, 2], 0, 1)
+    # in front of the head it does not count
+    refs, free, head, status = kvcache.free([0], [2], [[2, 3]], [0] * 5, [2, 4, 1], 2)
+    assert (refs, free, head, status) == ([0] * 5, [2, 3, 1], 0, 0)
+
+
 def test_compact_by_hand():
     # held: 0, 2, 5, 6 of 7 pages; 5 and 6 go to 1 and 3
     got = kvcache.compact([0, 4, 1, 3], 1, [6, 5, -1, 2, 4, 0], [1, 0, 2, 0, 0, 3, 4], 4)
