@@ -741,7 +741,9 @@ int attention(const char* op, const AttnCall& c) {
           : kq::attn_plan(c.tokens, c.n_seqs, c.q_heads, c.kv_heads, c.d, c.max_new, c.max_kv, window);
   kq::PrefixPlan flat = {0, 0, 0, 0};
   if (c.prefix) flat = kq::prefix_plan(c.tokens, c.q_heads, c.kv_heads, c.d, prefix_len);
-  const int64_t need = flat.bytes + plan.bytes;
+  // (a prefix: the bytes of all smaller calls, what this one takes among them)
+  const int64_t need =
+      c.prefix ? kq::prefix_need(c.tokens, c.q_heads, c.kv_heads, c.d, prefix_len, c.max_new, c.max_kv) : plan.bytes;
   if (need > 0) {
     if (!c.workspace || c.workspace_bytes < need)
       return fail(KQ_ERR_CAPACITY, op, "workspace of %lld bytes is below the %lld these sizes need",
@@ -828,8 +830,7 @@ int kq_kv_attention_prefix_workspace(int64_t tokens, int64_t n_seqs, int64_t q_h
   if (!bytes) return fail(KQ_ERR_ARG, op, "null output");
   *bytes = tokens == 0 || n_seqs == 0
                ? 0
-               : kq::prefix_plan(tokens, q_heads, kv_heads, d, prefix_len).bytes +
-                     tail_plan(tokens, n_seqs, q_heads, kv_heads, d, max_new, max_kv, prefix_len).bytes;
+               : kq::prefix_need(tokens, q_heads, kv_heads, d, prefix_len, max_new, max_kv);
   return KQ_OK;
 }
 

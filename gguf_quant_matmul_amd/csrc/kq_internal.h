@@ -445,6 +445,7 @@ AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_h
 AttnPlan sinks_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new,
                     int64_t max_kv, int64_t window, int64_t sinks);
 void plan_tiles(AttnPlan& p, int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t seen);
+int64_t plan_most(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new, int64_t max_kv);
 int attn_prompt_rows(int64_t d);  // rows of a prompt tile
 // The prefix's part: one tile kernel over all rows of the batch, each tile's
 // steps cut into `splits`.
@@ -454,6 +455,9 @@ struct PrefixPlan {
   int64_t bytes;       // of prefix_sums
 };
 PrefixPlan prefix_plan(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t prefix_len);
+// Bytes of workspace of a call, and of every call of no larger sizes.
+int64_t prefix_need(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t prefix_len, int64_t max_new,
+                    int64_t max_kv);
 hipError_t launch_kv_attention(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
 hipError_t launch_kv_attention_sinks(const AttnArgs& a, const AttnPlan& p, hipStream_t s);
 hipError_t launch_kv_attention_prefix(const AttnArgs& a, const AttnPlan& p, const PrefixPlan& f, hipStream_t s);

@@ -163,6 +163,20 @@ void plan_tiles(AttnPlan& p, int64_t tokens, int64_t q_heads, int64_t kv_heads, 
   if (p.few_wgs == 0) p.more_waves = tiles <= (d > 128 ? 128 : 256) && seen > STEP * WAVES;
 }
 
+// What no plan passes whose tokens, requests, new tokens and lengths are at most
+// these: fewer 16-row tiles may be shared where more are not, and a prompt's
+// tiles likewise, so that a plan's own bytes go up and down.  (attn_plan and
+// plan_tiles: 16-row tiles are shared above 1024 keys, prompt tiles where that
+// saves 12 steps, which tiles of as few do not hold.)
+int64_t plan_most(int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t max_new, int64_t max_kv) {
+  const int64_t most = (max_new < tokens ? max_new : tokens) * (q_heads / kv_heads), at_once = d <= 64 ? 1024 : 512;
+  AttnPlan p;
+  p.few_wgs = max_kv > 1024 ? (int)((at_once + kv_heads - 1) / kv_heads) : 0;
+  p.many_wgs = most > 64 && kv_heads <= 64 && max_kv > 12 * STEP ? (int)(256 / kv_heads) : 0;
+  plan_workspace(p, tokens, q_heads, kv_heads, d);
+  return p.bytes;
+}
+
 template <bool PREFIX>
 static hipError_t launch_join(const AttnArgs& a, hipStream_t s) {
   const int64_t n_rows = (int64_t)a.tokens * a.hq, fit = 256 / (a.d / 4);

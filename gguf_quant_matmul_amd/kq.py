@@ -518,7 +518,7 @@ def kq_kv_attention_sinks(codec, q, cu_new, seq_lens, table, k_cache, v_cache, p
 
 def kq_kv_attention_prefix_workspace(tokens: int, n_seqs: int, q_heads: int, kv_heads: int, d: int, prefix_len: int,
                                      max_new: int, max_kv: int) -> int:
-    """Bytes of workspace that kq_kv_attention_prefix needs for these sizes; prefix_len in keys."""
+    """Bytes of workspace that kq_kv_attention_prefix needs for these sizes and smaller ones; prefix_len in keys."""
     out = c_i64()
     _check(_lib.kq_kv_attention_prefix_workspace(tokens, n_seqs, q_heads, kv_heads, d, prefix_len, max_new, max_kv,
                                                  ctypes.byref(out)))

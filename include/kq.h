@@ -383,10 +383,11 @@ int kq_kv_load(int codec, const void* k_cache, const void* v_cache, int64_t page
  * workspace (16-byte aligned) holds partial results where the keys of a row
  * are split over workgroups: kq_kv_attention_workspace gives its bytes (0:
  * none needed, workspace may be NULL; KQ_ERR_CAPACITY if it is too small) for
- * the same sizes, whatever the window.  Its contents mean nothing between
- * calls; calls that may run at the same time need one each.  Results are
- * deterministic for given sizes, bounds and lengths; how a row's keys are split,
- * and so the last bits of its result, goes by the whole batch's lengths.
+ * exactly these sizes, whatever the window; a smaller batch may need more.  Its
+ * contents mean nothing between calls; calls that may run at the same time need
+ * one each.  Results are deterministic for given sizes, bounds and lengths; how a
+ * row's keys are split, and so the last bits of its result, goes by the whole
+ * batch's lengths.
  * q_heads and kv_heads are at most 4096, tokens * q_heads below 2^25, n_seqs
  * at most 65536 and n_seqs * kv_heads below 2^22, width * page below 2^30.
  * out and workspace must not overlap what is read, or each other
@@ -425,8 +426,9 @@ int kq_kv_attention_sinks(int codec, const void* q, int q_dtype, int64_t tokens,
  * prefix_len is at least 1 page and below 2^30 keys; keys whose prefix entry
  * is not a page of the cache are left out. max_kv bounds a request's length,
  * prefix included.  The workspace always holds the rows' sums over the prefix:
- * kq_kv_attention_prefix_workspace gives its bytes.  Other arguments, bounds
- * and precision as in kq_kv_attention. */
+ * kq_kv_attention_prefix_workspace gives its bytes, enough for every call whose
+ * tokens, n_seqs, prefix_len, max_new and max_kv are no larger.  Other
+ * arguments, bounds and precision as in kq_kv_attention. */
 int kq_kv_attention_prefix_workspace(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_heads, int64_t d,
                                      int64_t prefix_len, int64_t max_new, int64_t max_kv, int64_t* bytes);
 int kq_kv_attention_prefix(int codec, const void* q, int q_dtype, int64_t tokens, int64_t q_heads, int64_t kv_heads,
