@@ -593,7 +593,8 @@ def _attention(op, fn, codec, q, cu_new, seq_lens, table, prefix, k_cache, v_cac
 def kq_kv_fork(parents, children, lens, page: int, table, refs, free_pages, free_head, copy_src, copy_dst, free_head_out,
                status=None, stream=None) -> None:
     """Rows children int32 [n] of table int32 [n_seqs, width] start with the first lens int32 [n] tokens of rows parents
-    int32 [n].  refs int32 [pages]; copy_src, copy_dst int32 [n] are for kq_kv_copy_pages; free list as in kq_block_tables."""
+    int32 [n].  refs int32 [pages]; copy_src, copy_dst int32 [n] are for kq_kv_copy_pages; free list as in kq_block_tables.
+    Columns of a parent that were given back are set to -1 before."""
     if _kqcall is not None and stream is None and parents.is_cuda:
         dev = torch._C._cuda_getDevice()
         st = _kqcall.kv_fork(parents, children, lens, page, table, refs, free_pages, free_head, copy_src, copy_dst,

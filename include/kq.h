@@ -455,8 +455,11 @@ int kq_kv_attention_prefix(int codec, const void* q, int q_dtype, int64_t tokens
  * length ends inside a page, that page is to be copied: the child gets the
  * next free page in its place, and copy_src[i], copy_dst[i] are the two ids,
  * for kq_kv_copy_pages; both are -1 where there is nothing to copy.  Other
- * entries of the child's row stay as they were. Parent's entries that are no
- * pages are taken over and not counted.
+ * entries of the child's row stay as they were.  Parent's entries that are no
+ * pages are taken over and not counted: a parent's columns that were given back
+ * (kq_kv_free leaves the table as it is) are set to -1 first, else the fork
+ * counts a holder of pages that are free or another request's by now, and they
+ * do not come back.
  *   free_head_out  int32 [1]: free_head plus the pages taken
  *   status  nullable uint32 [1]: bit0 = a fork refused because the free pages
  *           ran out (later ones that need any are refused too), bit1 = one of more than

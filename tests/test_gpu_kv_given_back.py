@@ -4,10 +4,11 @@ such pages."""
 import numpy as np
 import pytest
 
+from _gpu import dev, host
 from oracle import kvcache
-from test_gpu_kv import _case, _f64
-from test_gpu_kv_pages import _free
-from test_gpu_kv_sinks_prefix import _args, _hold, _sinks, dev
+from test_gpu_kv import _case, _f64, _i32
+from test_gpu_kv_pages import _fork, _free
+from test_gpu_kv_sinks_prefix import _args, _hold, _sinks
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +89,56 @@ def test_listed_pages_given_back(kq, n, width, pages):
     # a list that names pages more than once
     free[held:held + pages // 8] = free[-1 - pages // 8:-1]
     _free(kq, np.zeros(n, int), np.full(n, width), table, np.zeros(pages, int), free, held, "listed twice")
+
+
+# ---------------------------------------------------------------------------
+# forks of requests whose window gave pages back
+# ---------------------------------------------------------------------------
+
+def test_forks_of_a_request_whose_middle_was_given_back(kq):
+    # request 0 keeps its sinks' column and its window's; the columns between are given back, set to -1, and request 1
+    # takes their pages; a fork of request 0 counts the held columns alone, and every page comes back in the end
+    page, width, pages, new = 16, 8, 14, 100
+    table = np.full((3, width), -1)
+    table[0, :7] = [9, 4, 11, 2, 6, 0, 13]
+    refs, free, head = np.zeros(pages, int), np.array([-1] * 7 + [1, 3, 5, 7, 8, 10, 12]), 7
+    t, r, f, h = _i32(table), _i32(refs), _i32(free), _i32([head])
+    i32 = lambda *x: _i32(list(x))
+
+    def state(what, status, want):
+        got = [host(x).tolist() for x in (t, r, f[int(host(h)[0]):])]
+        for g, w in zip(got, want):
+            assert g == w, what
+        assert host(status).tolist() == [0], what
+
+    h, st = kq.kv_free(i32(1, 0, 0), i32(4, 0, 0), t, r, f, h)
+    t[0, 1:4] = -1
+    state("window", st, ([[9, -1, -1, -1, 6, 0, 13, -1], [-1] * 8, [-1] * 8], [0] * pages, [2, 4, 11, 1, 3, 5, 7, 8, 10, 12]))
+    _, _, _, h, st = kq.block_tables(i32(0, 0, 0), i32(0, 40, 0), f, h, page, t, 40)
+    state("handed out anew", st, ([[9, -1, -1, -1, 6, 0, 13, -1], [2, 4, 11] + [-1] * 5, [-1] * 8], [0] * pages,
+                                  [1, 3, 5, 7, 8, 10, 12]))
+    src, dst, h, st = kq.kv_fork(i32(0), i32(2), i32(new), page, t, r, f, h)
+    assert (host(src).tolist(), host(dst).tolist()) == ([13], [1])
+    count = [0] * pages
+    for p in (9, 6, 0):
+        count[p] = 1
+    state("fork", st, ([[9, -1, -1, -1, 6, 0, 13, -1], [2, 4, 11] + [-1] * 5, [9, -1, -1, -1, 6, 0, 1, -1]], count,
+                       [3, 5, 7, 8, 10, 12]))
+    h, st = kq.kv_free(i32(0, 0, 0), i32(0, 0, width), t, r, f, h)  # the fork ends, then all others
+    state("fork ends", st, (host(t).tolist(), [0] * pages, [1, 3, 5, 7, 8, 10, 12]))
+    t[2] = -1
+    h, st = kq.kv_free(i32(0, 0, 0), i32(width, width, width), t, r, f, h)
+    assert host(st).tolist() == [0] and host(h).tolist() == [0] and not host(r).any()
+    assert sorted(host(f).tolist()) == list(range(pages))
+
+
+def test_an_entry_that_was_not_blanked_gives_its_page_a_holder(kq):
+    # what the header warns of: the fork cannot tell an entry whose page was given back
+    table = [[5, 3, 8, 1], [-1] * 4]
+    refs, free, head, status = kvcache.free([1, 0], [3, 0], table, [0] * 10, [0, 0, 7, 9], 2)
+    assert (free[head:], status) == ([3, 8, 7, 9], 0)
+    _fork(kq, [0], [1], [64], 16, table, refs, free, head, "stale")
+    assert kvcache.fork([0], [1], [64], 16, table, refs, free, head)[1][3] == 1
+    table[0][1:3] = [-1, -1]
+    _fork(kq, [0], [1], [64], 16, table, refs, free, head, "blanked")
+    assert kvcache.fork([0], [1], [64], 16, table, refs, free, head)[1][3] == 0
