@@ -997,7 +997,8 @@ int kq_rope_freqs(int64_t rot, double base, int scaling, double factor, int64_t 
   const int64_t pairs = rot / 2;
   if (factors)
     for (int64_t i = 0; i < pairs; ++i)
-      if (!(factors[i] > 0.f && factors[i] <= 1e30f)) return fail(KQ_ERR_ARG, op, "factors[%lld]=%g", (long long)i, factors[i]);
+      if (!(factors[i] >= 1e-30f && factors[i] <= 1e30f))
+        return fail(KQ_ERR_ARG, op, "factors[%lld]=%g out of 1e-30..1e30", (long long)i, factors[i]);
   // NTK: the lowest frequency is divided by `factor`, the highest stays
   if (scaling == KQ_ROPE_NTK) base *= std::pow(factor, (double)rot / (double)(rot - 2));
   double lo = 0., hi = 1.;

@@ -539,8 +539,8 @@ int kq_kv_copy_pages(const int32_t* src, const int32_t* dst, int64_t n, void* k_
  * * (q_heads + kv_heads) * d is below 2^34.
  *
  * kq_rope_freqs fills inv_freq [rot / 2] and mscale, on the host (HOST
- * pointers, no stream): base^(-2 i / rot), divided by factors[i] (float32,
- * positive, nullable: the rope_freqs tensor of a GGUF file) and stretched by
+ * pointers, no stream): base^(-2 i / rot), divided by factors[i] (float32, 1e-30
+ * to 1e30, nullable: the rope_freqs tensor of a GGUF file) and stretched by
  * `factor` >= 1 as `scaling` says.  KQ_ROPE_YARN keeps the frequencies that
  * make more than `fast` turns over `original` positions, divides those below
  * `slow` turns, ramps between them, and sets mscale to 0.1 ln(factor) + 1 (1
