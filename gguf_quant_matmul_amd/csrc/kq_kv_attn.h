@@ -106,7 +106,9 @@ __device__ __forceinline__ int steps_of(const Keys& k) {
 template <int M>
 __device__ __forceinline__ bool sees(const AttnArgs& a, int k, int p) {
   if constexpr (M == SINKS) return k <= p && (k > p - a.window || k < a.sinks);
-  if constexpr (M == PLAIN) return k <= p && (a.window <= 0 || k > p - a.window);
+  // (one comparison: a window above 0, else 2^31, which p - k >= 0 does not reach; two of them 16.7 us against
+  // 15.9 for 19 requests of 16 heads of 64 under a window)
+  if constexpr (M == PLAIN) return (uint32_t)(p - k) < (a.window > 0 ? (uint32_t)a.window : 0x80000000u);
   return k <= p;
 }
 template <int M>
