@@ -151,8 +151,8 @@ AttnPlan attn_plan(int64_t tokens, int64_t n_seqs, int64_t q_heads, int64_t kv_h
 // 16 at least, 128 at most.  (8 kv heads of 128, groups of 4, a window of 2000:
 // 32 requests 22 us against 32, 64 39 against 51; 8 requests, 1000: 13.4
 // against 16.2; 4000: 31 against 21.5.)  Eight waves to each where every one
-// has a CU, four where they share (64 requests, a window of 2000: 39 us
-// against 44).
+// has a CU, four where they share (64 requests, a window of 2000 and 4 sinks: 37
+// us against 40).
 void plan_tiles(AttnPlan& p, int64_t tokens, int64_t q_heads, int64_t kv_heads, int64_t d, int64_t seen) {
   const int64_t steps = (seen + STEP - 1) / STEP, tiles = p.few_tiles * kv_heads;
   const int64_t most = tiles / 2 < 16 ? 16 : tiles / 2 > 128 ? 128 : tiles / 2;

@@ -64,6 +64,10 @@ constexpr int region_bytes() {
 
 // SHARE: the workgroup takes an even share of all requests' steps, or (a.few_wgs =
 // 0) one tile; else one tile, with the registers that the shares need free.
+// (Three waves a SIMD are asked for also where a tail's LDS leaves two, at d = 128:
+// the registers are then given out otherwise, 64 requests behind 16384 keys 50.8
+// us against 53.4 with two, 100 to 300 behind 2048 47.6, 73.6, 97.8 against 46.7,
+// 72.4, 96.1.)
 template <int NB, int WAVES, int M, bool SHARE>
 __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : NB <= 4 && !SHARE && WAVES == 4 ? 3 : 2) void attn_split_kernel(AttnArgs a) {
   constexpr int D = 32 * NB;
@@ -157,7 +161,8 @@ __global__ __launch_bounds__(64 * WAVES, NB <= 2 ? 4 : NB <= 4 && !SHARE && WAVE
         for (int i = 0; i < NB; ++i) {
           const int piece = i * 64 + lane, key = piece / NB, b = piece % NB;
           const int64_t at = WHOLE ? gr.codes[4 * i / NB] : pick4(gr.codes, key >> 4);
-          // (read once: nontemporal, 8 to 13% faster on caches larger than the last-level cache)
+          // (nontemporal: 8 to 13% faster on caches larger than the last-level cache, where each row is read
+          // once; a prefix's rows are read by each of a head's tiles)
           w[i] = __builtin_nontemporal_load((const u32x4*)(cache + at + (uint32_t)((key & 15) * (D / 2) + 16 * b)));
         }
         const uint8_t* sp = cache + pick4(gr.scales, g) + (uint32_t)(col * (D / 16));

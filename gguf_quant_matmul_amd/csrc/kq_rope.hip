@@ -11,8 +11,9 @@
 // sums, 2^-23 off at most, so that far positions are as exact as near ones.
 // Rows are read and written once, 16 bytes a lane.
 //   Measured: 7.7k tokens of 40 heads of 128 in bfloat16, half of each turned,
-// 34.7 us, 4.6 TB/s of the 4.8 that a large copy reaches; 64 tokens 4.0 us,
-// bound by the launch and three dependent loads.
+// 34.7 us, 4.6 TB/s of the 4.8 that a large copy reaches; 64 tokens 4.0 us
+// by themselves (3.3 one behind the other in a graph), bound by the launch and three
+// dependent loads.
 #include "kq_internal.h"
 
 namespace kq {
@@ -178,7 +179,7 @@ hipError_t launch(const RopeArgs& a, hipStream_t s) {
   const uint32_t keep = a.copy_q || a.copy_k ? (uint32_t)((a.d - a.rot) / V) : 0u;
   const int64_t rounds = ((int64_t)(a.hq + a.hkv) * (turn + keep) + 63) / 64;  // of a token's wave
   // a token's rounds over up to 2048 / tokens waves: slices start earlier, but
-  // each computes the angles (40 heads of 128: 64 tokens 3.3 us in five slices,
+  // each computes the angles (40 heads of 128, in a graph: 64 tokens 3.3 us in five slices,
   // 5.2 in one; 512 4.7 in two, 4.9 in five, 6.0 in one; 4096 15.9 in one,
   // 17.8 in two)
   int64_t slices = 2048 / a.tokens;

@@ -406,8 +406,9 @@ int kq_kv_attention(int codec, const void* q, int q_dtype, int64_t tokens, int64
  * - window or j < sinks).  Nothing between the two enters, whatever its pages
  * hold, so that they may have been given back (kq_kv_free) and their table
  * entries name anything.  window 0, or window or sinks from 2^30 on: all keys.
- * Arguments, workspace (kq_kv_attention_workspace), bounds and precision as
- * there. */
+ * Keys are as they were stored: rotated ones keep the positions of their tokens
+ * in the request, which grow without end as the window moves.  Arguments,
+ * workspace (kq_kv_attention_workspace), bounds and precision as there. */
 int kq_kv_attention_sinks(int codec, const void* q, int q_dtype, int64_t tokens, int64_t q_heads, int64_t kv_heads,
                           int64_t d, int64_t q_stride, const int32_t* cu_new, const int32_t* seq_lens, int64_t n_seqs,
                           const int32_t* table, int64_t width, const void* k_cache, const void* v_cache, int64_t pages,
@@ -422,7 +423,9 @@ int kq_kv_attention_sinks(int codec, const void* q, int q_dtype, int64_t tokens,
  * page] below prefix_len, from table[s][j / page] from there on (the table's
  * columns of the prefix are not read).  A request whose new tokens do not all
  * stand behind the prefix (seq_lens[s] - n < prefix_len; an idle one among
- * them) has no part in it: all its keys come from its row of the table.
+ * them) has no part in it: all its keys come from its row of the table.  (The
+ * split goes by the keys behind the prefix, max_kv - prefix_len: a request with no
+ * part and many keys is right but slow, and is better called for by itself.)
  * prefix_len is at least 1 page and below 2^30 keys; keys whose prefix entry
  * is not a page of the cache are left out. max_kv bounds a request's length,
  * prefix included.  The workspace always holds the rows' sums over the prefix:
